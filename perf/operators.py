@@ -271,7 +271,7 @@ def _plan(st):
     at = table[b, (pos // P).clamp(0, M - 1)]
     slots = torch.where((t < total) & (pos // P < M) & (at >= 0), at * P + pos % P, -1)
     got = (n - off).clamp(min=0).minimum(need)
-    lost = (seq - ctx.maximum((old + got) * P)).clamp(min=0).sum()
+    lost = (seq - ctx.maximum((old.clamp(max=M) + got) * P)).clamp(min=0).sum()
     status = torch.stack((total, taken, wanted - taken, lost))
     return {"table": table, "seq": seq.int(), "cu": cu.int(), "slots": slots.int(), "pos": torch.where(t < total, pos, -1).int(),
             "left": (n - taken).int(), "status": status.int()}
