@@ -112,13 +112,7 @@ StreamWorkspace stream_workspace_layout(const fk_problem& p, int64_t chunk, char
     return w;
 }
 
-}  // namespace fk
-
-namespace {
-
-using namespace fk;
-
-thread_local char g_err[512] = "";
+static thread_local char g_err[512] = "";
 
 fk_status fail(fk_status st, const char* fmt, ...) {
     va_list ap;
@@ -131,6 +125,12 @@ fk_status fail(fk_status st, const char* fmt, ...) {
 fk_status hip_fail(hipError_t e, const char* what) {
     return fail(FK_EHIP, "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
 }
+
+}  // namespace fk
+
+namespace {
+
+using namespace fk;
 
 #define FK_TRY(call, what)                            \
     do {                                              \

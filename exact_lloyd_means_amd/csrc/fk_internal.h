@@ -20,6 +20,10 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 constexpr int kWave = 64;
 
+// Record the calling thread's error text (fk_last_error) and return the status.
+fk_status fail(fk_status st, const char* fmt, ...);
+fk_status hip_fail(hipError_t e, const char* what);
+
 // Element size in bytes of a problem dtype.
 inline int dtype_size(int dtype) { return dtype == FK_F32 ? 4 : 2; }
 

@@ -1,0 +1,786 @@
+// k_kv4_attn.inl -- attention over the 4-bit paged cache (fk_kv4_attention).
+//
+// One wave holds 16 NT query rows and walks blocks of 32 cached tokens:
+//
+//   S^T = K Q^T   v_mfma_f32_16x16x32_f16, A = 16 tokens x 32 dimensions of
+//                 codebook values, B = 32 dimensions x 16 query rows.  Lane
+//                 (16 g + n) gets rows 4 g + r of query n.  The token of row
+//                 m of tile u is 8 (m / 4) + 4 u + m % 4, so the two tiles
+//                 give a lane the eight consecutive tokens 8 g .. 8 g + 7.
+//   p, w          x = S * k scale, p = 2^(x qs - m), l += p, w = p * v scale,
+//                 all in fp32 in those lanes; w rounded to fp16 once.
+//   O^T += V^T w  A = 16 dimensions x 32 tokens, B = w: a lane's operand is
+//                 its own eight weights, so nothing crosses lanes.
+//
+// The rows of a (request, kv head) are numbered token * G + head of the
+// group: all query heads of a group and a few tokens share one pass.
+//
+// Codes become fp16 through a table in LDS of all 256 pairs of codebook
+// values, one 4-byte entry per byte of codes: k's at 256 byte, v's 128 bytes
+// on, each 32 times side by side so that the 32 lanes read at once lie in 32
+// banks whatever their codes.  The address (byte << 8 | 4 (lane % 32)) is one
+// v_perm of the codes.  (16-entry tables in registers cost 11 v_perm and
+// masks per 4 values; this costs 2 and 2 LDS reads.)  k's codes come in
+// operand order.  A lane's v codes are an 8 x 8 tile (token, dimension) of
+// nibbles that is transposed in registers, half an instruction a value.
+//
+// Running maximum: kept per query row and raised only when a score exceeds
+// it by 8 (p <= 256 in between), so that most blocks need no reduction over
+// lanes and no rescaling; l is summed over lanes at the end.  The v scales
+// are normalised by a power of two per wave (vg) that keeps w in fp16's
+// range; it follows the largest scale met.
+#pragma once
+
+#include "kv4_internal.h"
+
+namespace fk {
+namespace {
+
+constexpr int kAttnThreads = 256;
+constexpr int kAttnWaves = 4;
+constexpr int kTabBytes = 65536;
+constexpr int kMergeBytes = 16384;
+constexpr float kNoMax = -1e30f;   // running maximum before any key
+constexpr float kSlack = 8.f;      // how far a score may exceed it, log2
+
+typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
+
+struct Rows {       // the query rows of a tile within their request
+    int qlen, seq;  // of the request
+    int r0, n;      // first row, number of rows
+    int64_t tok0;   // first query token of the request
+};
+
+// Blocks [lo, hi) that some row of the tile sees.
+struct Span {
+    int lo, hi;
+};
+
+__device__ inline void request_lens(const AttnArgs& a, int64_t b, int64_t& tok0, int& qlen,
+                                    int& seq) {
+    int64_t c0 = a.cu[b], c1 = a.cu[b + 1];
+    c0 = c0 < 0 ? 0 : c0 > a.T ? a.T : c0;
+    c1 = c1 < c0 ? c0 : c1 > a.T ? a.T : c1;
+    tok0 = c0;
+    qlen = (int)(c1 - c0);
+    const int s = a.seq[b];
+    seq = s < 0 ? 0 : s;
+}
+
+// First and one past the last position that query token i sees.
+__device__ inline void bounds(const AttnArgs& a, int qlen, int seq, int64_t cap, int i, int& lo,
+                              int& hi) {
+    const int64_t pos = (int64_t)seq - qlen + i;
+    int64_t h = a.causal ? pos + 1 : seq, l = a.window > 0 ? pos - a.window + 1 : 0;
+    h = h > seq ? seq : h;
+    h = h > cap ? cap : h;
+    l = l < 0 ? 0 : l;
+    hi = h < 0 ? 0 : (int)h;
+    lo = l > hi ? hi : (int)l;
+}
+
+__device__ inline Span tile_span(const AttnArgs& a, int qlen, int seq, int r0, int n) {
+    if (n <= 0) return {0, 0};
+    const int64_t cap = a.max_pages * a.page_size;
+    int lo, hi, t0, t1;
+    bounds(a, qlen, seq, cap, r0 / a.G, lo, t0);
+    bounds(a, qlen, seq, cap, (r0 + n - 1) / a.G, t1, hi);
+    if (hi <= lo) return {0, 0};
+    return {lo / kKvBlock, (hi + kKvBlock - 1) / kKvBlock};
+}
+
+__device__ inline floatx4 mfma(half8 x, half8 y, floatx4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, c, 0, 0, 0);
+}
+
+typedef const __attribute__((address_space(3))) uint32_t* LdsWord;
+
+// Eight codes of a dword to eight fp16 codebook values.  lane4 = 4 (lane %
+// 32) selects the lane's copy of the table, V the codebook.
+template <bool V>
+__device__ inline half8 lookup(LdsWord tab, uint32_t codes, uint32_t lane4) {
+    uintx4 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // bytes of the address: lane4's byte 0, byte i of the codes, zeros
+        const uint32_t at = __builtin_amdgcn_perm(codes, lane4, 0x0c0c0000u | (4u + i) << 8);
+        y[i] = *(LdsWord)((const __attribute__((address_space(3))) char*)tab + at + (V ? 128 : 0));
+    }
+    return __builtin_bit_cast(half8, y);
+}
+
+// The pair table of one kv head: 256 entries of 64 dwords, k copies in 0-31,
+// v copies in 32-63.  Thread t writes 16-byte column t % 16 of the entries
+// whose low nibble is t / 16.
+__device__ inline void build_table(uint32_t* tab, const uint16_t* codebook, int H, int h, int tid) {
+    const int col = tid & 15, lo = tid >> 4;
+    const uint16_t* cb = codebook + ((col >> 3) * H + h) * 16;
+    const uint32_t low = cb[lo];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t v = low | (uint32_t)cb[i] << 16;
+        uintx4 y = {v, v, v, v};
+        *reinterpret_cast<uintx4*>(tab + (i * 16 + lo) * 64 + col * 4) = y;
+    }
+}
+
+// 8 rows (tokens) x 8 columns (dimensions) of nibbles, one row a dword, to 8
+// columns of 8 rows.
+__device__ inline void pair_columns(uint32_t even, uint32_t odd, uint32_t& c0, uint32_t& c1) {
+    constexpr uint32_t m = 0x0f0f0f0fu;
+    c0 = (even & m) | ((odd << 4) & ~m);
+    c1 = ((even >> 4) & m) | (odd & ~m);
+}
+__device__ inline void transpose8(const uint32_t (&x)[8], uint32_t (&y)[8]) {
+    uint32_t a[4], b[4];  // columns 0-3, 4-7 of rows j and j + 4
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        a[j] = __builtin_amdgcn_perm(x[j + 4], x[j], 0x05040100u);
+        b[j] = __builtin_amdgcn_perm(x[j + 4], x[j], 0x07060302u);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const uint32_t* s = c ? b : a;
+        const uint32_t lo0 = __builtin_amdgcn_perm(s[2], s[0], 0x06020400u);
+        const uint32_t lo1 = __builtin_amdgcn_perm(s[3], s[1], 0x06020400u);
+        const uint32_t hi0 = __builtin_amdgcn_perm(s[2], s[0], 0x07030501u);
+        const uint32_t hi1 = __builtin_amdgcn_perm(s[3], s[1], 0x07030501u);
+        pair_columns(lo0, lo1, y[4 * c], y[4 * c + 1]);
+        pair_columns(hi0, hi1, y[4 * c + 2], y[4 * c + 3]);
+    }
+}
+// 8 rows x 4 columns, two rows a dword.
+__device__ inline void transpose4(const uint32_t (&x)[4], uint32_t (&y)[4]) {
+    // bytes 0, 1 of a dword: columns 0-1, 2-3 of an even row; 2, 3: of the odd row
+    const uint32_t e0 = __builtin_amdgcn_perm(x[1], x[0], 0x05010400u);  // even rows 0, 2: c01 c01 c23 c23
+    const uint32_t e1 = __builtin_amdgcn_perm(x[3], x[2], 0x05010400u);
+    const uint32_t o0 = __builtin_amdgcn_perm(x[1], x[0], 0x07030602u);
+    const uint32_t o1 = __builtin_amdgcn_perm(x[3], x[2], 0x07030602u);
+    pair_columns(__builtin_amdgcn_perm(e1, e0, 0x05040100u),
+                 __builtin_amdgcn_perm(o1, o0, 0x05040100u), y[0], y[1]);
+    pair_columns(__builtin_amdgcn_perm(e1, e0, 0x07060302u),
+                 __builtin_amdgcn_perm(o1, o0, 0x07060302u), y[2], y[3]);
+}
+
+__device__ inline float max_groups(float x) {  // over the four lanes of a query row
+    x = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(x, __shfl_xor(x, 32));
+}
+
+// The codes and scales of one block, as one lane reads them.
+template <int D>
+struct Block {
+    uintx4 k[D / 64], v[D / 64], ks, vs;
+    bool there;
+};
+
+template <int D, int DT, int NT>
+struct Wave {
+    static constexpr int kDb = D / 16;  // dimension blocks of O
+    static constexpr int kKs = D / 32;  // contraction steps of S
+
+    half8 q[NT][kKs];
+    floatx4 o[NT][kDb];
+    float m[NT], l[NT], qs[NT];
+    int lo[NT], hi[NT];  // positions the lane's query row sees
+    float vg;
+    int inner_lo, inner_hi;  // positions every row of the wave sees
+
+    // Query rows r0 .. r0 + n - 1 of the request (n may be <= 0).
+    __device__ inline void load(const AttnArgs& a, const Rows& rw, int h, int lane) {
+        const int g = lane >> 4, c = lane & 15;
+        const int64_t cap = a.max_pages * a.page_size;
+        inner_lo = 0;
+        inner_hi = 0x7fffffff;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int r = rw.r0 + t * 16 + c;
+            const bool on = t * 16 + c < rw.n;
+            const int i = on ? r / a.G : 0, head = h * a.G + (on ? r - i * a.G : 0);
+            uint32_t x[D / 8];
+#pragma unroll
+            for (int w = 0; w < D / 8; ++w) x[w] = 0;
+            lo[t] = hi[t] = 0;
+            if (on) {
+                const uint16_t* p = a.q + (rw.tok0 + i) * a.q_token + head * a.q_head + g * (D / 4);
+                if (a.q_vec) {
+#pragma unroll
+                    for (int w = 0; w < D / 32; ++w) {
+                        const uintx4 y = reinterpret_cast<const uintx4*>(p)[w];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[4 * w + e] = y[e];
+                    }
+                } else {
+#pragma unroll
+                    for (int w = 0; w < D / 8; ++w) x[w] = p[2 * w] | (uint32_t)p[2 * w + 1] << 16;
+                }
+                bounds(a, rw.qlen, rw.seq, cap, i, lo[t], hi[t]);
+            }
+            // the row's largest magnitude, and the power of two below it
+            float big = 0.f;
+#pragma unroll
+            for (int w = 0; w < D / 8; ++w)
+                big = fmaxf(big, fmaxf(fabsf(kv_f32<DT>(x[w] & 0xffff)), fabsf(kv_f32<DT>(x[w] >> 16))));
+            big = max_groups(big);
+            int e = (int)(__builtin_bit_cast(uint32_t, big) >> 23 & 0xff);
+            e = big == 0.f || e == 255 ? 0 : (e < 1 ? 1 : e) - 127;
+            const float f = ldexpf(1.f, -e);
+            qs[t] = fmaxf(ldexpf(a.qk, e), 1.17549435e-38f);
+#pragma unroll
+            for (int s = 0; s < kKs; ++s)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t w = x[4 * s + j];
+                    q[t][s][2 * j] = (_Float16)(kv_f32<DT>(w & 0xffff) * f);
+                    q[t][s][2 * j + 1] = (_Float16)(kv_f32<DT>(w >> 16) * f);
+                }
+            m[t] = kNoMax;
+            l[t] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kDb; ++i) o[t][i] = floatx4{0, 0, 0, 0};
+        }
+        vg = 0x1p100f;
+        // bounds grow with the row, so the first and last rows tell
+        if (rw.n > 0) {
+            int x;
+            const int i0 = rw.r0 / a.G, i1 = (rw.r0 + rw.n - 1) / a.G;
+            bounds(a, rw.qlen, rw.seq, cap, i0, x, inner_hi);
+            int y;
+            bounds(a, rw.qlen, rw.seq, cap, i1, inner_lo, y);
+        }
+    }
+
+    // EDGE: some row of the wave does not see some token of the block.
+    template <bool EDGE>
+    __device__ inline void step(const Block<D>& blk, int at, LdsWord tab, uint32_t lane4, int g) {
+        // scores
+        floatx4 s[2][NT];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) s[u][t] = floatx4{0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < kKs; ++c)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int w = u * kKs + c;
+                const half8 x = lookup<false>(tab, blk.k[w >> 2][w & 3], lane4);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) s[u][t] = mfma(x, q[t][c], s[u][t]);
+            }
+        float ks[8], vs[8];
+        float big = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t kw = blk.ks[j >> 1], vw = blk.vs[j >> 1];
+            ks[j] = kv_f32<DT>(j & 1 ? kw >> 16 : kw & 0xffff);
+            vs[j] = kv_f32<DT>(j & 1 ? vw >> 16 : vw & 0xffff);
+        }
+        if constexpr (EDGE) {  // scales of rows that nothing wrote may be anything
+            const int p0 = at + 8 * g;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                bool seen = false;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) seen |= p0 + j >= lo[t] && p0 + j < hi[t];
+                if (!(seen && blk.there)) ks[j] = vs[j] = 0.f;
+            }
+        }
+        // v's scales below 2^6 after the common factor
+#pragma unroll
+        for (int j = 0; j < 8; ++j) big = fmaxf(big, vs[j]);
+        if (__any(big * vg > 64.f)) {
+            big = max_groups(big);
+            const int e = (int)(__builtin_bit_cast(uint32_t, big) >> 23 & 0xff) - 127;
+            const float f = ldexpf(1.f, -e);
+            // the new factor over the old; it only falls
+            const float r = f < vg ? f / vg : 1.f;
+            vg = f < vg ? f : vg;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < kDb; ++i) o[t][i] *= r;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) vs[j] *= vg;
+        half8 w[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = s[j >> 2][t][j & 3] * ks[j];
+            if constexpr (EDGE) {
+                const int p0 = at + 8 * g;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (!(blk.there && p0 + j >= lo[t] && p0 + j < hi[t])) x[j] = -INFINITY;
+            }
+            float top = x[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
+            if (__any(fmaf(top, qs[t], -m[t]) > kSlack)) {
+                const float nm = fmaxf(m[t], max_groups(top * qs[t]));
+                const float f = __builtin_amdgcn_exp2f(m[t] - nm);
+                m[t] = nm;
+                l[t] *= f;
+#pragma unroll
+                for (int i = 0; i < kDb; ++i) o[t][i] *= f;
+            }
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float p = __builtin_amdgcn_exp2f(fmaf(x[j], qs[t], -m[t]));
+                sum += p;
+                // a scale that another row of the lane sees may be NaN
+                w[t][j] = (_Float16)(EDGE && x[j] == -INFINITY ? 0.f : p * vs[j]);
+            }
+            l[t] += sum;
+        }
+        // values
+#pragma unroll
+        for (int half = 0; half < (D + 127) / 128; ++half) {
+            uint32_t col[D < 128 ? 4 : 8];
+            if constexpr (D == 64) {
+                uint32_t row[4] = {blk.v[0][0], blk.v[0][1], blk.v[0][2], blk.v[0][3]};
+                transpose4(row, col);
+            } else {
+                uint32_t row[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) row[j] = blk.v[2 * half + (j >> 2)][j & 3];
+                transpose8(row, col);
+            }
+#pragma unroll
+            for (int i = 0; i < (D < 128 ? 4 : 8); ++i) {
+                const half8 x = lookup<true>(tab, col[i], lane4);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) o[t][8 * half + i] = mfma(x, w[t], o[t][8 * half + i]);
+            }
+        }
+    }
+};
+
+// Where a wave's blocks lie.
+struct Walk {
+    const int32_t* table;  // the request's row
+    int h;
+};
+
+__device__ inline int block_page(const AttnArgs& a, const Walk& wk, int blk, int& in) {
+    const uint32_t pg = a.bpp == 1 ? (uint32_t)blk
+                                   : (uint32_t)(((uint64_t)(uint32_t)blk * a.bpp_magic) >> 32);
+    in = blk - (int)(pg * a.bpp);
+    return wk.table[pg];
+}
+
+template <int D>
+__device__ inline void load_block(const AttnArgs& a, const Walk& wk, int page, int in, int lane,
+                                  Block<D>& b) {
+    b.there = (int64_t)page >= 0 && (int64_t)page < a.pages;
+    const int64_t at = ((int64_t)(b.there ? page : 0) * a.Hkv + wk.h) * 2;
+    const uint8_t* k = a.codes + (at * a.bpp + in) * (16 * D) + lane * 16;
+    const uint8_t* v = k + (int64_t)a.bpp * (16 * D);
+    const uint16_t* s = a.scales + at * a.page_size + in * kKvBlock + 8 * (lane >> 4);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+        b.k[i] = *reinterpret_cast<const uintx4*>(k + 1024 * i);
+        b.v[i] = *reinterpret_cast<const uintx4*>(v + 1024 * i);
+    }
+    b.ks = *reinterpret_cast<const uintx4*>(s);
+    b.vs = *reinterpret_cast<const uintx4*>(s + a.page_size);
+}
+
+// Blocks first, first + stride, ... below end.  The next block's codes and
+// the page of the one after are loaded while a block is computed.
+template <int D, int DT, int NT>
+__device__ inline void walk(const AttnArgs& a, Wave<D, DT, NT>& wv, const Walk& wk, int first,
+                            int end, int stride, LdsWord tab, int lane) {
+    if (first >= end) return;
+    const uint32_t lane4 = 4 * (lane & 31);
+    const int g = lane >> 4, last = end - 1;
+    Block<D> cur, nxt;
+    int in, in2;
+    int page = block_page(a, wk, first, in);
+    load_block<D>(a, wk, page, in, lane, cur);
+    int b1 = first + stride < end ? first + stride : last;
+    page = block_page(a, wk, b1, in);
+    for (int b = first; b < end; b += stride) {
+        load_block<D>(a, wk, page, in, lane, nxt);
+        const int b2 = b + 2 * stride < end ? b + 2 * stride : last;
+        const int page2 = block_page(a, wk, b2, in2);
+        const int at = b * kKvBlock;
+        if (!cur.there || at < wv.inner_lo || at + kKvBlock > wv.inner_hi)
+            wv.template step<true>(cur, at, tab, lane4, g);
+        else
+            wv.template step<false>(cur, at, tab, lane4, g);
+        cur = nxt;
+        page = page2;
+        in = in2;
+    }
+}
+
+// Inclusive scan over the workgroup's 256 threads; scratch of 4 int64.
+__device__ inline int64_t group_scan(int64_t x, int64_t* scratch, int64_t& total, int tid) {
+    const int lane = tid & 63, wave = tid >> 6;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int64_t y = __shfl_up(x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 63) scratch[wave] = x;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) {
+        const int64_t y = scratch[w];
+        if (w < wave) x += y;
+        total += y;
+    }
+    __syncthreads();
+    return x;
+}
+
+template <int DT>
+__device__ inline void store_out(const AttnArgs& a, int64_t tok, int head, int D, int d,
+                                 floatx4 x) {
+    const uint32_t lo = kv_bits<DT>(x[0]) | kv_bits<DT>(x[1]) << 16;
+    const uint32_t hi = kv_bits<DT>(x[2]) | kv_bits<DT>(x[3]) << 16;
+    *reinterpret_cast<uint2*>(a.out + (tok * a.Hq + head) * D + d) = make_uint2(lo, hi);
+}
+
+// ---- rows form: every wave of a workgroup takes other query rows ------------
+
+// Grid (row tiles of all requests, kv heads).  A workgroup's tile is 4 x 16
+// NT rows of one request; tiles of a request run from its last rows, which
+// see the most keys, to its first.
+template <int D, int DT, int NT>
+__global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_attn_rows(AttnArgs a) {
+    extern __shared__ uint32_t tab[];
+    int64_t* scratch = reinterpret_cast<int64_t*>(tab);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int h = blockIdx.y;
+    constexpr int rows = 16 * NT * kAttnWaves;
+    // which request holds tile blockIdx.x
+    const int per = (a.B + kAttnThreads - 1) / kAttnThreads;
+    const int64_t b0 = (int64_t)tid * per;
+    int64_t mine = 0, total, tok0;
+    int qlen, seq;
+    for (int64_t b = b0; b < b0 + per && b < a.B; ++b) {
+        request_lens(a, b, tok0, qlen, seq);
+        mine += ((int64_t)qlen * a.G + rows - 1) / rows;
+    }
+    int64_t before = group_scan(mine, scratch, total, tid) - mine;
+    const int64_t want = blockIdx.x;
+    if (want >= total) return;
+    if (want >= before && want < before + mine) {
+        int64_t b = b0;
+        for (;; ++b) {
+            request_lens(a, b, tok0, qlen, seq);
+            const int64_t n = ((int64_t)qlen * a.G + rows - 1) / rows;
+            if (want < before + n) {
+                scratch[0] = b;
+                scratch[1] = n - 1 - (want - before);
+                break;
+            }
+            before += n;
+        }
+    }
+    __syncthreads();
+    const int64_t b = scratch[0];
+    const int tile = (int)scratch[1];
+    __syncthreads();
+    build_table(tab, a.codebook, a.Hkv, h, tid);
+    Rows rw;
+    request_lens(a, b, rw.tok0, rw.qlen, rw.seq);
+    rw.r0 = tile * rows + wave * 16 * NT;
+    const int64_t left = (int64_t)rw.qlen * a.G - rw.r0;
+    rw.n = left < 0 ? 0 : left > 16 * NT ? 16 * NT : (int)left;
+    Wave<D, DT, NT> wv;
+    wv.load(a, rw, h, lane);
+    __syncthreads();
+    const Span sp = tile_span(a, rw.qlen, rw.seq, rw.r0, rw.n);
+    const Walk wk{a.table + b * a.max_pages, h};
+    walk<D, DT, NT>(a, wv, wk, sp.lo, sp.hi, 1, (LdsWord)tab, lane);
+    const int g = lane >> 4, c = lane & 15;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        float l = wv.l[t];
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        if (t * 16 + c >= rw.n) continue;
+        const int r = rw.r0 + t * 16 + c, i = r / a.G, head = h * a.G + r - i * a.G;
+        const int64_t tok = rw.tok0 + i;
+        const float inv = l == 0.f ? 0.f : 1.f / (l * wv.vg);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k) {
+                floatx4 x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = wv.o[t][4 * k + j][e] * inv;
+                store_out<DT>(a, tok, head, D, (4 * g + e) * (D / 16) + 4 * k, x);
+            }
+        if (a.lse && g == 0)
+            a.lse[tok * a.Hq + head] = (wv.m[t] + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+    }
+}
+
+// ---- split form: every wave of a workgroup takes other keys -----------------
+
+// Visible blocks of row tile rt of request b.
+template <int NT>
+__device__ inline Span split_span(const AttnArgs& a, int64_t b, int rt, Rows& rw) {
+    request_lens(a, b, rw.tok0, rw.qlen, rw.seq);
+    rw.r0 = rt * 16 * NT;
+    const int64_t left = (int64_t)rw.qlen * a.G - rw.r0;
+    rw.n = left < 0 ? 0 : left > 16 * NT ? 16 * NT : (int)left;
+    return tile_span(a, rw.qlen, rw.seq, rw.r0, rw.n);
+}
+
+// Blocks a workgroup takes of `total`: an equal share of at least one a wave.
+__device__ inline int64_t split_share(int64_t total, int splits) {
+    const int64_t per = (total + splits - 1) / splits;
+    return per < kAttnWaves ? kAttnWaves : per;
+}
+
+// Grid (splits, row tiles x kv heads).  The blocks of a (row tile, head) over
+// all requests form one line that is cut into equal shares, whatever the
+// lengths; a workgroup walks its share request by request, its waves taking
+// every fourth block, and adds the waves up in LDS.  A request that lies
+// within one share is finished there; else its shares go to the workspace
+// and k_kv4_attn_join adds them in order.
+template <int D, int DT, int NT>
+__global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_attn_split(AttnArgs a) {
+    extern __shared__ uint32_t lds[];
+    uint32_t* tab = lds;
+    float* merge = reinterpret_cast<float*>(lds + kTabBytes / 4);
+    int64_t* scratch = reinterpret_cast<int64_t*>(merge);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y - h * a.row_tiles;
+    const int per = (a.B + kAttnThreads - 1) / kAttnThreads;
+    const int64_t b0 = (int64_t)tid * per;
+    Rows rw;
+    int64_t mine = 0, total;
+    for (int64_t b = b0; b < b0 + per && b < a.B; ++b) {
+        const Span sp = split_span<NT>(a, b, rt, rw);
+        mine += sp.hi - sp.lo;
+    }
+    int64_t before = group_scan(mine, scratch, total, tid) - mine;
+    if (blockIdx.x == 0 && h == 0) {  // what the join needs
+        int64_t at = before;
+        int64_t* prefix = a.prefix + (int64_t)rt * (a.B + 1);
+        for (int64_t b = b0; b < b0 + per && b < a.B; ++b) {
+            const Span sp = split_span<NT>(a, b, rt, rw);
+            prefix[b] = at;
+            at += sp.hi - sp.lo;
+        }
+        if (tid == 0) prefix[a.B] = total;
+    }
+    const int64_t share = split_share(total, a.splits);
+    const int64_t from = (int64_t)blockIdx.x * share;
+    const int64_t to = from + share < total ? from + share : total;
+    if (from >= to) return;
+    if (from >= before && from < before + mine) {
+        int64_t at = before;
+        for (int64_t b = b0;; ++b) {
+            const Span sp = split_span<NT>(a, b, rt, rw);
+            if (from < at + sp.hi - sp.lo) {
+                scratch[0] = b;
+                scratch[1] = from - at;
+                break;
+            }
+            at += sp.hi - sp.lo;
+        }
+    }
+    __syncthreads();
+    int64_t b = scratch[0];
+    int skip = (int)scratch[1];  // blocks of request b that lie before the share
+    __syncthreads();
+    build_table(tab, a.codebook, a.Hkv, h, tid);
+    __syncthreads();
+
+    const int g = lane >> 4, c = lane & 15;
+    for (int64_t at = from; at < to; ++b, skip = 0) {
+        const Span sp = split_span<NT>(a, b, rt, rw);
+        const int all = sp.hi - sp.lo;
+        if (all == 0) continue;
+        const int first = sp.lo + skip;
+        const int take = (int)(to - at < all - skip ? to - at : all - skip);
+        Wave<D, DT, NT> wv;
+        wv.load(a, rw, h, lane);
+        const Walk wk{a.table + b * a.max_pages, h};
+        walk<D, DT, NT>(a, wv, wk, first + wave, first + take, kAttnWaves, (LdsWord)tab, lane);
+        at += take;
+        const bool whole = take == all;
+        // partial results of this share: place 0 for a request that began
+        // before it or ends with it as its first, else 1
+        const int64_t part = ((int64_t)blockIdx.y * a.splits + blockIdx.x) * 2 +
+                             (at - take == from ? 0 : 1);
+        // maxima and sums of the waves
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float l = wv.l[t];
+            l += __shfl_xor(l, 16);
+            l += __shfl_xor(l, 32);
+            if (g == 0) {
+                merge[(wave * 16 * NT + t * 16 + c) * 2] = wv.m[t];
+                merge[(wave * 16 * NT + t * 16 + c) * 2 + 1] = l;
+            }
+        }
+        __syncthreads();
+        float top[NT], sum[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float mw[kAttnWaves], lw[kAttnWaves];
+            top[t] = kNoMax;
+#pragma unroll
+            for (int w = 0; w < kAttnWaves; ++w) {
+                mw[w] = merge[(w * 16 * NT + t * 16 + c) * 2];
+                lw[w] = merge[(w * 16 * NT + t * 16 + c) * 2 + 1];
+                top[t] = fmaxf(top[t], mw[w]);
+            }
+            sum[t] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kAttnWaves; ++w)
+                sum[t] += lw[w] * __builtin_amdgcn_exp2f(mw[w] - top[t]);
+            const float f = __builtin_amdgcn_exp2f(wv.m[t] - top[t]) / wv.vg;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) wv.o[t][i] *= f;
+        }
+        __syncthreads();
+        // sums of O over the waves, 16 accumulators a round: wave w adds
+        // piece w (4 consecutive dimensions a lane) of the four waves
+        constexpr int kRegs = 256 / D;  // accumulator elements e of a round
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e0 = 0; e0 < 4; e0 += kRegs) {
+                floatx4* buf = reinterpret_cast<floatx4*>(merge);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const int e = e0 + p / (D / 64), k = p % (D / 64);
+                    floatx4 x;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] = wv.o[t][4 * k + j][e];
+                    buf[(wave * 4 + p) * 64 + lane] = x;
+                }
+                __syncthreads();
+                floatx4 x = buf[wave * 64 + lane];
+#pragma unroll
+                for (int w = 1; w < kAttnWaves; ++w) x += buf[(w * 4 + wave) * 64 + lane];
+                const int e = e0 + wave / (D / 64), k = wave % (D / 64);
+                const int d = (4 * g + e) * (D / 16) + 4 * k;
+                if (t * 16 + c < rw.n) {
+                    if (whole) {
+                        const int r = rw.r0 + t * 16 + c, i = r / a.G, head = h * a.G + r - i * a.G;
+                        const float inv = sum[t] == 0.f ? 0.f : 1.f / sum[t];
+                        store_out<DT>(a, rw.tok0 + i, head, D, d, x * inv);
+                    } else {
+                        *reinterpret_cast<floatx4*>(a.part_o + (part * 16 * NT + t * 16 + c) * D + d) = x;
+                    }
+                }
+                __syncthreads();
+            }
+        if (wave == 0 && g == 0) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (t * 16 + c >= rw.n) continue;
+                if (whole) {
+                    const int r = rw.r0 + t * 16 + c, i = r / a.G, head = h * a.G + r - i * a.G;
+                    if (a.lse)
+                        a.lse[(rw.tok0 + i) * a.Hq + head] =
+                            (top[t] + __builtin_amdgcn_logf(sum[t])) * 0.6931471805599453f;
+                } else {
+                    float* ml = a.part_ml + (part * 16 * NT + t * 16 + c) * 2;
+                    ml[0] = top[t];
+                    ml[1] = sum[t];
+                }
+            }
+        }
+    }
+}
+
+// Adds the shares of requests that lie in several, in their order, and writes
+// zeros for rows that see nothing.  Grid (B, row tiles x kv heads); a thread
+// holds 4 consecutive dimensions of a row.
+template <int D, int DT, int NT>
+__global__ __launch_bounds__(kAttnThreads) void k_kv4_attn_join(AttnArgs a) {
+    const int tid = threadIdx.x;
+    const int64_t b = blockIdx.x;
+    const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y - h * a.row_tiles;
+    const int64_t* prefix = a.prefix + (int64_t)rt * (a.B + 1);
+    const int64_t lo = prefix[b], hi = prefix[b + 1], share = split_share(prefix[a.B], a.splits);
+    const int64_t w0 = lo / share, w1 = hi > lo ? (hi - 1) / share : w0;
+    if (hi > lo && w0 == w1) return;
+    Rows rw;
+    split_span<NT>(a, b, rt, rw);
+    for (int x = tid; x < rw.n * (D / 4); x += kAttnThreads) {
+        const int c = x / (D / 4), d = 4 * (x - c * (D / 4));
+        float top = kNoMax, sum = 0.f;
+        floatx4 o = {0, 0, 0, 0};
+        if (hi > lo)
+            for (int64_t w = w0; w <= w1; ++w) {
+                const int64_t part = (((int64_t)blockIdx.y * a.splits + w) * 2 +
+                                      (w == w0 && lo != w * share ? 1 : 0)) * 16 * NT + c;
+                const float m = a.part_ml[part * 2], l = a.part_ml[part * 2 + 1];
+                const floatx4 y = *reinterpret_cast<const floatx4*>(a.part_o + part * D + d);
+                const float nm = fmaxf(top, m);
+                const float f = __builtin_amdgcn_exp2f(top - nm), k = __builtin_amdgcn_exp2f(m - nm);
+                o = o * f + y * k;
+                sum = sum * f + l * k;
+                top = nm;
+            }
+        const int r = rw.r0 + c, i = r / a.G, head = h * a.G + r - i * a.G;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        store_out<DT>(a, rw.tok0 + i, head, D, d, o * inv);
+        if (a.lse && d == 0)
+            a.lse[(rw.tok0 + i) * a.Hq + head] =
+                (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+    }
+}
+
+// ---- launches ------------------------------------------------------------------
+
+template <int D, int DT, int NT>
+hipError_t attn_as(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+    static LdsAttr rows_rec, split_rec;
+    if (!p.split) {
+        auto kern = k_kv4_attn_rows<D, DT, NT>;
+        hipError_t e = ensure_lds(rows_rec, reinterpret_cast<const void*>(kern), kTabBytes);
+        if (e != hipSuccess) return e;
+        constexpr int rows = 16 * NT * kAttnWaves;
+        const int64_t tiles = (a.T * a.G + rows - 1) / rows + a.B;
+        kern<<<dim3((unsigned)tiles, (unsigned)a.Hkv), dim3(kAttnThreads), kTabBytes, s>>>(a);
+        return hipGetLastError();
+    }
+    auto kern = k_kv4_attn_split<D, DT, NT>;
+    hipError_t e =
+        ensure_lds(split_rec, reinterpret_cast<const void*>(kern), kTabBytes + kMergeBytes);
+    if (e != hipSuccess) return e;
+    const unsigned y = (unsigned)(a.Hkv * p.row_tiles);
+    kern<<<dim3((unsigned)p.splits, y), dim3(kAttnThreads), kTabBytes + kMergeBytes, s>>>(a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    k_kv4_attn_join<D, DT, NT><<<dim3((unsigned)a.B, y), dim3(kAttnThreads), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <int D, int DT>
+hipError_t attn_cols(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+    switch (p.col_blocks) {
+        case 1: return attn_as<D, DT, 1>(a, p, s);
+        case 2: return attn_as<D, DT, 2>(a, p, s);
+        default:
+            if constexpr (D <= 128) return attn_as<D, DT, 4>(a, p, s);
+            else return hipErrorInvalidValue;
+    }
+}
+
+template <int D>
+hipError_t attn_d(const AttnArgs& a, const AttnPlan& p, int dtype, hipStream_t s) {
+    return dtype == FK_BF16 ? attn_cols<D, FK_BF16>(a, p, s) : attn_cols<D, FK_F16>(a, p, s);
+}
+
+}  // namespace
+}  // namespace fk

@@ -1,0 +1,10 @@
+// k_kv4_attn_d64.hip -- cache attention for heads of 64 dimensions.
+#include "k_kv4_attn.inl"
+
+namespace fk {
+
+hipError_t launch_kv4_attn_d64(const AttnArgs& a, const AttnPlan& p, int dtype, hipStream_t s) {
+    return attn_d<64>(a, p, dtype, s);
+}
+
+}  // namespace fk
