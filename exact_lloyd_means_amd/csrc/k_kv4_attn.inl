@@ -93,18 +93,20 @@ __device__ inline floatx4 mfma(half8 x, half8 y, floatx4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, c, 0, 0, 0);
 }
 
+// The table starts the workgroup's LDS (the kernels have no static LDS), so an
+// entry's address needs no base.
 typedef const __attribute__((address_space(3))) uint32_t* LdsWord;
 
 // Eight codes of a dword to eight fp16 codebook values.  lane4 = 4 (lane %
 // 32) selects the lane's copy of the table, V the codebook.
 template <bool V>
-__device__ inline half8 lookup(LdsWord tab, uint32_t codes, uint32_t lane4) {
+__device__ inline half8 lookup(uint32_t codes, uint32_t lane4) {
     uintx4 y;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         // bytes of the address: lane4's byte 0, byte i of the codes, zeros
         const uint32_t at = __builtin_amdgcn_perm(codes, lane4, 0x0c0c0000u | (4u + i) << 8);
-        y[i] = *(LdsWord)((const __attribute__((address_space(3))) char*)tab + at + (V ? 128 : 0));
+        y[i] = *((LdsWord)at + (V ? 32 : 0));
     }
     return __builtin_bit_cast(half8, y);
 }
@@ -250,24 +252,34 @@ struct Wave {
         }
     }
 
-    // EDGE: some row of the wave does not see some token of the block.
-    template <bool EDGE>
-    __device__ inline void step(const Block<D>& blk, int at, LdsWord tab, uint32_t lane4, int g) {
+    // One block; `at` is its first position.
+    __device__ inline void step(const Block<D>& blk, int at, uint32_t lane4, int g) {
         // scores
         floatx4 s[2][NT];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int t = 0; t < NT; ++t) s[u][t] = floatx4{0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < kKs; ++c)
+        // the lookups of a step ahead of the products of the one before, and no
+        // further: unfenced, the compiler hoists them all and runs out of registers
+        half8 x[2][2];
+        auto keys = [&](int c) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int w = u * kKs + c;
-                const half8 x = lookup<false>(tab, blk.k[w >> 2][w & 3], lane4);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) s[u][t] = mfma(x, q[t][c], s[u][t]);
+                x[c & 1][u] = lookup<false>(blk.k[w >> 2][w & 3], lane4);
             }
+        };
+        keys(0);
+#pragma unroll
+        for (int c = 0; c < kKs; ++c) {
+            if (c + 1 < kKs) keys(c + 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) s[u][t] = mfma(x[c & 1][u], q[t][c], s[u][t]);
+        }
         float ks[8], vs[8];
         float big = 0.f;
 #pragma unroll
@@ -276,63 +288,89 @@ struct Wave {
             ks[j] = kv_f32<DT>(j & 1 ? kw >> 16 : kw & 0xffff);
             vs[j] = kv_f32<DT>(j & 1 ? vw >> 16 : vw & 0xffff);
         }
-        if constexpr (EDGE) {  // scales of rows that nothing wrote may be anything
+        half8 w[NT];
+        float top[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j >> 2][t][j & 3] *= ks[j];
+        if (!blk.there || at < inner_lo || at + kKvBlock > inner_hi) {
+            // Some row does not see some token.  Scales of tokens that none
+            // sees may be anything.
+            asm volatile("");  // keeps this a branch: as selects it would run for every block
             const int p0 = at + 8 * g;
+            bool nan = false;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                bool seen = false;
+                bool any = false;
 #pragma unroll
-                for (int t = 0; t < NT; ++t) seen |= p0 + j >= lo[t] && p0 + j < hi[t];
-                if (!(seen && blk.there)) ks[j] = vs[j] = 0.f;
+                for (int t = 0; t < NT; ++t) {
+                    const bool sees = blk.there && p0 + j >= lo[t] && p0 + j < hi[t];
+                    any |= sees;
+                    if (!sees) s[j >> 2][t][j & 3] = -INFINITY;
+                }
+                if (!any) vs[j] = 0.f;
+                nan |= vs[j] != vs[j];
+            }
+            if (__any(nan)) {
+                // 0 * NaN must not reach the rows that do not see it: the
+                // others' results become NaN here, the scale zero
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    float hit = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (vs[j] != vs[j] && p0 + j >= lo[t] && p0 + j < hi[t]) hit = 1.f;
+                    const float z = max_groups(hit) > 0.f ? __builtin_nanf("") : 0.f;
+#pragma unroll
+                    for (int i = 0; i < kDb; ++i) o[t][i] += z;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) vs[j] = vs[j] != vs[j] ? 0.f : vs[j];
             }
         }
-        // v's scales below 2^6 after the common factor
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            top[t] = s[0][t][0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) top[t] = fmaxf(top[t], s[j >> 2][t][j & 3]);
+        }
+        // raise the maxima by more than kSlack, keep v's scales below 2^6
+        // after their common factor
 #pragma unroll
         for (int j = 0; j < 8; ++j) big = fmaxf(big, vs[j]);
-        if (__any(big * vg > 64.f)) {
+        bool raise = big * vg > 64.f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) raise |= fmaf(top[t], qs[t], -m[t]) > kSlack;
+        if (__any(raise)) {
             big = max_groups(big);
             const int e = (int)(__builtin_bit_cast(uint32_t, big) >> 23 & 0xff) - 127;
-            const float f = ldexpf(1.f, -e);
-            // the new factor over the old; it only falls
-            const float r = f < vg ? f / vg : 1.f;
-            vg = f < vg ? f : vg;
+            float f = ldexpf(1.f, -e);
+            f = big * vg > 64.f && f < vg ? f : vg;  // it only falls
+            const float r = f / vg;
+            vg = f;
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t) {
+                const float nm = fmaxf(m[t], max_groups(top[t] * qs[t]));
+                float x = __builtin_amdgcn_exp2f(m[t] - nm);
+                m[t] = nm;
+                l[t] *= x;
+                x *= r;
 #pragma unroll
-                for (int i = 0; i < kDb; ++i) o[t][i] *= r;
+                for (int i = 0; i < kDb; ++i) o[t][i] *= x;
+            }
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) vs[j] *= vg;
-        half8 w[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            float x[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = s[j >> 2][t][j & 3] * ks[j];
-            if constexpr (EDGE) {
-                const int p0 = at + 8 * g;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (!(blk.there && p0 + j >= lo[t] && p0 + j < hi[t])) x[j] = -INFINITY;
-            }
-            float top = x[0];
-#pragma unroll
-            for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
-            if (__any(fmaf(top, qs[t], -m[t]) > kSlack)) {
-                const float nm = fmaxf(m[t], max_groups(top * qs[t]));
-                const float f = __builtin_amdgcn_exp2f(m[t] - nm);
-                m[t] = nm;
-                l[t] *= f;
-#pragma unroll
-                for (int i = 0; i < kDb; ++i) o[t][i] *= f;
-            }
             float sum = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float p = __builtin_amdgcn_exp2f(fmaf(x[j], qs[t], -m[t]));
+                const float x = s[j >> 2][t][j & 3];
+                const float p = __builtin_amdgcn_exp2f(fmaf(x, qs[t], -m[t]));
                 sum += p;
-                // a scale that another row of the lane sees may be NaN
-                w[t][j] = (_Float16)(EDGE && x[j] == -INFINITY ? 0.f : p * vs[j]);
+                w[t][j] = (_Float16)(p * vs[j]);
             }
             l[t] += sum;
         }
@@ -349,11 +387,16 @@ struct Wave {
                 for (int j = 0; j < 8; ++j) row[j] = blk.v[2 * half + (j >> 2)][j & 3];
                 transpose8(row, col);
             }
+            constexpr int n = D < 128 ? 4 : 8;
+            half8 x[2];
+            x[0] = lookup<true>(col[0], lane4);
 #pragma unroll
-            for (int i = 0; i < (D < 128 ? 4 : 8); ++i) {
-                const half8 x = lookup<true>(tab, col[i], lane4);
+            for (int i = 0; i < n; ++i) {
+                if (i + 1 < n) x[(i + 1) & 1] = lookup<true>(col[i + 1], lane4);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) o[t][8 * half + i] = mfma(x, w[t], o[t][8 * half + i]);
+                for (int t = 0; t < NT; ++t)
+                    o[t][8 * half + i] = mfma(x[i & 1], w[t], o[t][8 * half + i]);
             }
         }
     }
@@ -389,32 +432,35 @@ __device__ inline void load_block(const AttnArgs& a, const Walk& wk, int page, i
     b.vs = *reinterpret_cast<const uintx4*>(s + a.page_size);
 }
 
-// Blocks first, first + stride, ... below end.  The next block's codes and
-// the page of the one after are loaded while a block is computed.
-template <int D, int DT, int NT>
+// Blocks first, first + stride, ... below end, through a ring of R blocks in
+// registers: a block's codes are loaded R steps ahead, into the registers of
+// the one just done, and its page one step before that.
+template <int R, int D, int DT, int NT>
 __device__ inline void walk(const AttnArgs& a, Wave<D, DT, NT>& wv, const Walk& wk, int first,
-                            int end, int stride, LdsWord tab, int lane) {
+                            int end, int stride, int lane) {
     if (first >= end) return;
     const uint32_t lane4 = 4 * (lane & 31);
     const int g = lane >> 4, last = end - 1;
-    Block<D> cur, nxt;
-    int in, in2;
-    int page = block_page(a, wk, first, in);
-    load_block<D>(a, wk, page, in, lane, cur);
-    int b1 = first + stride < end ? first + stride : last;
-    page = block_page(a, wk, b1, in);
-    for (int b = first; b < end; b += stride) {
-        load_block<D>(a, wk, page, in, lane, nxt);
-        const int b2 = b + 2 * stride < end ? b + 2 * stride : last;
-        const int page2 = block_page(a, wk, b2, in2);
-        const int at = b * kKvBlock;
-        if (!cur.there || at < wv.inner_lo || at + kKvBlock > wv.inner_hi)
-            wv.template step<true>(cur, at, tab, lane4, g);
-        else
-            wv.template step<false>(cur, at, tab, lane4, g);
-        cur = nxt;
-        page = page2;
-        in = in2;
+    Block<D> ring[R];
+    int page, in;
+    auto ahead = [&](int b) { page = block_page(a, wk, b < end ? b : last, in); };
+    ahead(first);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int p = page, i = in;
+        ahead(first + (r + 1) * stride);
+        load_block<D>(a, wk, p, i, lane, ring[r]);
+    }
+    for (int b = first;;) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            wv.step(ring[r], b * kKvBlock, lane4, g);
+            const int p = page, i = in;
+            ahead(b + (R + 1) * stride);
+            load_block<D>(a, wk, p, i, lane, ring[r]);
+            b += stride;
+            if (b >= end) return;
+        }
     }
 }
 
@@ -500,7 +546,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_attn_rows(AttnArgs a) {
     __syncthreads();
     const Span sp = tile_span(a, rw.qlen, rw.seq, rw.r0, rw.n);
     const Walk wk{a.table + b * a.max_pages, h};
-    walk<D, DT, NT>(a, wv, wk, sp.lo, sp.hi, 1, (LdsWord)tab, lane);
+    walk<1, D, DT, NT>(a, wv, wk, sp.lo, sp.hi, 1, lane);
     const int g = lane >> 4, c = lane & 15;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -610,7 +656,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_attn_split(AttnArgs a) 
         Wave<D, DT, NT> wv;
         wv.load(a, rw, h, lane);
         const Walk wk{a.table + b * a.max_pages, h};
-        walk<D, DT, NT>(a, wv, wk, first + wave, first + take, kAttnWaves, (LdsWord)tab, lane);
+        walk<2, D, DT, NT>(a, wv, wk, first + wave, first + take, kAttnWaves, lane);
         at += take;
         const bool whole = take == all;
         // partial results of this share: place 0 for a request that began
@@ -743,23 +789,26 @@ __global__ __launch_bounds__(kAttnThreads) void k_kv4_attn_join(AttnArgs a) {
 // ---- launches ------------------------------------------------------------------
 
 template <int D, int DT, int NT>
-hipError_t attn_as(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
-    static LdsAttr rows_rec, split_rec;
-    if (!p.split) {
-        auto kern = k_kv4_attn_rows<D, DT, NT>;
-        hipError_t e = ensure_lds(rows_rec, reinterpret_cast<const void*>(kern), kTabBytes);
-        if (e != hipSuccess) return e;
-        constexpr int rows = 16 * NT * kAttnWaves;
-        const int64_t tiles = (a.T * a.G + rows - 1) / rows + a.B;
-        kern<<<dim3((unsigned)tiles, (unsigned)a.Hkv), dim3(kAttnThreads), kTabBytes, s>>>(a);
-        return hipGetLastError();
-    }
+hipError_t attn_rows(const AttnArgs& a, hipStream_t s) {
+    static LdsAttr rec;
+    auto kern = k_kv4_attn_rows<D, DT, NT>;
+    hipError_t e = ensure_lds(rec, reinterpret_cast<const void*>(kern), kTabBytes);
+    if (e != hipSuccess) return e;
+    constexpr int rows = 16 * NT * kAttnWaves;
+    const int64_t tiles = (a.T * a.G + rows - 1) / rows + a.B;
+    kern<<<dim3((unsigned)tiles, (unsigned)a.Hkv), dim3(kAttnThreads), kTabBytes, s>>>(a);
+    return hipGetLastError();
+}
+
+template <int D, int DT, int NT>
+hipError_t attn_split(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+    static LdsAttr rec;
     auto kern = k_kv4_attn_split<D, DT, NT>;
-    hipError_t e =
-        ensure_lds(split_rec, reinterpret_cast<const void*>(kern), kTabBytes + kMergeBytes);
+    constexpr int lds = kTabBytes + kMergeBytes;
+    hipError_t e = ensure_lds(rec, reinterpret_cast<const void*>(kern), lds);
     if (e != hipSuccess) return e;
     const unsigned y = (unsigned)(a.Hkv * p.row_tiles);
-    kern<<<dim3((unsigned)p.splits, y), dim3(kAttnThreads), kTabBytes + kMergeBytes, s>>>(a);
+    kern<<<dim3((unsigned)p.splits, y), dim3(kAttnThreads), lds, s>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     k_kv4_attn_join<D, DT, NT><<<dim3((unsigned)a.B, y), dim3(kAttnThreads), 0, s>>>(a);
@@ -768,11 +817,12 @@ hipError_t attn_as(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
 
 template <int D, int DT>
 hipError_t attn_cols(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+    if (!p.split) return attn_rows<D, DT, kRowCols<D>>(a, s);
     switch (p.col_blocks) {
-        case 1: return attn_as<D, DT, 1>(a, p, s);
-        case 2: return attn_as<D, DT, 2>(a, p, s);
+        case 1: return attn_split<D, DT, 1>(a, p, s);
+        case 2: return attn_split<D, DT, 2>(a, p, s);
         default:
-            if constexpr (D <= 128) return attn_as<D, DT, 4>(a, p, s);
+            if constexpr (D <= 128) return attn_split<D, DT, 4>(a, p, s);
             else return hipErrorInvalidValue;
     }
 }

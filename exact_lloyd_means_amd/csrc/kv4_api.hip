@@ -19,7 +19,7 @@ AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q)
     const int64_t tiles = (rows + tile - 1) / tile;
     // Waves over rows need no join, but a card full of rows; below that the
     // keys are split.
-    const int64_t row_wgs = (T * G + 4 * tile - 1) / (4 * tile) * Hkv;
+    const int64_t wg = 64 * row_cols(D), row_wgs = (T * G + wg - 1) / wg * Hkv;
     p.split = (rows <= tile || row_wgs < kResident) && tiles * Hkv <= 65535;
     p.row_tiles = p.split ? (int)tiles : 1;
     if (p.split) {

@@ -69,6 +69,14 @@ struct AttnArgs {
     int64_t* prefix;      //             [row_tiles][B + 1] blocks before each request
 };
 
+#ifndef ROWS_NT
+#define ROWS_NT 3
+#endif
+// Column blocks of a wave in the rows form, by head dimension.
+template <int D>
+constexpr int kRowCols = D == 64 ? 4 : D == 128 ? ROWS_NT : 2;
+inline int row_cols(int D) { return D == 64 ? kRowCols<64> : D == 128 ? kRowCols<128> : kRowCols<256>; }
+
 // Query rows of a tile (16 per matrix column block) and the form a call runs.
 struct AttnPlan {
     int col_blocks;   // 1, 2 or 4 blocks of 16 query rows per wave
