@@ -39,7 +39,6 @@ namespace {
 constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = 4;
 constexpr int kTabBytes = 65536;
-constexpr int kMergeBytes = 16384;
 constexpr float kNoMax = -1e30f;   // running maximum before any key
 constexpr float kSlack = 8.f;      // how far a score may exceed it, log2
 
@@ -112,14 +111,14 @@ __device__ inline half8 lookup(uint32_t codes, uint32_t lane4) {
 }
 
 // The pair table of one kv head: 256 entries of 64 dwords, k copies in 0-31,
-// v copies in 32-63.  Thread t writes 16-byte column t % 16 of the entries
-// whose low nibble is t / 16.
-__device__ inline void build_table(uint32_t* tab, const uint16_t* codebook, int H, int h, int tid) {
-    const int col = tid & 15, lo = tid >> 4;
+// v copies in 32-63.  A thread writes the 16-byte column tid % 16 of entries
+// whose low nibble is tid / 16 % 16.
+__device__ inline void build_table(uint32_t* tab, const uint16_t* codebook, int H, int h, int tid,
+                                   int threads) {
+    const int col = tid & 15, lo = tid >> 4 & 15;
     const uint16_t* cb = codebook + ((col >> 3) * H + h) * 16;
     const uint32_t low = cb[lo];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = tid >> 8; i < 16; i += threads >> 8) {
         const uint32_t v = low | (uint32_t)cb[i] << 16;
         uintx4 y = {v, v, v, v};
         *reinterpret_cast<uintx4*>(tab + (i * 16 + lo) * 64 + col * 4) = y;
@@ -464,7 +463,8 @@ __device__ inline void walk(const AttnArgs& a, Wave<D, DT, NT>& wv, const Walk& 
     }
 }
 
-// Inclusive scan over the workgroup's 256 threads; scratch of 4 int64.
+// Inclusive scan over the threads of W waves; scratch of W int64.
+template <int W>
 __device__ inline int64_t group_scan(int64_t x, int64_t* scratch, int64_t& total, int tid) {
     const int lane = tid & 63, wave = tid >> 6;
 #pragma unroll
@@ -476,7 +476,7 @@ __device__ inline int64_t group_scan(int64_t x, int64_t* scratch, int64_t& total
     __syncthreads();
     total = 0;
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) {
+    for (int w = 0; w < W; ++w) {
         const int64_t y = scratch[w];
         if (w < wave) x += y;
         total += y;
@@ -493,60 +493,10 @@ __device__ inline void store_out(const AttnArgs& a, int64_t tok, int head, int D
     *reinterpret_cast<uint2*>(a.out + (tok * a.Hq + head) * D + d) = make_uint2(lo, hi);
 }
 
-// ---- rows form: every wave of a workgroup takes other query rows ------------
-
-// Grid (row tiles of all requests, kv heads).  A workgroup's tile is 4 x 16
-// NT rows of one request; tiles of a request run from its last rows, which
-// see the most keys, to its first.
+// Results of a wave that saw all keys of its rows.
 template <int D, int DT, int NT>
-__global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_attn_rows(AttnArgs a) {
-    extern __shared__ uint32_t tab[];
-    int64_t* scratch = reinterpret_cast<int64_t*>(tab);
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int h = blockIdx.y;
-    constexpr int rows = 16 * NT * kAttnWaves;
-    // which request holds tile blockIdx.x
-    const int per = (a.B + kAttnThreads - 1) / kAttnThreads;
-    const int64_t b0 = (int64_t)tid * per;
-    int64_t mine = 0, total, tok0;
-    int qlen, seq;
-    for (int64_t b = b0; b < b0 + per && b < a.B; ++b) {
-        request_lens(a, b, tok0, qlen, seq);
-        mine += ((int64_t)qlen * a.G + rows - 1) / rows;
-    }
-    int64_t before = group_scan(mine, scratch, total, tid) - mine;
-    const int64_t want = blockIdx.x;
-    if (want >= total) return;
-    if (want >= before && want < before + mine) {
-        int64_t b = b0;
-        for (;; ++b) {
-            request_lens(a, b, tok0, qlen, seq);
-            const int64_t n = ((int64_t)qlen * a.G + rows - 1) / rows;
-            if (want < before + n) {
-                scratch[0] = b;
-                scratch[1] = n - 1 - (want - before);
-                break;
-            }
-            before += n;
-        }
-    }
-    __syncthreads();
-    const int64_t b = scratch[0];
-    const int tile = (int)scratch[1];
-    __syncthreads();
-    build_table(tab, a.codebook, a.Hkv, h, tid);
-    Rows rw;
-    request_lens(a, b, rw.tok0, rw.qlen, rw.seq);
-    rw.r0 = tile * rows + wave * 16 * NT;
-    const int64_t left = (int64_t)rw.qlen * a.G - rw.r0;
-    rw.n = left < 0 ? 0 : left > 16 * NT ? 16 * NT : (int)left;
-    Wave<D, DT, NT> wv;
-    wv.load(a, rw, h, lane);
-    __syncthreads();
-    const Span sp = tile_span(a, rw.qlen, rw.seq, rw.r0, rw.n);
-    const Walk wk{a.table + b * a.max_pages, h};
-    walk<1, D, DT, NT>(a, wv, wk, sp.lo, sp.hi, 1, lane);
+__device__ inline void finish(const AttnArgs& a, const Wave<D, DT, NT>& wv, const Rows& rw, int h,
+                              int lane) {
     const int g = lane >> 4, c = lane & 15;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -571,7 +521,64 @@ __global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_attn_rows(AttnArgs a) {
     }
 }
 
-// ---- split form: every wave of a workgroup takes other keys -----------------
+// ---- rows form: every wave of a workgroup takes other query rows ------------
+
+// Grid (row tiles of all requests, kv heads).  A workgroup's tile is 4 x 16
+// NT rows of one request; tiles of a request run from its last rows, which
+// see the most keys, to its first.
+template <int D, int DT, int NT>
+__global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_attn_rows(AttnArgs a) {
+    extern __shared__ uint32_t tab[];
+    int64_t* scratch = reinterpret_cast<int64_t*>(tab);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int h = blockIdx.y;
+    constexpr int rows = 16 * NT * kAttnWaves;
+    // which request holds tile blockIdx.x
+    const int per = (a.B + kAttnThreads - 1) / kAttnThreads;
+    const int64_t b0 = (int64_t)tid * per;
+    int64_t mine = 0, total, tok0;
+    int qlen, seq;
+    for (int64_t b = b0; b < b0 + per && b < a.B; ++b) {
+        request_lens(a, b, tok0, qlen, seq);
+        mine += ((int64_t)qlen * a.G + rows - 1) / rows;
+    }
+    int64_t before = group_scan<kAttnWaves>(mine, scratch, total, tid) - mine;
+    const int64_t want = blockIdx.x;
+    if (want >= total) return;
+    if (want >= before && want < before + mine) {
+        int64_t b = b0;
+        for (;; ++b) {
+            request_lens(a, b, tok0, qlen, seq);
+            const int64_t n = ((int64_t)qlen * a.G + rows - 1) / rows;
+            if (want < before + n) {
+                scratch[0] = b;
+                scratch[1] = n - 1 - (want - before);
+                break;
+            }
+            before += n;
+        }
+    }
+    __syncthreads();
+    const int64_t b = scratch[0];
+    const int tile = (int)scratch[1];
+    __syncthreads();
+    build_table(tab, a.codebook, a.Hkv, h, tid, kAttnThreads);
+    Rows rw;
+    request_lens(a, b, rw.tok0, rw.qlen, rw.seq);
+    rw.r0 = tile * rows + wave * 16 * NT;
+    const int64_t left = (int64_t)rw.qlen * a.G - rw.r0;
+    rw.n = left < 0 ? 0 : left > 16 * NT ? 16 * NT : (int)left;
+    Wave<D, DT, NT> wv;
+    wv.load(a, rw, h, lane);
+    __syncthreads();
+    const Span sp = tile_span(a, rw.qlen, rw.seq, rw.r0, rw.n);
+    const Walk wk{a.table + b * a.max_pages, h};
+    walk<1, D, DT, NT>(a, wv, wk, sp.lo, sp.hi, 1, lane);
+    finish<D, DT, NT>(a, wv, rw, h, lane);
+}
+
+// ---- split form: every wave takes other keys ------------------------------------
 
 // Visible blocks of row tile rt of request b.
 template <int NT>
@@ -583,28 +590,66 @@ __device__ inline Span split_span(const AttnArgs& a, int64_t b, int rt, Rows& rw
     return tile_span(a, rw.qlen, rw.seq, rw.r0, rw.n);
 }
 
-// Blocks a workgroup takes of `total`: an equal share of at least one a wave.
-__device__ inline int64_t split_share(int64_t total, int splits) {
-    const int64_t per = (total + splits - 1) / splits;
-    return per < kAttnWaves ? kAttnWaves : per;
+// Waves of a workgroup: with one column block of at most 128 dimensions four
+// waves fit a SIMD (128 registers), else two.
+#ifndef SW1
+#define SW1 8
+#endif
+template <int D, int NT>
+constexpr int kSplitWaves = NT == 1 && D <= 128 ? SW1 : 4;
+
+// Blocks a wave takes of `total`: an equal share of at least kMinShare, so
+// that the results of a share do not outweigh its codes.
+#ifndef MINSHARE
+#define MINSHARE 4
+#endif
+__device__ inline int64_t split_share(int64_t total, int64_t waves) {
+    const int64_t per = (total + waves - 1) / waves;
+    return per < MINSHARE ? MINSHARE : per;
+}
+
+// Sums of a share of a request, for the join.
+template <int D, int DT, int NT>
+__device__ inline void store_part(const AttnArgs& a, const Wave<D, DT, NT>& wv, const Rows& rw,
+                                  int64_t part, int lane) {
+    const int g = lane >> 4, c = lane & 15;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        float l = wv.l[t];
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        if (t * 16 + c >= rw.n) continue;
+        const int64_t row = part * a.part_rows + t * 16 + c;
+        const float f = 1.f / wv.vg;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k) {
+                floatx4 x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = wv.o[t][4 * k + j][e] * f;
+                *reinterpret_cast<floatx4*>(a.part_o + row * D + (4 * g + e) * (D / 16) + 4 * k) = x;
+            }
+        if (g == 0) *reinterpret_cast<float2*>(a.part_ml + row * 2) = make_float2(wv.m[t], l);
+    }
 }
 
 // Grid (splits, row tiles x kv heads).  The blocks of a (row tile, head) over
 // all requests form one line that is cut into equal shares, whatever the
-// lengths; a workgroup walks its share request by request, its waves taking
-// every fourth block, and adds the waves up in LDS.  A request that lies
-// within one share is finished there; else its shares go to the workspace
-// and k_kv4_attn_join adds them in order.
+// lengths, one a wave.  A wave walks its share request by request; a request
+// that lies whole in it is finished there, else its sums go to the workspace
+// and k_kv4_attn_join adds the shares of a request in order.  Waves meet
+// nowhere after the table is built.
 template <int D, int DT, int NT>
-__global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_attn_split(AttnArgs a) {
-    extern __shared__ uint32_t lds[];
-    uint32_t* tab = lds;
-    float* merge = reinterpret_cast<float*>(lds + kTabBytes / 4);
-    int64_t* scratch = reinterpret_cast<int64_t*>(merge);
+__global__ __launch_bounds__((64 * kSplitWaves<D, NT>), (kSplitWaves<D, NT> / 2))
+void k_kv4_attn_split(AttnArgs a) {
+    constexpr int W = kSplitWaves<D, NT>, kThreads = 64 * W;
+    extern __shared__ uint32_t tab[];
+    int64_t* scratch = reinterpret_cast<int64_t*>(tab);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y - h * a.row_tiles;
-    const int per = (a.B + kAttnThreads - 1) / kAttnThreads;
+    const int per = (a.B + kThreads - 1) / kThreads;
     const int64_t b0 = (int64_t)tid * per;
     Rows rw;
     int64_t mine = 0, total;
@@ -612,178 +657,120 @@ __global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_attn_split(AttnArgs a) 
         const Span sp = split_span<NT>(a, b, rt, rw);
         mine += sp.hi - sp.lo;
     }
-    int64_t before = group_scan(mine, scratch, total, tid) - mine;
-    if (blockIdx.x == 0 && h == 0) {  // what the join needs
-        int64_t at = before;
+    int64_t at = group_scan<W>(mine, scratch, total, tid) - mine;
+    const int64_t share = split_share(total, (int64_t)a.splits * W);
+    const int64_t first_wave = (int64_t)blockIdx.x * W;
+    // Where the shares of this workgroup begin, and what the join needs.
+    const bool tell = blockIdx.x == 0 && h == 0;
+    const int64_t begin = first_wave * share, stop = begin + W * share;
+    if (tell || (at < stop && at + mine > begin)) {
         int64_t* prefix = a.prefix + (int64_t)rt * (a.B + 1);
         for (int64_t b = b0; b < b0 + per && b < a.B; ++b) {
             const Span sp = split_span<NT>(a, b, rt, rw);
-            prefix[b] = at;
-            at += sp.hi - sp.lo;
-        }
-        if (tid == 0) prefix[a.B] = total;
-    }
-    const int64_t share = split_share(total, a.splits);
-    const int64_t from = (int64_t)blockIdx.x * share;
-    const int64_t to = from + share < total ? from + share : total;
-    if (from >= to) return;
-    if (from >= before && from < before + mine) {
-        int64_t at = before;
-        for (int64_t b = b0;; ++b) {
-            const Span sp = split_span<NT>(a, b, rt, rw);
-            if (from < at + sp.hi - sp.lo) {
-                scratch[0] = b;
-                scratch[1] = from - at;
-                break;
+            const int n = sp.hi - sp.lo;
+            if (tell) prefix[b] = at;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const int64_t from = begin + w * share;
+                if (from >= at && from < at + n) {
+                    scratch[2 * w] = b;
+                    scratch[2 * w + 1] = from - at;
+                }
             }
-            at += sp.hi - sp.lo;
+            at += n;
         }
+        if (tell && tid == 0) a.prefix[(int64_t)rt * (a.B + 1) + a.B] = total;
     }
+    if (begin >= total) return;
     __syncthreads();
-    int64_t b = scratch[0];
-    int skip = (int)scratch[1];  // blocks of request b that lie before the share
+    int64_t b = scratch[2 * wave];
+    int skip = (int)scratch[2 * wave + 1];  // blocks of request b before the share
     __syncthreads();
-    build_table(tab, a.codebook, a.Hkv, h, tid);
+    build_table(tab, a.codebook, a.Hkv, h, tid, kThreads);
     __syncthreads();
 
-    const int g = lane >> 4, c = lane & 15;
-    for (int64_t at = from; at < to; ++b, skip = 0) {
+    const int64_t from = begin + wave * share;
+    int64_t left = total - from;  // of the share
+    left = left > share ? share : left;
+    const int64_t part = ((int64_t)blockIdx.y * a.splits * W + first_wave + wave) * 2;
+    b = __builtin_amdgcn_readfirstlane((int)b);
+    skip = __builtin_amdgcn_readfirstlane(skip);
+    for (int place = 0; left > 0; ++b, skip = 0) {
         const Span sp = split_span<NT>(a, b, rt, rw);
         const int all = sp.hi - sp.lo;
         if (all == 0) continue;
-        const int first = sp.lo + skip;
-        const int take = (int)(to - at < all - skip ? to - at : all - skip);
+        const int take = all - skip < left ? all - skip : (int)left;
         Wave<D, DT, NT> wv;
         wv.load(a, rw, h, lane);
         const Walk wk{a.table + b * a.max_pages, h};
-        walk<2, D, DT, NT>(a, wv, wk, first + wave, first + take, kAttnWaves, lane);
-        at += take;
-        const bool whole = take == all;
-        // partial results of this share: place 0 for a request that began
-        // before it or ends with it as its first, else 1
-        const int64_t part = ((int64_t)blockIdx.y * a.splits + blockIdx.x) * 2 +
-                             (at - take == from ? 0 : 1);
-        // maxima and sums of the waves
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float l = wv.l[t];
-            l += __shfl_xor(l, 16);
-            l += __shfl_xor(l, 32);
-            if (g == 0) {
-                merge[(wave * 16 * NT + t * 16 + c) * 2] = wv.m[t];
-                merge[(wave * 16 * NT + t * 16 + c) * 2 + 1] = l;
-            }
-        }
-        __syncthreads();
-        float top[NT], sum[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float mw[kAttnWaves], lw[kAttnWaves];
-            top[t] = kNoMax;
-#pragma unroll
-            for (int w = 0; w < kAttnWaves; ++w) {
-                mw[w] = merge[(w * 16 * NT + t * 16 + c) * 2];
-                lw[w] = merge[(w * 16 * NT + t * 16 + c) * 2 + 1];
-                top[t] = fmaxf(top[t], mw[w]);
-            }
-            sum[t] = 0.f;
-#pragma unroll
-            for (int w = 0; w < kAttnWaves; ++w)
-                sum[t] += lw[w] * __builtin_amdgcn_exp2f(mw[w] - top[t]);
-            const float f = __builtin_amdgcn_exp2f(wv.m[t] - top[t]) / wv.vg;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) wv.o[t][i] *= f;
-        }
-        __syncthreads();
-        // sums of O over the waves, 16 accumulators a round: wave w adds
-        // piece w (4 consecutive dimensions a lane) of the four waves
-        constexpr int kRegs = 256 / D;  // accumulator elements e of a round
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e0 = 0; e0 < 4; e0 += kRegs) {
-                floatx4* buf = reinterpret_cast<floatx4*>(merge);
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const int e = e0 + p / (D / 64), k = p % (D / 64);
-                    floatx4 x;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j] = wv.o[t][4 * k + j][e];
-                    buf[(wave * 4 + p) * 64 + lane] = x;
-                }
-                __syncthreads();
-                floatx4 x = buf[wave * 64 + lane];
-#pragma unroll
-                for (int w = 1; w < kAttnWaves; ++w) x += buf[(w * 4 + wave) * 64 + lane];
-                const int e = e0 + wave / (D / 64), k = wave % (D / 64);
-                const int d = (4 * g + e) * (D / 16) + 4 * k;
-                if (t * 16 + c < rw.n) {
-                    if (whole) {
-                        const int r = rw.r0 + t * 16 + c, i = r / a.G, head = h * a.G + r - i * a.G;
-                        const float inv = sum[t] == 0.f ? 0.f : 1.f / sum[t];
-                        store_out<DT>(a, rw.tok0 + i, head, D, d, x * inv);
-                    } else {
-                        *reinterpret_cast<floatx4*>(a.part_o + (part * 16 * NT + t * 16 + c) * D + d) = x;
-                    }
-                }
-                __syncthreads();
-            }
-        if (wave == 0 && g == 0) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (t * 16 + c >= rw.n) continue;
-                if (whole) {
-                    const int r = rw.r0 + t * 16 + c, i = r / a.G, head = h * a.G + r - i * a.G;
-                    if (a.lse)
-                        a.lse[(rw.tok0 + i) * a.Hq + head] =
-                            (top[t] + __builtin_amdgcn_logf(sum[t])) * 0.6931471805599453f;
-                } else {
-                    float* ml = a.part_ml + (part * 16 * NT + t * 16 + c) * 2;
-                    ml[0] = top[t];
-                    ml[1] = sum[t];
-                }
-            }
-        }
+        walk<1, D, DT, NT>(a, wv, wk, sp.lo + skip, sp.lo + skip + take, 1, lane);
+        if (take == all) finish<D, DT, NT>(a, wv, rw, h, lane);
+        else store_part<D, DT, NT>(a, wv, rw, part + place, lane);
+        left -= take;
+        place = 1;  // the share's first request has place 0, its last place 1
     }
 }
 
 // Adds the shares of requests that lie in several, in their order, and writes
-// zeros for rows that see nothing.  Grid (B, row tiles x kv heads); a thread
-// holds 4 consecutive dimensions of a row.
+// zeros for rows that see nothing.  Grid (B, row tiles x kv heads, rows); the
+// threads of a workgroup are D/4 wide, four dimensions each, and take every
+// kGroups-th share.
 template <int D, int DT, int NT>
 __global__ __launch_bounds__(kAttnThreads) void k_kv4_attn_join(AttnArgs a) {
-    const int tid = threadIdx.x;
+    constexpr int kGroups = kAttnThreads / (D / 4);
+    __shared__ floatx4 so[kAttnThreads];
+    __shared__ float sm[kGroups], sl[kGroups];
+    const int tid = threadIdx.x, grp = tid / (D / 4), d = 4 * (tid % (D / 4));
     const int64_t b = blockIdx.x;
-    const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y - h * a.row_tiles;
+    const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y - h * a.row_tiles, row = blockIdx.z;
     const int64_t* prefix = a.prefix + (int64_t)rt * (a.B + 1);
-    const int64_t lo = prefix[b], hi = prefix[b + 1], share = split_share(prefix[a.B], a.splits);
+    const int64_t lo = prefix[b], hi = prefix[b + 1];
+    const int64_t waves = (int64_t)a.splits * kSplitWaves<D, NT>;
+    const int64_t share = split_share(prefix[a.B], waves);
     const int64_t w0 = lo / share, w1 = hi > lo ? (hi - 1) / share : w0;
     if (hi > lo && w0 == w1) return;
     Rows rw;
     split_span<NT>(a, b, rt, rw);
-    for (int x = tid; x < rw.n * (D / 4); x += kAttnThreads) {
-        const int c = x / (D / 4), d = 4 * (x - c * (D / 4));
-        float top = kNoMax, sum = 0.f;
-        floatx4 o = {0, 0, 0, 0};
-        if (hi > lo)
-            for (int64_t w = w0; w <= w1; ++w) {
-                const int64_t part = (((int64_t)blockIdx.y * a.splits + w) * 2 +
-                                      (w == w0 && lo != w * share ? 1 : 0)) * 16 * NT + c;
-                const float m = a.part_ml[part * 2], l = a.part_ml[part * 2 + 1];
-                const floatx4 y = *reinterpret_cast<const floatx4*>(a.part_o + part * D + d);
-                const float nm = fmaxf(top, m);
-                const float f = __builtin_amdgcn_exp2f(top - nm), k = __builtin_amdgcn_exp2f(m - nm);
-                o = o * f + y * k;
-                sum = sum * f + l * k;
-                top = nm;
-            }
-        const int r = rw.r0 + c, i = r / a.G, head = h * a.G + r - i * a.G;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        store_out<DT>(a, rw.tok0 + i, head, D, d, o * inv);
-        if (a.lse && d == 0)
-            a.lse[(rw.tok0 + i) * a.Hq + head] =
-                (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+    if (row >= rw.n) return;
+    float top = kNoMax, sum = 0.f;
+    floatx4 o = {0, 0, 0, 0};
+    if (hi > lo) {
+#pragma unroll 4
+        for (int64_t w = w0 + grp; w <= w1; w += kGroups) {
+            const int64_t part = ((blockIdx.y * waves + w) * 2 +
+                                  (w == w0 && lo != w * share ? 1 : 0)) * a.part_rows + row;
+            const float m = a.part_ml[part * 2], l = a.part_ml[part * 2 + 1];
+            const floatx4 y = *reinterpret_cast<const floatx4*>(a.part_o + part * D + d);
+            const float nm = fmaxf(top, m);
+            const float f = __builtin_amdgcn_exp2f(top - nm), k = __builtin_amdgcn_exp2f(m - nm);
+            o = o * f + y * k;
+            sum = sum * f + l * k;
+            top = nm;
+        }
     }
+    so[tid] = o;
+    if (d == 0) {
+        sm[grp] = top;
+        sl[grp] = sum;
+    }
+    __syncthreads();
+    if (grp != 0) return;
+    float all = kNoMax;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) all = fmaxf(all, sm[i]);
+    sum = 0.f;
+    o = floatx4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        const float f = __builtin_amdgcn_exp2f(sm[i] - all);
+        sum += sl[i] * f;
+        o += so[i * (D / 4) + tid] * f;
+    }
+    const int r = rw.r0 + row, i = r / a.G, head = h * a.G + r - i * a.G;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    store_out<DT>(a, rw.tok0 + i, head, D, d, o * inv);
+    if (a.lse && d == 0)
+        a.lse[(rw.tok0 + i) * a.Hq + head] = (all + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
 }
 
 // ---- launches ------------------------------------------------------------------
@@ -804,14 +791,13 @@ template <int D, int DT, int NT>
 hipError_t attn_split(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
     static LdsAttr rec;
     auto kern = k_kv4_attn_split<D, DT, NT>;
-    constexpr int lds = kTabBytes + kMergeBytes;
-    hipError_t e = ensure_lds(rec, reinterpret_cast<const void*>(kern), lds);
+    hipError_t e = ensure_lds(rec, reinterpret_cast<const void*>(kern), kTabBytes);
     if (e != hipSuccess) return e;
     const unsigned y = (unsigned)(a.Hkv * p.row_tiles);
-    kern<<<dim3((unsigned)p.splits, y), dim3(kAttnThreads), lds, s>>>(a);
+    kern<<<dim3((unsigned)p.splits, y), dim3(64 * kSplitWaves<D, NT>), kTabBytes, s>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    k_kv4_attn_join<D, DT, NT><<<dim3((unsigned)a.B, y), dim3(kAttnThreads), 0, s>>>(a);
+    k_kv4_attn_join<D, DT, NT><<<dim3((unsigned)a.B, y, (unsigned)p.rows), dim3(kAttnThreads), 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -822,7 +808,7 @@ hipError_t attn_cols(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
         case 1: return attn_split<D, DT, 1>(a, p, s);
         case 2: return attn_split<D, DT, 2>(a, p, s);
         default:
-            if constexpr (D <= 128) return attn_split<D, DT, 4>(a, p, s);
+            if constexpr (kRowCols<D> > 2) return attn_split<D, DT, kRowCols<D>>(a, p, s);
             else return hipErrorInvalidValue;
     }
 }

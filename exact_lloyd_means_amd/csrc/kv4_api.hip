@@ -14,7 +14,7 @@ constexpr int kResident = 512;
 AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q) {
     AttnPlan p{};
     const int64_t G = Hq / Hkv, rows = G * max_q;
-    p.col_blocks = rows <= 16 ? 1 : rows <= 32 || D > 128 ? 2 : 4;
+    p.col_blocks = rows <= 16 ? 1 : rows <= 32 ? 2 : row_cols(D);
     const int64_t tile = 16 * p.col_blocks;
     const int64_t tiles = (rows + tile - 1) / tile;
     // Waves over rows need no join, but a card full of rows; below that the
@@ -22,11 +22,12 @@ AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q)
     const int64_t wg = 64 * row_cols(D), row_wgs = (T * G + wg - 1) / wg * Hkv;
     p.split = (rows <= tile || row_wgs < kResident) && tiles * Hkv <= 65535;
     p.row_tiles = p.split ? (int)tiles : 1;
+    p.rows = (int)(rows < tile ? rows : tile);
     if (p.split) {
         const int64_t s = kResident / (Hkv * tiles);
         p.splits = s < 1 ? 1 : (int)s;
         const size_t parts =
-            p.splits > 1 ? (size_t)Hkv * p.row_tiles * p.splits * 2 * (size_t)tile : 0;
+            (size_t)Hkv * p.row_tiles * p.splits * 8 * 2 * (size_t)p.rows;
         size_t o = 0;
         p.part_o = o;
         o = align256(o + parts * D * sizeof(float));
@@ -301,6 +302,7 @@ fk_status fk_kv4_attention(const fk_kv4_cache* c, const fk_kv4_attn* p, void* ws
     a.qk = p->scale * 1.4426950408889634f;
     a.row_tiles = plan.row_tiles;
     a.splits = plan.splits;
+    a.part_rows = plan.rows;
     char* w = static_cast<char*>(ws);
     a.part_o = reinterpret_cast<float*>(w + plan.part_o);
     a.part_ml = reinterpret_cast<float*>(w + plan.part_ml);

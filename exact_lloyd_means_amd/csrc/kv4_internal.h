@@ -64,8 +64,9 @@ struct AttnArgs {
     float qk;             // scale * log2 e
     int32_t row_tiles;    // split form: tiles of query rows of one request
     int32_t splits;       // split form: workgroups per (kv head, row tile)
-    float* part_o;        // split form: [Hkv * row_tiles][splits][2][rows][D]
-    float* part_ml;       //             [Hkv * row_tiles][splits][2][rows][2]
+    int32_t part_rows;    // split form: most rows of a tile
+    float* part_o;        // split form: [Hkv * row_tiles][waves][2][part_rows][D]
+    float* part_ml;       //             [Hkv * row_tiles][waves][2][part_rows][2]
     int64_t* prefix;      //             [row_tiles][B + 1] blocks before each request
 };
 
@@ -79,9 +80,10 @@ inline int row_cols(int D) { return D == 64 ? kRowCols<64> : D == 128 ? kRowCols
 
 // Query rows of a tile (16 per matrix column block) and the form a call runs.
 struct AttnPlan {
-    int col_blocks;   // 1, 2 or 4 blocks of 16 query rows per wave
+    int col_blocks;   // split form: blocks of 16 query rows per wave
     bool split;       // keys split over waves and workgroups, else rows
     int row_tiles, splits;
+    int rows;         // split form: most rows of a tile
     size_t part_o, part_ml, prefix, total;  // workspace: offsets and size
 };
 AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q);
