@@ -39,6 +39,7 @@ namespace {
 constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = 4;
 constexpr int kTabBytes = 65536;
+constexpr int kSplitLds = kTabBytes + 512;  // and what the waves tell each other
 constexpr float kNoMax = -1e30f;   // running maximum before any key
 constexpr float kSlack = 8.f;      // how far a score may exceed it, log2
 
@@ -175,6 +176,13 @@ struct Block {
     bool there;
 };
 
+#ifndef AHEAD1
+#define AHEAD1 1
+#endif
+// Lookups run this many products ahead of the matrix instructions.
+template <int NT>
+constexpr int kAhead = NT == 1 ? AHEAD1 : 1;
+
 template <int D, int DT, int NT>
 struct Wave {
     static constexpr int kDb = D / 16;  // dimension blocks of O
@@ -261,23 +269,25 @@ struct Wave {
             for (int t = 0; t < NT; ++t) s[u][t] = floatx4{0, 0, 0, 0};
         // the lookups of a step ahead of the products of the one before, and no
         // further: unfenced, the compiler hoists them all and runs out of registers
-        half8 x[2][2];
+        constexpr int F = kAhead<NT>;
+        half8 x[F + 1][2];
         auto keys = [&](int c) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int w = u * kKs + c;
-                x[c & 1][u] = lookup<false>(blk.k[w >> 2][w & 3], lane4);
+                x[c % (F + 1)][u] = lookup<false>(blk.k[w >> 2][w & 3], lane4);
             }
         };
-        keys(0);
+#pragma unroll
+        for (int c = 0; c < F && c < kKs; ++c) keys(c);
 #pragma unroll
         for (int c = 0; c < kKs; ++c) {
-            if (c + 1 < kKs) keys(c + 1);
+            if (c + F < kKs) keys(c + F);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) s[u][t] = mfma(x[c & 1][u], q[t][c], s[u][t]);
+                for (int t = 0; t < NT; ++t) s[u][t] = mfma(x[c % (F + 1)][u], q[t][c], s[u][t]);
         }
         float ks[8], vs[8];
         float big = 0.f;
@@ -387,81 +397,82 @@ struct Wave {
                 transpose8(row, col);
             }
             constexpr int n = D < 128 ? 4 : 8;
-            half8 x[2];
-            x[0] = lookup<true>(col[0], lane4);
+            half8 x[F + 1];
+#pragma unroll
+            for (int i = 0; i < F; ++i) x[i] = lookup<true>(col[i], lane4);
 #pragma unroll
             for (int i = 0; i < n; ++i) {
-                if (i + 1 < n) x[(i + 1) & 1] = lookup<true>(col[i + 1], lane4);
+                if (i + F < n) x[(i + F) % (F + 1)] = lookup<true>(col[i + F], lane4);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
-                    o[t][8 * half + i] = mfma(x[i & 1], w[t], o[t][8 * half + i]);
+                    o[t][8 * half + i] = mfma(x[i % (F + 1)], w[t], o[t][8 * half + i]);
             }
         }
     }
 };
 
-// Where a wave's blocks lie.
+// Blocks first, first + stride, ... below end (at least one) of a request, through a ring of R
+// blocks in registers: a block's codes are loaded R steps ahead, into the
+// registers of the one just done, and its page one step before that.  The
+// first loads are issued by begin(), ahead of other work.
+template <int R, int D>
 struct Walk {
     const int32_t* table;  // the request's row
-    int h;
-};
-
-__device__ inline int block_page(const AttnArgs& a, const Walk& wk, int blk, int& in) {
-    const uint32_t pg = a.bpp == 1 ? (uint32_t)blk
-                                   : (uint32_t)(((uint64_t)(uint32_t)blk * a.bpp_magic) >> 32);
-    in = blk - (int)(pg * a.bpp);
-    return wk.table[pg];
-}
-
-template <int D>
-__device__ inline void load_block(const AttnArgs& a, const Walk& wk, int page, int in, int lane,
-                                  Block<D>& b) {
-    b.there = (int64_t)page >= 0 && (int64_t)page < a.pages;
-    const int64_t at = ((int64_t)(b.there ? page : 0) * a.Hkv + wk.h) * 2;
-    const uint8_t* k = a.codes + (at * a.bpp + in) * (16 * D) + lane * 16;
-    const uint8_t* v = k + (int64_t)a.bpp * (16 * D);
-    const uint16_t* s = a.scales + at * a.page_size + in * kKvBlock + 8 * (lane >> 4);
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-        b.k[i] = *reinterpret_cast<const uintx4*>(k + 1024 * i);
-        b.v[i] = *reinterpret_cast<const uintx4*>(v + 1024 * i);
-    }
-    b.ks = *reinterpret_cast<const uintx4*>(s);
-    b.vs = *reinterpret_cast<const uintx4*>(s + a.page_size);
-}
-
-// Blocks first, first + stride, ... below end, through a ring of R blocks in
-// registers: a block's codes are loaded R steps ahead, into the registers of
-// the one just done, and its page one step before that.
-template <int R, int D, int DT, int NT>
-__device__ inline void walk(const AttnArgs& a, Wave<D, DT, NT>& wv, const Walk& wk, int first,
-                            int end, int stride, int lane) {
-    if (first >= end) return;
-    const uint32_t lane4 = 4 * (lane & 31);
-    const int g = lane >> 4, last = end - 1;
+    int h, first, end, stride, page, in;
     Block<D> ring[R];
-    int page, in;
-    auto ahead = [&](int b) { page = block_page(a, wk, b < end ? b : last, in); };
-    ahead(first);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int p = page, i = in;
-        ahead(first + (r + 1) * stride);
-        load_block<D>(a, wk, p, i, lane, ring[r]);
+
+    __device__ inline void ahead(const AttnArgs& a, int blk) {
+        blk = blk < end ? blk : end - 1;
+        const uint32_t pg = a.bpp == 1 ? (uint32_t)blk
+                                       : (uint32_t)(((uint64_t)(uint32_t)blk * a.bpp_magic) >> 32);
+        in = blk - (int)(pg * a.bpp);
+        page = table[pg];
     }
-    for (int b = first;;) {
+    __device__ inline void load(const AttnArgs& a, int lane, Block<D>& b) {
+        b.there = page >= 0 && page < a.pages;
+        const int64_t at = ((int64_t)(b.there ? page : 0) * a.Hkv + h) * 2;
+        const uint8_t* k = a.codes + (at * a.bpp + in) * (16 * D) + lane * 16;
+        const uint8_t* v = k + (int64_t)a.bpp * (16 * D);
+        const uint16_t* s = a.scales + at * a.page_size + in * kKvBlock + 8 * (lane >> 4);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            b.k[i] = *reinterpret_cast<const uintx4*>(k + 1024 * i);
+            b.v[i] = *reinterpret_cast<const uintx4*>(v + 1024 * i);
+        }
+        b.ks = *reinterpret_cast<const uintx4*>(s);
+        b.vs = *reinterpret_cast<const uintx4*>(s + a.page_size);
+    }
+    __device__ inline void begin(const AttnArgs& a, const int32_t* row, int head, int lo, int hi,
+                                 int by, int lane) {
+        table = row;
+        h = head;
+        first = lo;
+        end = hi;
+        stride = by;
+        ahead(a, first);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            wv.step(ring[r], b * kKvBlock, lane4, g);
-            const int p = page, i = in;
-            ahead(b + (R + 1) * stride);
-            load_block<D>(a, wk, p, i, lane, ring[r]);
-            b += stride;
-            if (b >= end) return;
+            load(a, lane, ring[r]);
+            ahead(a, first + (r + 1) * stride);
         }
     }
-}
+    template <int DT, int NT>
+    __device__ inline void run(const AttnArgs& a, Wave<D, DT, NT>& wv, int lane) {
+        const uint32_t lane4 = 4 * (lane & 31);
+        const int g = lane >> 4;
+        for (int b = first;;) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                wv.step(ring[r], b * kKvBlock, lane4, g);
+                b += stride;
+                if (b >= end) return;
+                load(a, lane, ring[r]);
+                ahead(a, b + R * stride);
+            }
+        }
+    }
+};
 
 // Inclusive scan over the threads of W waves; scratch of W int64.
 template <int W>
@@ -569,25 +580,30 @@ __global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_attn_rows(AttnArgs a) {
     rw.r0 = tile * rows + wave * 16 * NT;
     const int64_t left = (int64_t)rw.qlen * a.G - rw.r0;
     rw.n = left < 0 ? 0 : left > 16 * NT ? 16 * NT : (int)left;
+    const Span sp = tile_span(a, rw.qlen, rw.seq, rw.r0, rw.n);
+    Walk<1, D> wk;
+    if (sp.hi > sp.lo) wk.begin(a, a.table + b * a.max_pages, h, sp.lo, sp.hi, 1, lane);
     Wave<D, DT, NT> wv;
     wv.load(a, rw, h, lane);
     __syncthreads();
-    const Span sp = tile_span(a, rw.qlen, rw.seq, rw.r0, rw.n);
-    const Walk wk{a.table + b * a.max_pages, h};
-    walk<1, D, DT, NT>(a, wv, wk, sp.lo, sp.hi, 1, lane);
+    if (sp.hi > sp.lo) wk.run(a, wv, lane);
     finish<D, DT, NT>(a, wv, rw, h, lane);
 }
 
-// ---- split form: every wave takes other keys ------------------------------------
+// ---- few query rows: row tiles of requests ----------------------------------------
 
-// Visible blocks of row tile rt of request b.
+// Row tile rt of the request whose lengths rw holds, and its visible blocks.
 template <int NT>
-__device__ inline Span split_span(const AttnArgs& a, int64_t b, int rt, Rows& rw) {
-    request_lens(a, b, rw.tok0, rw.qlen, rw.seq);
+__device__ inline Span split_rows(const AttnArgs& a, int rt, Rows& rw) {
     rw.r0 = rt * 16 * NT;
     const int64_t left = (int64_t)rw.qlen * a.G - rw.r0;
     rw.n = left < 0 ? 0 : left > 16 * NT ? 16 * NT : (int)left;
     return tile_span(a, rw.qlen, rw.seq, rw.r0, rw.n);
+}
+template <int NT>
+__device__ inline Span split_span(const AttnArgs& a, int64_t b, int rt, Rows& rw) {
+    request_lens(a, b, rw.tok0, rw.qlen, rw.seq);
+    return split_rows<NT>(a, rt, rw);
 }
 
 // Waves of a workgroup: with one column block of at most 128 dimensions four
@@ -598,10 +614,93 @@ __device__ inline Span split_span(const AttnArgs& a, int64_t b, int rt, Rows& rw
 template <int D, int NT>
 constexpr int kSplitWaves = NT == 1 && D <= 128 ? SW1 : 4;
 
+// ---- whole form: one workgroup a (request, row tile, kv head) --------------------
+
+// Grid (B, row tiles x kv heads).  The waves take every W-th block; their
+// sums meet in LDS, over the table, which nobody needs by then.
+template <int D, int DT, int NT>
+__global__ __launch_bounds__((64 * kSplitWaves<D, NT>), (kSplitWaves<D, NT> / 2))
+void k_kv4_attn_whole(AttnArgs a) {
+    constexpr int W = kSplitWaves<D, NT>, kThreads = 64 * W;
+    extern __shared__ uint32_t tab[];
+    float2* ml = reinterpret_cast<float2*>(tab + kTabBytes / 4);  // [16 NT][W]
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t b = blockIdx.x;
+    const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y - h * a.row_tiles;
+    Rows rw;
+    const Span sp = split_span<NT>(a, b, rt, rw);
+    if (rw.n <= 0) return;
+    const bool some = sp.lo + wave < sp.hi;
+    Walk<1, D> wk;
+    if (some) wk.begin(a, a.table + b * a.max_pages, h, sp.lo + wave, sp.hi, W, lane);
+    build_table(tab, a.codebook, a.Hkv, h, tid, kThreads);
+    Wave<D, DT, NT> wv;
+    wv.load(a, rw, h, lane);
+    __syncthreads();
+    if (some) wk.run(a, wv, lane);
+    const int c = lane & 15;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        float l = wv.l[t];
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        if (lane < 16) ml[(t * 16 + c) * W + wave] = make_float2(wv.m[t], l);
+    }
+    __syncthreads();
+    floatx4* buf = reinterpret_cast<floatx4*>(tab);  // [W][D / 16][64]: accumulators of a wave
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        float top = kNoMax;
+#pragma unroll
+        for (int w = 0; w < W; ++w) top = fmaxf(top, ml[(t * 16 + c) * W + w].x);
+        const float f = __builtin_amdgcn_exp2f(wv.m[t] - top) / wv.vg;
+#pragma unroll
+        for (int p = 0; p < D / 16; ++p) {
+            const int e = p / (D / 64), k = p % (D / 64);
+            floatx4 x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = wv.o[t][4 * k + j][e] * f;
+            buf[(wave * (D / 16) + p) * 64 + lane] = x;
+        }
+        __syncthreads();
+        for (int i = tid; i < 4 * D; i += kThreads) {
+            const int p = i >> 6, e = p / (D / 64), k = p % (D / 64), row = t * 16 + (i & 15);
+            if (row >= rw.n) continue;
+            floatx4 x = buf[i];
+#pragma unroll
+            for (int w = 1; w < W; ++w) x += buf[w * 4 * D + i];
+            float most = kNoMax, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) most = fmaxf(most, ml[row * W + w].x);
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                sum += ml[row * W + w].y * __builtin_amdgcn_exp2f(ml[row * W + w].x - most);
+            const int r = rw.r0 + row, q = r / a.G, head = h * a.G + r - q * a.G;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int d = (4 * ((i >> 4) & 3) + e) * (D / 16) + 4 * k;
+            store_out<DT>(a, rw.tok0 + q, head, D, d, x * inv);
+            if (a.lse && d == 0)
+                a.lse[(rw.tok0 + q) * a.Hq + head] =
+                    (most + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+        }
+        if (t + 1 < NT) __syncthreads();
+    }
+}
+
+// ---- split form: shares of the keys, a wave each ----------------------------------
+
+#ifndef RING1
+#define RING1 1
+#endif
+// Blocks in flight per wave.
+template <int D, int NT>
+constexpr int kSplitRing = NT == 1 && D <= 128 ? RING1 : 1;
+
 // Blocks a wave takes of `total`: an equal share of at least kMinShare, so
 // that the results of a share do not outweigh its codes.
 #ifndef MINSHARE
-#define MINSHARE 4
+#define MINSHARE 2
 #endif
 __device__ inline int64_t split_share(int64_t total, int64_t waves) {
     const int64_t per = (total + waves - 1) / waves;
@@ -643,18 +742,25 @@ __device__ inline void store_part(const AttnArgs& a, const Wave<D, DT, NT>& wv, 
 template <int D, int DT, int NT>
 __global__ __launch_bounds__((64 * kSplitWaves<D, NT>), (kSplitWaves<D, NT> / 2))
 void k_kv4_attn_split(AttnArgs a) {
-    constexpr int W = kSplitWaves<D, NT>, kThreads = 64 * W;
+    constexpr int W = kSplitWaves<D, NT>, kThreads = 64 * W, R = kSplitRing<D, NT>;
     extern __shared__ uint32_t tab[];
-    int64_t* scratch = reinterpret_cast<int64_t*>(tab);
+    int64_t* scratch = reinterpret_cast<int64_t*>(tab + kTabBytes / 4);
+    struct Start {  // where a share begins
+        int64_t tok0;
+        int b, skip, qlen, seq;
+    };
+    Start* start = reinterpret_cast<Start*>(scratch + W);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y - h * a.row_tiles;
+    build_table(tab, a.codebook, a.Hkv, h, tid, kThreads);
     const int per = (a.B + kThreads - 1) / kThreads;
-    const int64_t b0 = (int64_t)tid * per;
+    const int b0 = tid * per;
     Rows rw;
     int64_t mine = 0, total;
-    for (int64_t b = b0; b < b0 + per && b < a.B; ++b) {
-        const Span sp = split_span<NT>(a, b, rt, rw);
+    Span sp = {0, 0};
+    for (int b = b0; b < b0 + per && b < a.B; ++b) {
+        sp = split_span<NT>(a, b, rt, rw);
         mine += sp.hi - sp.lo;
     }
     int64_t at = group_scan<W>(mine, scratch, total, tid) - mine;
@@ -665,17 +771,15 @@ void k_kv4_attn_split(AttnArgs a) {
     const int64_t begin = first_wave * share, stop = begin + W * share;
     if (tell || (at < stop && at + mine > begin)) {
         int64_t* prefix = a.prefix + (int64_t)rt * (a.B + 1);
-        for (int64_t b = b0; b < b0 + per && b < a.B; ++b) {
-            const Span sp = split_span<NT>(a, b, rt, rw);
+        for (int b = b0; b < b0 + per && b < a.B; ++b) {
+            if (per > 1) sp = split_span<NT>(a, b, rt, rw);
             const int n = sp.hi - sp.lo;
             if (tell) prefix[b] = at;
 #pragma unroll
             for (int w = 0; w < W; ++w) {
                 const int64_t from = begin + w * share;
-                if (from >= at && from < at + n) {
-                    scratch[2 * w] = b;
-                    scratch[2 * w + 1] = from - at;
-                }
+                if (from >= at && from < at + n)
+                    start[w] = {rw.tok0, b, (int)(from - at), rw.qlen, rw.seq};
             }
             at += n;
         }
@@ -683,46 +787,49 @@ void k_kv4_attn_split(AttnArgs a) {
     }
     if (begin >= total) return;
     __syncthreads();
-    int64_t b = scratch[2 * wave];
-    int skip = (int)scratch[2 * wave + 1];  // blocks of request b before the share
-    __syncthreads();
-    build_table(tab, a.codebook, a.Hkv, h, tid, kThreads);
-    __syncthreads();
 
-    const int64_t from = begin + wave * share;
-    int64_t left = total - from;  // of the share
+    int64_t left = total - (begin + wave * share);  // of the wave's share
     left = left > share ? share : left;
+    if (left <= 0) return;
     const int64_t part = ((int64_t)blockIdx.y * a.splits * W + first_wave + wave) * 2;
-    b = __builtin_amdgcn_readfirstlane((int)b);
-    skip = __builtin_amdgcn_readfirstlane(skip);
-    for (int place = 0; left > 0; ++b, skip = 0) {
-        const Span sp = split_span<NT>(a, b, rt, rw);
+    int b = __builtin_amdgcn_readfirstlane(start[wave].b);
+    int skip = __builtin_amdgcn_readfirstlane(start[wave].skip);  // blocks of b before the share
+    rw.tok0 = __builtin_amdgcn_readfirstlane((int)start[wave].tok0);
+    rw.qlen = __builtin_amdgcn_readfirstlane(start[wave].qlen);
+    rw.seq = __builtin_amdgcn_readfirstlane(start[wave].seq);
+    for (int place = 0;;) {
+        sp = split_rows<NT>(a, rt, rw);
         const int all = sp.hi - sp.lo;
-        if (all == 0) continue;
-        const int take = all - skip < left ? all - skip : (int)left;
-        Wave<D, DT, NT> wv;
-        wv.load(a, rw, h, lane);
-        const Walk wk{a.table + b * a.max_pages, h};
-        walk<1, D, DT, NT>(a, wv, wk, sp.lo + skip, sp.lo + skip + take, 1, lane);
-        if (take == all) finish<D, DT, NT>(a, wv, rw, h, lane);
-        else store_part<D, DT, NT>(a, wv, rw, part + place, lane);
-        left -= take;
-        place = 1;  // the share's first request has place 0, its last place 1
+        if (all > 0) {
+            const int take = all - skip < left ? all - skip : (int)left;
+            Walk<R, D> wk;
+            wk.begin(a, a.table + b * a.max_pages, h, sp.lo + skip, sp.lo + skip + take, 1, lane);
+            Wave<D, DT, NT> wv;
+            wv.load(a, rw, h, lane);
+            wk.run(a, wv, lane);
+            if (take == all) finish<D, DT, NT>(a, wv, rw, h, lane);
+            else store_part<D, DT, NT>(a, wv, rw, part + place, lane);
+            left -= take;
+            if (left <= 0) return;
+            place = 1;  // the share's first request has place 0, its last place 1
+            skip = 0;
+        }
+        ++b;
+        request_lens(a, b, rw.tok0, rw.qlen, rw.seq);
     }
 }
 
 // Adds the shares of requests that lie in several, in their order, and writes
-// zeros for rows that see nothing.  Grid (B, row tiles x kv heads, rows); the
-// threads of a workgroup are D/4 wide, four dimensions each, and take every
-// kGroups-th share.
+// zeros for rows that see nothing.  Grid (B, row tiles x kv heads, z): a
+// workgroup takes every z-th row, join_rows of them at once; the threads of a
+// row are D/4 wide, four dimensions each, and take every n-th share.
 template <int D, int DT, int NT>
 __global__ __launch_bounds__(kAttnThreads) void k_kv4_attn_join(AttnArgs a) {
     constexpr int kGroups = kAttnThreads / (D / 4);
     __shared__ floatx4 so[kAttnThreads];
     __shared__ float sm[kGroups], sl[kGroups];
-    const int tid = threadIdx.x, grp = tid / (D / 4), d = 4 * (tid % (D / 4));
     const int64_t b = blockIdx.x;
-    const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y - h * a.row_tiles, row = blockIdx.z;
+    const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y - h * a.row_tiles;
     const int64_t* prefix = a.prefix + (int64_t)rt * (a.B + 1);
     const int64_t lo = prefix[b], hi = prefix[b + 1];
     const int64_t waves = (int64_t)a.splits * kSplitWaves<D, NT>;
@@ -731,46 +838,71 @@ __global__ __launch_bounds__(kAttnThreads) void k_kv4_attn_join(AttnArgs a) {
     if (hi > lo && w0 == w1) return;
     Rows rw;
     split_span<NT>(a, b, rt, rw);
-    if (row >= rw.n) return;
-    float top = kNoMax, sum = 0.f;
-    floatx4 o = {0, 0, 0, 0};
-    if (hi > lo) {
-#pragma unroll 4
-        for (int64_t w = w0 + grp; w <= w1; w += kGroups) {
-            const int64_t part = ((blockIdx.y * waves + w) * 2 +
-                                  (w == w0 && lo != w * share ? 1 : 0)) * a.part_rows + row;
-            const float m = a.part_ml[part * 2], l = a.part_ml[part * 2 + 1];
-            const floatx4 y = *reinterpret_cast<const floatx4*>(a.part_o + part * D + d);
-            const float nm = fmaxf(top, m);
-            const float f = __builtin_amdgcn_exp2f(top - nm), k = __builtin_amdgcn_exp2f(m - nm);
-            o = o * f + y * k;
-            sum = sum * f + l * k;
-            top = nm;
+    const int tid = threadIdx.x, grp = tid / (D / 4), d = 4 * (tid % (D / 4));
+    const int n = kGroups / a.join_rows, sub = grp % n;  // threads of a row, which of them
+    for (int r0 = 0; r0 * (int)gridDim.z < rw.n; r0 += a.join_rows) {
+        const int row = (r0 + grp / n) * gridDim.z + blockIdx.z;
+        float top = kNoMax, sum = 0.f;
+        floatx4 o = {0, 0, 0, 0};
+        if (hi > lo && row < rw.n) {
+            constexpr int kBatch = 4;  // shares loaded at a time
+            for (int64_t w = w0 + sub; w <= w1; w += kBatch * n) {
+                float2 ml[kBatch];
+                floatx4 y[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int64_t x = w + i * n <= w1 ? w + i * n : w;
+                    const int64_t part = ((blockIdx.y * waves + x) * 2 +
+                                          (x == w0 && lo != x * share ? 1 : 0)) * a.part_rows + row;
+                    ml[i] = *reinterpret_cast<const float2*>(a.part_ml + part * 2);
+                    y[i] = *reinterpret_cast<const floatx4*>(a.part_o + part * D + d);
+                }
+                float nm = top;
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) nm = fmaxf(nm, ml[i].x);
+                float f = __builtin_amdgcn_exp2f(top - nm);
+                o *= f;
+                sum *= f;
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    f = w + i * n <= w1 ? __builtin_amdgcn_exp2f(ml[i].x - nm) : 0.f;
+                    o += y[i] * f;
+                    sum += ml[i].y * f;
+                }
+                top = nm;
+            }
+        }
+        if (n > 1) {
+            so[tid] = o;
+            if (d == 0) {
+                sm[grp] = top;
+                sl[grp] = sum;
+            }
+            __syncthreads();
+            if (sub == 0) {
+                float all = top;
+                for (int i = 1; i < n; ++i) all = fmaxf(all, sm[grp + i]);
+                float f = __builtin_amdgcn_exp2f(top - all);
+                sum *= f;
+                o *= f;
+                for (int i = 1; i < n; ++i) {
+                    f = __builtin_amdgcn_exp2f(sm[grp + i] - all);
+                    sum += sl[grp + i] * f;
+                    o += so[tid + i * (D / 4)] * f;
+                }
+                top = all;
+            }
+            __syncthreads();
+        }
+        if (sub == 0 && row < rw.n) {
+            const int r = rw.r0 + row, i = r / a.G, head = h * a.G + r - i * a.G;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            store_out<DT>(a, rw.tok0 + i, head, D, d, o * inv);
+            if (a.lse && d == 0)
+                a.lse[(rw.tok0 + i) * a.Hq + head] =
+                    (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
         }
     }
-    so[tid] = o;
-    if (d == 0) {
-        sm[grp] = top;
-        sl[grp] = sum;
-    }
-    __syncthreads();
-    if (grp != 0) return;
-    float all = kNoMax;
-#pragma unroll
-    for (int i = 0; i < kGroups; ++i) all = fmaxf(all, sm[i]);
-    sum = 0.f;
-    o = floatx4{0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-        const float f = __builtin_amdgcn_exp2f(sm[i] - all);
-        sum += sl[i] * f;
-        o += so[i * (D / 4) + tid] * f;
-    }
-    const int r = rw.r0 + row, i = r / a.G, head = h * a.G + r - i * a.G;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    store_out<DT>(a, rw.tok0 + i, head, D, d, o * inv);
-    if (a.lse && d == 0)
-        a.lse[(rw.tok0 + i) * a.Hq + head] = (all + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
 }
 
 // ---- launches ------------------------------------------------------------------
@@ -788,16 +920,29 @@ hipError_t attn_rows(const AttnArgs& a, hipStream_t s) {
 }
 
 template <int D, int DT, int NT>
+hipError_t attn_whole(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+    static LdsAttr rec;
+    auto kern = k_kv4_attn_whole<D, DT, NT>;
+    constexpr int W = kSplitWaves<D, NT>, lds = kTabBytes + 16 * NT * W * 8;
+    hipError_t e = ensure_lds(rec, reinterpret_cast<const void*>(kern), lds);
+    if (e != hipSuccess) return e;
+    kern<<<dim3((unsigned)a.B, (unsigned)(a.Hkv * p.row_tiles)), dim3(64 * W), lds, s>>>(a);
+    return hipGetLastError();
+}
+
+template <int D, int DT, int NT>
 hipError_t attn_split(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+    if (p.whole) return attn_whole<D, DT, NT>(a, p, s);
     static LdsAttr rec;
     auto kern = k_kv4_attn_split<D, DT, NT>;
-    hipError_t e = ensure_lds(rec, reinterpret_cast<const void*>(kern), kTabBytes);
+    hipError_t e = ensure_lds(rec, reinterpret_cast<const void*>(kern), kSplitLds);
     if (e != hipSuccess) return e;
     const unsigned y = (unsigned)(a.Hkv * p.row_tiles);
-    kern<<<dim3((unsigned)p.splits, y), dim3(64 * kSplitWaves<D, NT>), kTabBytes, s>>>(a);
+    kern<<<dim3((unsigned)p.splits, y), dim3(64 * kSplitWaves<D, NT>), kSplitLds, s>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    k_kv4_attn_join<D, DT, NT><<<dim3((unsigned)a.B, y, (unsigned)p.rows), dim3(kAttnThreads), 0, s>>>(a);
+    k_kv4_attn_join<D, DT, NT>
+        <<<dim3((unsigned)a.B, y, (unsigned)p.join_z), dim3(kAttnThreads), 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -4,6 +4,12 @@
 
 #include "kv4_internal.h"
 
+#ifndef WHOLE_A
+#define WHOLE_A 32
+#endif
+#ifndef WHOLE_B
+#define WHOLE_B 0
+#endif
 namespace fk {
 
 static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -11,7 +17,8 @@ static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 // Workgroups that run at once: two of 80 KB of LDS on each of 256 CUs.
 constexpr int kResident = 512;
 
-AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q) {
+AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q,
+                        int64_t max_blocks) {
     AttnPlan p{};
     const int64_t G = Hq / Hkv, rows = G * max_q;
     p.col_blocks = rows <= 16 ? 1 : rows <= 32 ? 2 : row_cols(D);
@@ -23,7 +30,19 @@ AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q)
     p.split = (rows <= tile || row_wgs < kResident) && tiles * Hkv <= 65535;
     p.row_tiles = p.split ? (int)tiles : 1;
     p.rows = (int)(rows < tile ? rows : tile);
-    if (p.split) {
+    // The keys of a request by one workgroup, no join: where the longest
+    // request that the table has room for is short, or the requests fill the
+    // card and none can hold it up for long.
+    if (p.split) p.whole = max_blocks <= WHOLE_A || (B * Hkv * tiles >= kResident / 2 && max_blocks <= WHOLE_B);
+    if (p.split && !p.whole) {
+        // The join's workgroups, of 1024 / D rows at a time: about eight a CU.
+        const int64_t tiles_all = B * Hkv * tiles;
+        int64_t z = 2048 / tiles_all;
+        z = z < 1 ? 1 : z > p.rows ? p.rows : z;
+        p.join_z = (int)z;
+        const int each = (int)((p.rows + z - 1) / z), most = 1024 / D;
+        p.join_rows = 1;
+        while (p.join_rows < each && p.join_rows < most) p.join_rows *= 2;
         const int64_t s = kResident / (Hkv * tiles);
         p.splits = s < 1 ? 1 : (int)s;
         const size_t parts =
@@ -244,7 +263,9 @@ size_t fk_kv4_attn_workspace_bytes(const fk_kv4_cache* c, int64_t B, int64_t T, 
     if (check_shape(c) != FK_OK || check_requests(B) != FK_OK || check_tokens(T) != FK_OK ||
         check_heads(c, T, q_heads, max_q) != FK_OK)
         return 0;
-    return plan_attention(B, T, q_heads, c->kv_heads, c->head_dim, clamp_max_q(T, max_q)).total;
+    // as much as a call with any block table needs
+    return plan_attention(B, T, q_heads, c->kv_heads, c->head_dim, clamp_max_q(T, max_q),
+                          (int64_t)1 << 40).total;
 }
 
 fk_status fk_kv4_attention(const fk_kv4_cache* c, const fk_kv4_attn* p, void* ws, size_t ws_bytes,
@@ -269,7 +290,8 @@ fk_status fk_kv4_attention(const fk_kv4_cache* c, const fk_kv4_attn* p, void* ws
     FK_CHECK(need(p->out, "out", 16));
     if (p->lse) FK_CHECK(need(p->lse, "lse", 4));
     const AttnPlan plan = plan_attention(p->B, p->T, p->q_heads, c->kv_heads, c->head_dim,
-                                         clamp_max_q(p->T, p->max_q));
+                                         clamp_max_q(p->T, p->max_q),
+                                         p->max_pages * (c->page_size / kKvBlock));
     if (!ws) return fail(FK_EWORKSPACE, "workspace is NULL");
     if (!aligned(ws, 16)) return fail(FK_EINVAL, "workspace is not 16-byte aligned");
     if (ws_bytes < plan.total)
@@ -303,6 +325,7 @@ fk_status fk_kv4_attention(const fk_kv4_cache* c, const fk_kv4_attn* p, void* ws
     a.row_tiles = plan.row_tiles;
     a.splits = plan.splits;
     a.part_rows = plan.rows;
+    a.join_rows = plan.join_rows;
     char* w = static_cast<char*>(ws);
     a.part_o = reinterpret_cast<float*>(w + plan.part_o);
     a.part_ml = reinterpret_cast<float*>(w + plan.part_ml);

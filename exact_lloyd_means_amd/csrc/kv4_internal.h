@@ -65,6 +65,7 @@ struct AttnArgs {
     int32_t row_tiles;    // split form: tiles of query rows of one request
     int32_t splits;       // split form: workgroups per (kv head, row tile)
     int32_t part_rows;    // split form: most rows of a tile
+    int32_t join_rows;    // join: rows of a workgroup at a time
     float* part_o;        // split form: [Hkv * row_tiles][waves][2][part_rows][D]
     float* part_ml;       //             [Hkv * row_tiles][waves][2][part_rows][2]
     int64_t* prefix;      //             [row_tiles][B + 1] blocks before each request
@@ -81,12 +82,15 @@ inline int row_cols(int D) { return D == 64 ? kRowCols<64> : D == 128 ? kRowCols
 // Query rows of a tile (16 per matrix column block) and the form a call runs.
 struct AttnPlan {
     int col_blocks;   // split form: blocks of 16 query rows per wave
-    bool split;       // keys split over waves and workgroups, else rows
+    bool split;       // row tiles of requests, else rows
+    bool whole;       // a workgroup takes a tile's keys whole, else shares
     int row_tiles, splits;
     int rows;         // split form: most rows of a tile
+    int join_z, join_rows;  // join: workgroups of a tile, rows of one at a time
     size_t part_o, part_ml, prefix, total;  // workspace: offsets and size
 };
-AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q);
+AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q,
+                        int64_t max_blocks);
 
 hipError_t launch_kv4_attn_d64(const AttnArgs& a, const AttnPlan& p, int dtype, hipStream_t s);
 hipError_t launch_kv4_attn_d128(const AttnArgs& a, const AttnPlan& p, int dtype, hipStream_t s);

@@ -22,79 +22,117 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
-from . import (DTYPES, _check, _need_gpu, _P, _stream, _want, _want_ws, lib)
+from . import DTYPES, _check, _need_gpu, _P, _stream, _want, _want_ws, lib
 
-__all__ = ["fk_kv_plan", "fk_kv4_write", "fk_kv4_read",
-           "fk_kv4_attention", "kv_plan_workspace", "kv4_attention_workspace"]
+__all__ = ["fk_kv_plan", "fk_kv4_write", "fk_kv4_read", "fk_kv4_attention", "kv_plan_workspace",
+           "kv4_attention_workspace"]
 
 _I32, _I64, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+# fk_kv4_cache and fk_kv4_attn of the C ABI, packed field by field: a decode
+# step makes several calls of a few microseconds, and a ctypes.Structure costs
+# more to fill than the rest of a call
+_CACHE = struct.Struct("@PPPqiiii")
+_ATTN = struct.Struct("@qqiiqqqPPPPfiiPP")
 
-
-class Kv4CacheArgs(ctypes.Structure):
-    _fields_ = [("codes", _P), ("scales", _P), ("codebook", _P), ("pages", _I64),
-                ("page_size", _I32), ("kv_heads", _I32), ("head_dim", _I32), ("dtype", _I32)]
-
-
-class Kv4AttnArgs(ctypes.Structure):
-    _fields_ = [("B", _I64), ("T", _I64), ("q_heads", _I32), ("max_q", _I32), ("max_pages", _I64),
-                ("q_token", _I64), ("q_head", _I64), ("q", _P), ("cu_q", _P), ("seq_lens", _P),
-                ("block_table", _P), ("scale", ctypes.c_float), ("causal", _I32),
-                ("window", _I32), ("out", _P), ("lse", _P)]
-
-
-_CP, _AP = ctypes.POINTER(Kv4CacheArgs), ctypes.POINTER(Kv4AttnArgs)
 for _name, (_args, _res) in {
     "fk_kv_plan_workspace_bytes": ([_I64], _SZ),
     "fk_kv_plan": ([_I64, _I64, _I32, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _P,
                     _SZ, _P], ctypes.c_int),
-    "fk_kv4_write": ([_CP, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P], ctypes.c_int),
-    "fk_kv4_read": ([_CP, _I64, _P, _P, _P, _P], ctypes.c_int),
-    "fk_kv4_attn_workspace_bytes": ([_CP, _I64, _I64, _I32, _I32], _SZ),
-    "fk_kv4_attention": ([_CP, _AP, _P, _SZ, _P], ctypes.c_int),
+    "fk_kv4_write": ([_P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P], ctypes.c_int),
+    "fk_kv4_read": ([_P, _I64, _P, _P, _P, _P], ctypes.c_int),
+    "fk_kv4_attn_workspace_bytes": ([_P, _I64, _I64, _I32, _I32], _SZ),
+    "fk_kv4_attention": ([_P, _P, _P, _SZ, _P], ctypes.c_int),
 }.items():
     _fn = getattr(lib, _name)
     _fn.argtypes = _args
     _fn.restype = _res
 
 _HALVES = (torch.float16, torch.bfloat16)
+_i32, _f16, _u8 = torch.int32, torch.float16, torch.uint8
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _cache_args(codebook, codes, scales):
-    """The C description of a cache, from its three tensors."""
-    if not isinstance(codes, torch.Tensor):
-        raise TypeError("codes must be a torch tensor")
-    if codes.dtype != torch.uint8 or codes.dim() != 5 or codes.shape[2] != 2:
-        raise ValueError("codes must be uint8 (pages, kv_heads, 2, page_size / 32, 16 * head_dim)")
-    pages, H, _, blocks, row = codes.shape
-    if row % 16:
-        raise ValueError("the last dimension of codes must be 16 * head_dim")
-    dev = codes.device
-    if not codes.is_contiguous():
-        raise ValueError("codes must be contiguous")
-    _want(scales, "scales", _HALVES, (pages, H, 2, 32 * blocks), dev)
-    if codebook is not None:
-        _want(codebook, "codebook", torch.float16, (2, H, 16), dev)
-    return Kv4CacheArgs(codes.data_ptr(), scales.data_ptr(),
-                        None if codebook is None else codebook.data_ptr(), pages, 32 * blocks, H,
-                        row // 16, DTYPES[scales.dtype]), dev
+def _device_of(index):
+    return torch.device("cuda", index) if index >= 0 else torch.device("cpu")
 
 
-def _want_rows(t, name, dtype, shape, dev):
-    """A (tokens, heads, head_dim) tensor whose rows are contiguous; tokens
-    and heads may be strided (a slice of a fused projection)."""
+def _at(t, name, dtype, shape, index):
+    """Address of a contiguous tensor of this dtype and shape on the device
+    of this index (-1: CPU).  Anything else goes to the binding's checks,
+    which say what is wrong with it."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == index
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _want(t, name, dtype, shape, _device_of(index))
+    return t.data_ptr()
+
+
+def _rows_at(t, name, dtype, shape, index):
+    """Address and strides of a (tokens, heads, head_dim) tensor whose rows
+    are contiguous; tokens and heads may be strided (a slice of a fused
+    projection)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.stride(2) != 1:
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected {_device_of(index)}")
+    token, head, one = t.stride()
+    if one != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t.data_ptr(), token, head
+
+
+def _tensor(t, name, dims):
+    """The shape of a tensor of so many dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(shape)}")
+    return shape
+
+
+def _on_gpu(index):
+    if index < 0:
+        _need_gpu(_device_of(index))
+
+
+def _stream_of(stream, index):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(index)
+    return _stream(stream)
+
+
+def _ws_at(ws, index):
+    if ws.dtype is not _u8 or ws.dim() != 1 or ws.get_device() != index:
+        _want_ws(ws, _device_of(index))
+    return ws.data_ptr(), ws.numel()
+
+
+def _cache(codebook, codes, scales):
+    """The C description of a cache, its heads, head_dim, dtype and device."""
+    pages, H, two, blocks, row = _tensor(codes, "codes", 5)
+    if codes.dtype is not _u8 or two != 2 or row % 16:
+        raise ValueError("codes must be uint8 (pages, kv_heads, 2, page_size / 32, 16 * head_dim)")
+    if not codes.is_contiguous():
+        raise ValueError("codes must be contiguous")
+    if not isinstance(scales, torch.Tensor) or scales.dtype not in _HALVES:
+        _want(scales, "scales", _HALVES, (pages, H, 2, 32 * blocks), codes.device)
+    dtype, index = scales.dtype, codes.get_device()
+    s = _at(scales, "scales", dtype, (pages, H, 2, 32 * blocks), index)
+    c = _at(codebook, "codebook", _f16, (2, H, 16), index)
+    return (_CACHE.pack(codes.data_ptr(), s, c, pages, 32 * blocks, H, row // 16, DTYPES[dtype]),
+            H, row // 16, dtype, index)
 
 
 def kv_plan_workspace(B: int, device=None) -> torch.Tensor:
@@ -109,71 +147,51 @@ def fk_kv_plan(ctx_lens, new_lens, page_size: int, free_pages, free_count, block
     (all int32): writes the needed entries of block_table (B, max_pages),
     seq_lens (B), cu_new (B + 1), slots and positions (any length; positions
     may be None), free_left (1) and status (4)."""
-    if not isinstance(ctx_lens, torch.Tensor):
-        raise TypeError("ctx_lens must be a torch tensor")
-    dev, i32 = ctx_lens.device, torch.int32
-    B = ctx_lens.numel()
-    _want(ctx_lens, "ctx_lens", i32, (B,), dev)
-    _want(new_lens, "new_lens", i32, (B,), dev)
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise ValueError("block_table must be a (B, max_pages) tensor")
-    M = block_table.shape[1]
-    _want(block_table, "block_table", i32, (B, M), dev)
-    _want(seq_lens, "seq_lens", i32, (B,), dev)
-    _want(cu_new, "cu_new", i32, (B + 1,), dev)
-    for t, name in ((free_pages, "free_pages"), (slots, "slots")):
-        if not isinstance(t, torch.Tensor) or t.dim() != 1:
-            raise ValueError(f"{name} must be a 1-D tensor")
-        _want(t, name, i32, t.shape, dev)
-    _want(positions, "positions", i32, slots.shape, dev, optional=True)
-    _want(free_count, "free_count", i32, (1,), dev)
-    _want(free_left, "free_left", i32, (1,), dev)
-    _want(status, "status", i32, (4,), dev)
-    _want_ws(ws, dev)
-    _need_gpu(dev)
-    ws = kv_plan_workspace(B, dev) if ws is None else ws
-    _check(lib.fk_kv_plan(B, M, int(page_size), ctx_lens.data_ptr(), new_lens.data_ptr(),
-                          free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(),
-                          block_table.data_ptr(), seq_lens.data_ptr(), cu_new.data_ptr(),
-                          slots.data_ptr(), None if positions is None else positions.data_ptr(),
-                          slots.numel(), free_left.data_ptr(), status.data_ptr(), ws.data_ptr(),
-                          ws.numel(), _stream(stream)), "fk_kv_plan")
+    (B,) = one = _tensor(ctx_lens, "ctx_lens", 1)
+    table = _tensor(block_table, "block_table", 2)
+    free = _tensor(free_pages, "free_pages", 1)
+    cap = _tensor(slots, "slots", 1)
+    index = ctx_lens.get_device()
+    args = (B, table[1], int(page_size), _at(ctx_lens, "ctx_lens", _i32, one, index),
+            _at(new_lens, "new_lens", _i32, one, index), _at(free_pages, "free_pages", _i32, free, index),
+            free[0], _at(free_count, "free_count", _i32, (1,), index),
+            _at(block_table, "block_table", _i32, (B, table[1]), index),
+            _at(seq_lens, "seq_lens", _i32, one, index), _at(cu_new, "cu_new", _i32, (B + 1,), index),
+            _at(slots, "slots", _i32, cap, index),
+            None if positions is None else _at(positions, "positions", _i32, cap, index), cap[0],
+            _at(free_left, "free_left", _i32, (1,), index), _at(status, "status", _i32, (4,), index))
+    _on_gpu(index)
+    if ws is None:
+        ws = kv_plan_workspace(B, ctx_lens.device)
+    _check(lib.fk_kv_plan(*args, *_ws_at(ws, index), _stream_of(stream, index)), "fk_kv_plan")
 
 
 def fk_kv4_write(k, v, slots, codebook, codes, scales, stream=None) -> None:
     """Rows k, v (T, kv_heads, head_dim) into the slots (T) of the cache."""
-    c, dev = _cache_args(codebook, codes, scales)
-    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
-        raise ValueError("slots must be a 1-D tensor")
-    T = slots.numel()
-    _want(slots, "slots", torch.int32, (T,), dev)
-    _want_rows(k, "k", scales.dtype, (T, c.kv_heads, c.head_dim), dev)
-    _want_rows(v, "v", scales.dtype, (T, c.kv_heads, c.head_dim), dev)
-    _need_gpu(dev)
-    _check(lib.fk_kv4_write(c, T, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
-                            v.stride(0), v.stride(1), slots.data_ptr(), _stream(stream)),
-           "fk_kv4_write")
+    c, H, D, dtype, index = _cache(codebook, codes, scales)
+    (T,) = one = _tensor(slots, "slots", 1)
+    at = _at(slots, "slots", _i32, one, index)
+    rows = (T, H, D)
+    args = (*_rows_at(k, "k", dtype, rows, index), *_rows_at(v, "v", dtype, rows, index))
+    _on_gpu(index)
+    _check(lib.fk_kv4_write(c, T, *args, at, _stream_of(stream, index)), "fk_kv4_write")
 
 
 def fk_kv4_read(slots, codebook, codes, scales, k, v, stream=None) -> None:
     """The rows of the slots (T) as values: k, v (T, kv_heads, head_dim)."""
-    c, dev = _cache_args(codebook, codes, scales)
-    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
-        raise ValueError("slots must be a 1-D tensor")
-    T = slots.numel()
-    _want(slots, "slots", torch.int32, (T,), dev)
-    _want(k, "k", scales.dtype, (T, c.kv_heads, c.head_dim), dev)
-    _want(v, "v", scales.dtype, (T, c.kv_heads, c.head_dim), dev)
-    _need_gpu(dev)
-    _check(lib.fk_kv4_read(c, T, slots.data_ptr(), k.data_ptr(), v.data_ptr(), _stream(stream)),
-           "fk_kv4_read")
+    c, H, D, dtype, index = _cache(codebook, codes, scales)
+    (T,) = one = _tensor(slots, "slots", 1)
+    args = (_at(slots, "slots", _i32, one, index), _at(k, "k", dtype, (T, H, D), index),
+            _at(v, "v", dtype, (T, H, D), index))
+    _on_gpu(index)
+    _check(lib.fk_kv4_read(c, T, *args, _stream_of(stream, index)), "fk_kv4_read")
 
 
 def kv4_attention_workspace(q, seq_lens, codes, max_q: int) -> torch.Tensor:
     """A caller-owned workspace for fk_kv4_attention of these sizes."""
-    T, Hq, D = q.shape
-    pages, H, _, blocks, _ = codes.shape
-    c = Kv4CacheArgs(None, None, None, pages, 32 * blocks, H, D, DTYPES.get(q.dtype, -1))
+    T, Hq, D = _tensor(q, "q", 3)
+    pages, H, _, blocks, _ = _tensor(codes, "codes", 5)
+    c = _CACHE.pack(0, 0, 0, pages, 32 * blocks, H, D, DTYPES.get(q.dtype, -1))
     n = lib.fk_kv4_attn_workspace_bytes(c, seq_lens.numel(), T, Hq, int(max_q))
     if n == 0:
         raise ValueError(lib.fk_last_error().decode())
@@ -187,28 +205,21 @@ def fk_kv4_attention(q, cu_q, seq_lens, block_table, codebook, codes, scales, ou
     cu_q[b] .. cu_q[b + 1] - 1, over the cached tokens of their requests; out
     like q, contiguous; lse (T, q_heads) fp32 or None; scale None: 1 /
     sqrt(head_dim)."""
-    c, dev = _cache_args(codebook, codes, scales)
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a (T, q_heads, head_dim) tensor")
-    T, Hq, D = q.shape
-    _want_rows(q, "q", scales.dtype, (T, Hq, c.head_dim), dev)
-    if not isinstance(seq_lens, torch.Tensor) or seq_lens.dim() != 1:
-        raise ValueError("seq_lens must be a 1-D tensor")
-    B, i32 = seq_lens.numel(), torch.int32
-    _want(seq_lens, "seq_lens", i32, (B,), dev)
-    _want(cu_q, "cu_q", i32, (B + 1,), dev)
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise ValueError("block_table must be a (B, max_pages) tensor")
-    M = block_table.shape[1]
-    _want(block_table, "block_table", i32, (B, M), dev)
-    _want(out, "out", scales.dtype, (T, Hq, D), dev)
-    _want(lse, "lse", torch.float32, (T, Hq), dev, optional=True)
-    _want_ws(ws, dev)
-    _need_gpu(dev)
-    ws = kv4_attention_workspace(q, seq_lens, codes, max_q) if ws is None else ws
-    a = Kv4AttnArgs(B, T, Hq, int(max_q), M, q.stride(0), q.stride(1), q.data_ptr(),
-                    cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
-                    1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(causal)),
-                    int(window), out.data_ptr(), None if lse is None else lse.data_ptr())
-    _check(lib.fk_kv4_attention(c, a, ws.data_ptr(), ws.numel(), _stream(stream)),
+    c, H, D, dtype, index = _cache(codebook, codes, scales)
+    T, Hq, _ = _tensor(q, "q", 3)
+    rows = (T, Hq, D)
+    at, token, head = _rows_at(q, "q", dtype, rows, index)
+    (B,) = one = _tensor(seq_lens, "seq_lens", 1)
+    table = _tensor(block_table, "block_table", 2)
+    args = _ATTN.pack(
+        B, T, Hq, max_q, table[1], token, head, at, _at(cu_q, "cu_q", _i32, (B + 1,), index),
+        _at(seq_lens, "seq_lens", _i32, one, index),
+        _at(block_table, "block_table", _i32, (B, table[1]), index),
+        1.0 / math.sqrt(D) if scale is None else scale, bool(causal), window,
+        _at(out, "out", dtype, rows, index),
+        0 if lse is None else _at(lse, "lse", torch.float32, (T, Hq), index))
+    _on_gpu(index)
+    if ws is None:
+        ws = kv4_attention_workspace(q, seq_lens, codes, max_q)
+    _check(lib.fk_kv4_attention(c, args, *_ws_at(ws, index), _stream_of(stream, index)),
            "fk_kv4_attention")
