@@ -26,9 +26,10 @@
 //
 // Running maximum: kept per query row and raised only when a score exceeds
 // it by 8 (p <= 256 in between), so that most blocks need no reduction over
-// lanes and no rescaling; l is summed over lanes at the end.  The v scales
-// are normalised by a power of two per wave (vg) that keeps w in fp16's
-// range; it follows the largest scale met.
+// lanes and no rescaling; l is summed over lanes at the end.  m also contains
+// the log2 of a power of two, the unit of v's scales, which follows the
+// largest scale met, so that w stays in fp16's range whatever the scales; it
+// scales O and l alike and cancels.
 #pragma once
 
 #include "kv4_internal.h"
@@ -192,7 +193,8 @@ struct Wave {
     floatx4 o[NT][kDb];
     float m[NT], l[NT], qs[NT];
     int lo[NT], hi[NT];  // positions the lane's query row sees
-    float vg;
+    float limit;  // 2^6 units
+    float slack;  // kSlack less log2 of the v scales' unit, which m contains
     int inner_lo, inner_hi;  // positions every row of the wave sees
 
     // Query rows r0 .. r0 + n - 1 of the request (n may be <= 0).
@@ -248,7 +250,8 @@ struct Wave {
 #pragma unroll
             for (int i = 0; i < kDb; ++i) o[t][i] = floatx4{0, 0, 0, 0};
         }
-        vg = 0x1p100f;
+        slack = kSlack;
+        limit = 0.f;  // the first scale sets the unit
         // bounds grow with the row, so the first and last rows tell
         if (rw.n > 0) {
             int x;
@@ -290,7 +293,6 @@ struct Wave {
                 for (int t = 0; t < NT; ++t) s[u][t] = mfma(x[c % (F + 1)][u], q[t][c], s[u][t]);
         }
         float ks[8], vs[8];
-        float big = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint32_t kw = blk.ks[j >> 1], vw = blk.vs[j >> 1];
@@ -344,33 +346,35 @@ struct Wave {
 #pragma unroll
             for (int j = 1; j < 8; ++j) top[t] = fmaxf(top[t], s[j >> 2][t][j & 3]);
         }
-        // raise the maxima by more than kSlack, keep v's scales below 2^6
-        // after their common factor
+        // raise the maxima by more than kSlack, keep v's scales below 2^6 units
+        float big = vs[0];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) big = fmaxf(big, vs[j]);
-        bool raise = big * vg > 64.f;
+        for (int j = 1; j < 8; ++j) big = fmaxf(big, vs[j]);
+        bool raise = big > limit;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) raise |= fmaf(top[t], qs[t], -m[t]) > kSlack;
+        for (int t = 0; t < NT; ++t) raise |= fmaf(top[t], qs[t], -m[t]) > slack;
         if (__any(raise)) {
             big = max_groups(big);
-            const int e = (int)(__builtin_bit_cast(uint32_t, big) >> 23 & 0xff) - 127;
-            float f = ldexpf(1.f, -e);
-            f = big * vg > 64.f && f < vg ? f : vg;  // it only falls
-            const float r = f / vg;
-            vg = f;
+            // log2 of the unit: of the power of two below the largest scale,
+            // down to 2^-96 (l holds its inverse)
+            const float old = kSlack - slack;
+            float unit = old;
+            if (big > limit) {
+                const int e = (int)(__builtin_bit_cast(uint32_t, big) >> 23 & 0xff) - 127;
+                unit = (float)(e < -96 ? -96 : e);
+                limit = ldexpf(64.f, (int)unit);
+                slack = kSlack - unit;
+            }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const float nm = fmaxf(m[t], max_groups(top[t] * qs[t]));
-                float x = __builtin_amdgcn_exp2f(m[t] - nm);
+                const float nm = fmaxf(m[t] - old, max_groups(top[t] * qs[t])) + unit;
+                const float x = __builtin_amdgcn_exp2f(m[t] - nm);
                 m[t] = nm;
                 l[t] *= x;
-                x *= r;
 #pragma unroll
                 for (int i = 0; i < kDb; ++i) o[t][i] *= x;
             }
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) vs[j] *= vg;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             float sum = 0.f;
@@ -517,7 +521,7 @@ __device__ inline void finish(const AttnArgs& a, const Wave<D, DT, NT>& wv, cons
         if (t * 16 + c >= rw.n) continue;
         const int r = rw.r0 + t * 16 + c, i = r / a.G, head = h * a.G + r - i * a.G;
         const int64_t tok = rw.tok0 + i;
-        const float inv = l == 0.f ? 0.f : 1.f / (l * wv.vg);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -534,45 +538,111 @@ __device__ inline void finish(const AttnArgs& a, const Wave<D, DT, NT>& wv, cons
 
 // ---- rows form: every wave of a workgroup takes other query rows ------------
 
-// Grid (row tiles of all requests, kv heads).  A workgroup's tile is 4 x 16
-// NT rows of one request; tiles of a request run from its last rows, which
-// see the most keys, to its first.
+// Requests that the heavy-first order can sort.
+constexpr int kOrderB = 256;
+
+// Grid: row tiles of all requests x kv heads, heads fastest, so that the
+// workgroups of a head tend to share an XCD's L2 and the heavy tiles of all
+// heads come first.  A workgroup's tile is 4 x 16 NT rows of one request.  Tiles differ in work by as much as the requests'
+// lengths, and a workgroup that starts late with a long one holds up the
+// end, so they are taken in the order of the keys before their last row, most
+// first.  With n_b tiles in request b and o_b tiles' worth of keys before
+// them, tile t is at level o_b + t; F(x) = sum_b clamp(o_b + n_b - x, 0, n_b)
+// tiles are at level x or above.  Every lane tries another x.  For more than
+// kOrderB requests each search would cost as much as it saves: requests in
+// order, each from its last tile.
 template <int D, int DT, int NT>
 __global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_attn_rows(AttnArgs a) {
     extern __shared__ uint32_t tab[];
-    int64_t* scratch = reinterpret_cast<int64_t*>(tab);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int h = blockIdx.y;
     constexpr int rows = 16 * NT * kAttnWaves;
-    // which request holds tile blockIdx.x
-    const int per = (a.B + kAttnThreads - 1) / kAttnThreads;
-    const int64_t b0 = (int64_t)tid * per;
-    int64_t mine = 0, total, tok0;
-    int qlen, seq;
-    for (int64_t b = b0; b < b0 + per && b < a.B; ++b) {
-        request_lens(a, b, tok0, qlen, seq);
-        mine += ((int64_t)qlen * a.G + rows - 1) / rows;
-    }
-    int64_t before = group_scan<kAttnWaves>(mine, scratch, total, tid) - mine;
-    const int64_t want = blockIdx.x;
-    if (want >= total) return;
-    if (want >= before && want < before + mine) {
-        int64_t b = b0;
-        for (;; ++b) {
-            request_lens(a, b, tok0, qlen, seq);
-            const int64_t n = ((int64_t)qlen * a.G + rows - 1) / rows;
-            if (want < before + n) {
-                scratch[0] = b;
-                scratch[1] = n - 1 - (want - before);
+    const int want = blockIdx.x / (uint32_t)a.Hkv, h = blockIdx.x - want * a.Hkv;
+    int64_t b = 0;
+    int tile = 0;
+    if (a.B <= kOrderB) {
+        int2* req = reinterpret_cast<int2*>(tab);  // (o_b, n_b)
+        int* most = reinterpret_cast<int*>(req + kOrderB);
+        if (tid == 0) most[0] = most[1] = 0;
+        __syncthreads();
+        if (tid < a.B) {
+            int64_t tok0;
+            int qlen, seq;
+            request_lens(a, tid, tok0, qlen, seq);
+            const int n = (int)(((int64_t)qlen * a.G + rows - 1) / rows);
+            int64_t before = a.causal ? (int64_t)seq - qlen : seq;
+            before = before < 0 ? 0 : before * a.G / rows;
+            const int o = before > (1 << 29) ? 1 << 29 : (int)before;
+            req[tid] = make_int2(o, n);
+            atomicMax(&most[0], o + n);
+            atomicAdd(&most[1], n);
+        }
+        __syncthreads();
+        if (want >= most[1]) return;
+        int lo = 0, len = most[0];  // F(lo) > want, F(lo + len) <= want
+        while (len > 1) {
+            const int step = (len + 63) / 64, x = lo + lane * step;
+            int f = 0;
+            for (int i = 0; i < a.B; ++i) {
+                const int2 r = req[i];
+                const int c = r.x + r.y - x;
+                f += c < 0 ? 0 : c > r.y ? r.y : c;
+            }
+            const int k = __popcll(__ballot(lane * step < len && f > want)) - 1;
+            lo += k * step;
+            len = len - k * step < step ? len - k * step : step;
+        }
+        int f = 0;  // tiles above the level
+        for (int i = lane; i < a.B; i += 64) {
+            const int2 r = req[i];
+            const int c = r.x + r.y - lo - 1;
+            f += c < 0 ? 0 : c > r.y ? r.y : c;
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) f += __shfl_xor(f, o);
+        int rank = want - f;  // within the level
+        for (int i0 = 0; i0 < a.B; i0 += 64) {
+            const int2 r = i0 + lane < a.B ? req[i0 + lane] : make_int2(0, 0);
+            uint64_t m = __ballot(lo >= r.x && lo < r.x + r.y);
+            const int k = __popcll(m);
+            if (rank < k) {
+                for (; rank > 0; --rank) m &= m - 1;
+                b = i0 + __builtin_ctzll(m);
+                tile = lo - req[b].x;
                 break;
             }
-            before += n;
+            rank -= k;
         }
+    } else {
+        int64_t* scratch = reinterpret_cast<int64_t*>(tab);
+        const int per = (a.B + kAttnThreads - 1) / kAttnThreads;
+        const int64_t b0 = (int64_t)tid * per;
+        int64_t mine = 0, total, tok0;
+        int qlen, seq;
+        for (int64_t i = b0; i < b0 + per && i < a.B; ++i) {
+            request_lens(a, i, tok0, qlen, seq);
+            mine += ((int64_t)qlen * a.G + rows - 1) / rows;
+        }
+        int64_t before = group_scan<kAttnWaves>(mine, scratch, total, tid) - mine;
+        if (want >= total) return;
+        if (want >= before && want < before + mine) {
+            for (int64_t i = b0;; ++i) {
+                request_lens(a, i, tok0, qlen, seq);
+                const int64_t n = ((int64_t)qlen * a.G + rows - 1) / rows;
+                if (want < before + n) {
+                    scratch[0] = i;
+                    scratch[1] = n - 1 - (want - before);
+                    break;
+                }
+                before += n;
+            }
+        }
+        __syncthreads();
+        b = scratch[0];
+        tile = (int)scratch[1];
     }
-    __syncthreads();
-    const int64_t b = scratch[0];
-    const int tile = (int)scratch[1];
+    b = __builtin_amdgcn_readfirstlane((int)b);
+    tile = __builtin_amdgcn_readfirstlane(tile);
     __syncthreads();
     build_table(tab, a.codebook, a.Hkv, h, tid, kAttnThreads);
     Rows rw;
@@ -654,7 +724,7 @@ void k_kv4_attn_whole(AttnArgs a) {
         float top = kNoMax;
 #pragma unroll
         for (int w = 0; w < W; ++w) top = fmaxf(top, ml[(t * 16 + c) * W + w].x);
-        const float f = __builtin_amdgcn_exp2f(wv.m[t] - top) / wv.vg;
+        const float f = __builtin_amdgcn_exp2f(wv.m[t] - top);
 #pragma unroll
         for (int p = 0; p < D / 16; ++p) {
             const int e = p / (D / 64), k = p % (D / 64);
@@ -719,14 +789,13 @@ __device__ inline void store_part(const AttnArgs& a, const Wave<D, DT, NT>& wv, 
         l += __shfl_xor(l, 32);
         if (t * 16 + c >= rw.n) continue;
         const int64_t row = part * a.part_rows + t * 16 + c;
-        const float f = 1.f / wv.vg;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
             for (int k = 0; k < D / 64; ++k) {
                 floatx4 x;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = wv.o[t][4 * k + j][e] * f;
+                for (int j = 0; j < 4; ++j) x[j] = wv.o[t][4 * k + j][e];
                 *reinterpret_cast<floatx4*>(a.part_o + row * D + (4 * g + e) * (D / 16) + 4 * k) = x;
             }
         if (g == 0) *reinterpret_cast<float2*>(a.part_ml + row * 2) = make_float2(wv.m[t], l);
@@ -915,7 +984,7 @@ hipError_t attn_rows(const AttnArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
     constexpr int rows = 16 * NT * kAttnWaves;
     const int64_t tiles = (a.T * a.G + rows - 1) / rows + a.B;
-    kern<<<dim3((unsigned)tiles, (unsigned)a.Hkv), dim3(kAttnThreads), kTabBytes, s>>>(a);
+    kern<<<dim3((unsigned)(tiles * a.Hkv)), dim3(kAttnThreads), kTabBytes, s>>>(a);
     return hipGetLastError();
 }
 
