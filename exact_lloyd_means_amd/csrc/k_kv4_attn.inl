@@ -170,19 +170,41 @@ __device__ inline float max_groups(float x) {  // over the four lanes of a query
     return fmaxf(x, __shfl_xor(x, 32));
 }
 
+// Where a lane reads a block: its first codes of k and v, its scales.
+struct Source {
+    const uint8_t *k, *v;
+    const uint16_t *ks, *vs;
+    bool there;
+};
+
 // The codes and scales of one block, as one lane reads them.
 template <int D>
 struct Block {
     uintx4 k[D / 64], v[D / 64], ks, vs;
     bool there;
+
+    __device__ inline void load_k(const Source& s) {
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) k[i] = *reinterpret_cast<const uintx4*>(s.k + 1024 * i);
+        ks = *reinterpret_cast<const uintx4*>(s.ks);
+    }
+    __device__ inline void load_v(const Source& s) {
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) v[i] = *reinterpret_cast<const uintx4*>(s.v + 1024 * i);
+        vs = *reinterpret_cast<const uintx4*>(s.vs);
+        there = s.there;
+    }
 };
 
 #ifndef AHEAD1
 #define AHEAD1 1
 #endif
+#ifndef AHEAD3
+#define AHEAD3 1
+#endif
 // Lookups run this many products ahead of the matrix instructions.
 template <int NT>
-constexpr int kAhead = NT == 1 ? AHEAD1 : 1;
+constexpr int kAhead = NT == 1 ? AHEAD1 : AHEAD3;
 
 template <int D, int DT, int NT>
 struct Wave {
@@ -262,8 +284,9 @@ struct Wave {
         }
     }
 
-    // One block; `at` is its first position.
-    __device__ inline void step(const Block<D>& blk, int at, uint32_t lane4, int g) {
+    // One block; `at` is its first position.  The next block's k and v are
+    // loaded into the same registers as soon as this one's are done with.
+    __device__ inline void step(Block<D>& blk, const Source& next, int at, uint32_t lane4, int g) {
         // scores
         floatx4 s[2][NT];
 #pragma unroll
@@ -346,6 +369,7 @@ struct Wave {
 #pragma unroll
             for (int j = 1; j < 8; ++j) top[t] = fmaxf(top[t], s[j >> 2][t][j & 3]);
         }
+        blk.load_k(next);
         // raise the maxima by more than kSlack, keep v's scales below 2^6 units
         float big = vs[0];
 #pragma unroll
@@ -413,39 +437,35 @@ struct Wave {
                     o[t][8 * half + i] = mfma(x[i % (F + 1)], w[t], o[t][8 * half + i]);
             }
         }
+        blk.load_v(next);
     }
 };
 
-// Blocks first, first + stride, ... below end (at least one) of a request, through a ring of R
-// blocks in registers: a block's codes are loaded R steps ahead, into the
-// registers of the one just done, and its page one step before that.  The
-// first loads are issued by begin(), ahead of other work.
-template <int R, int D>
+// Blocks first, first + stride, ... below end (at least one) of a request.
+// begin() issues the first loads, ahead of other work; a block's page is
+// looked up a step before its codes are loaded.
+template <int D>
 struct Walk {
     const int32_t* table;  // the request's row
     int h, first, end, stride, page, in;
-    Block<D> ring[R];
+    Block<D> blk;
 
-    __device__ inline void ahead(const AttnArgs& a, int blk) {
-        blk = blk < end ? blk : end - 1;
-        const uint32_t pg = a.bpp == 1 ? (uint32_t)blk
-                                       : (uint32_t)(((uint64_t)(uint32_t)blk * a.bpp_magic) >> 32);
-        in = blk - (int)(pg * a.bpp);
+    __device__ inline void ahead(const AttnArgs& a, int b) {
+        b = b < end ? b : end - 1;
+        const uint32_t pg = a.bpp == 1 ? (uint32_t)b
+                                       : (uint32_t)(((uint64_t)(uint32_t)b * a.bpp_magic) >> 32);
+        in = b - (int)(pg * a.bpp);
         page = table[pg];
     }
-    __device__ inline void load(const AttnArgs& a, int lane, Block<D>& b) {
-        b.there = page >= 0 && page < a.pages;
-        const int64_t at = ((int64_t)(b.there ? page : 0) * a.Hkv + h) * 2;
-        const uint8_t* k = a.codes + (at * a.bpp + in) * (16 * D) + lane * 16;
-        const uint8_t* v = k + (int64_t)a.bpp * (16 * D);
-        const uint16_t* s = a.scales + at * a.page_size + in * kKvBlock + 8 * (lane >> 4);
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-            b.k[i] = *reinterpret_cast<const uintx4*>(k + 1024 * i);
-            b.v[i] = *reinterpret_cast<const uintx4*>(v + 1024 * i);
-        }
-        b.ks = *reinterpret_cast<const uintx4*>(s);
-        b.vs = *reinterpret_cast<const uintx4*>(s + a.page_size);
+    __device__ inline Source source(const AttnArgs& a, int lane) const {
+        Source s;
+        s.there = page >= 0 && page < a.pages;
+        const int64_t at = ((int64_t)(s.there ? page : 0) * a.Hkv + h) * 2;
+        s.k = a.codes + (at * a.bpp + in) * (16 * D) + lane * 16;
+        s.v = s.k + (int64_t)a.bpp * (16 * D);
+        s.ks = a.scales + at * a.page_size + in * kKvBlock + 8 * (lane >> 4);
+        s.vs = s.ks + a.page_size;
+        return s;
     }
     __device__ inline void begin(const AttnArgs& a, const int32_t* row, int head, int lo, int hi,
                                  int by, int lane) {
@@ -455,25 +475,19 @@ struct Walk {
         end = hi;
         stride = by;
         ahead(a, first);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            load(a, lane, ring[r]);
-            ahead(a, first + (r + 1) * stride);
-        }
+        const Source s = source(a, lane);
+        blk.load_k(s);
+        blk.load_v(s);
+        ahead(a, first + stride);
     }
     template <int DT, int NT>
     __device__ inline void run(const AttnArgs& a, Wave<D, DT, NT>& wv, int lane) {
         const uint32_t lane4 = 4 * (lane & 31);
         const int g = lane >> 4;
-        for (int b = first;;) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                wv.step(ring[r], b * kKvBlock, lane4, g);
-                b += stride;
-                if (b >= end) return;
-                load(a, lane, ring[r]);
-                ahead(a, b + R * stride);
-            }
+        for (int b = first; b < end; b += stride) {
+            const Source next = source(a, lane);
+            ahead(a, b + 2 * stride);
+            wv.step(blk, next, b * kKvBlock, lane4, g);
         }
     }
 };
@@ -651,7 +665,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_attn_rows(AttnArgs a) {
     const int64_t left = (int64_t)rw.qlen * a.G - rw.r0;
     rw.n = left < 0 ? 0 : left > 16 * NT ? 16 * NT : (int)left;
     const Span sp = tile_span(a, rw.qlen, rw.seq, rw.r0, rw.n);
-    Walk<1, D> wk;
+    Walk<D> wk;
     if (sp.hi > sp.lo) wk.begin(a, a.table + b * a.max_pages, h, sp.lo, sp.hi, 1, lane);
     Wave<D, DT, NT> wv;
     wv.load(a, rw, h, lane);
@@ -702,7 +716,7 @@ void k_kv4_attn_whole(AttnArgs a) {
     const Span sp = split_span<NT>(a, b, rt, rw);
     if (rw.n <= 0) return;
     const bool some = sp.lo + wave < sp.hi;
-    Walk<1, D> wk;
+    Walk<D> wk;
     if (some) wk.begin(a, a.table + b * a.max_pages, h, sp.lo + wave, sp.hi, W, lane);
     build_table(tab, a.codebook, a.Hkv, h, tid, kThreads);
     Wave<D, DT, NT> wv;
@@ -760,13 +774,6 @@ void k_kv4_attn_whole(AttnArgs a) {
 
 // ---- split form: shares of the keys, a wave each ----------------------------------
 
-#ifndef RING1
-#define RING1 1
-#endif
-// Blocks in flight per wave.
-template <int D, int NT>
-constexpr int kSplitRing = NT == 1 && D <= 128 ? RING1 : 1;
-
 // Blocks a wave takes of `total`: an equal share of at least kMinShare, so
 // that the results of a share do not outweigh its codes.
 #ifndef MINSHARE
@@ -811,7 +818,7 @@ __device__ inline void store_part(const AttnArgs& a, const Wave<D, DT, NT>& wv, 
 template <int D, int DT, int NT>
 __global__ __launch_bounds__((64 * kSplitWaves<D, NT>), (kSplitWaves<D, NT> / 2))
 void k_kv4_attn_split(AttnArgs a) {
-    constexpr int W = kSplitWaves<D, NT>, kThreads = 64 * W, R = kSplitRing<D, NT>;
+    constexpr int W = kSplitWaves<D, NT>, kThreads = 64 * W;
     extern __shared__ uint32_t tab[];
     int64_t* scratch = reinterpret_cast<int64_t*>(tab + kTabBytes / 4);
     struct Start {  // where a share begins
@@ -871,7 +878,7 @@ void k_kv4_attn_split(AttnArgs a) {
         const int all = sp.hi - sp.lo;
         if (all > 0) {
             const int take = all - skip < left ? all - skip : (int)left;
-            Walk<R, D> wk;
+            Walk<D> wk;
             wk.begin(a, a.table + b * a.max_pages, h, sp.lo + skip, sp.lo + skip + take, 1, lane);
             Wave<D, DT, NT> wv;
             wv.load(a, rw, h, lane);
