@@ -165,6 +165,36 @@ __device__ inline void transpose4(const uint32_t (&x)[4], uint32_t (&y)[4]) {
                  __builtin_amdgcn_perm(o1, o0, 0x07060302u), y[2], y[3]);
 }
 
+// Maxima that skip the quieting of NaN operands that fmaxf comes with; a NaN
+// loses to a number.
+__device__ inline float max2(float x, float y) {
+    float r;
+    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
+    return r;
+}
+__device__ inline float max3(float x, float y, float z) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+    return r;
+}
+
+typedef unsigned short ushortx2 __attribute__((ext_vector_type(2)));
+__device__ inline uint32_t max_u16(uint32_t x, uint32_t y) {  // of both halves
+    return __builtin_bit_cast(uint32_t,
+                              __builtin_elementwise_max(__builtin_bit_cast(ushortx2, x),
+                                                        __builtin_bit_cast(ushortx2, y)));
+}
+// 2^e as bits of the cache dtype in both halves, at most infinity's.
+template <int DT>
+__device__ inline uint32_t pow2_bits(int e) {
+    uint32_t b;
+    if constexpr (DT == FK_BF16) b = (uint32_t)(e + 127) << 7;
+    else b = e < -14 ? 1u << (e + 24) : (uint32_t)(e + 15) << 10;
+    const uint32_t inf = DT == FK_BF16 ? 0x7f80 : 0x7c00;
+    b = b < inf ? b : inf;
+    return b | b << 16;
+}
+
 __device__ inline float max_groups(float x) {  // over the four lanes of a query row
     x = fmaxf(x, __shfl_xor(x, 16));
     return fmaxf(x, __shfl_xor(x, 32));
@@ -215,7 +245,7 @@ struct Wave {
     floatx4 o[NT][kDb];
     float m[NT], l[NT], qs[NT];
     int lo[NT], hi[NT];  // positions the lane's query row sees
-    float limit;  // 2^6 units
+    uint32_t limit;  // 2^6 units, bits of the cache dtype in both halves
     float slack;  // kSlack less log2 of the v scales' unit, which m contains
     int inner_lo, inner_hi;  // positions every row of the wave sees
 
@@ -273,7 +303,7 @@ struct Wave {
             for (int i = 0; i < kDb; ++i) o[t][i] = floatx4{0, 0, 0, 0};
         }
         slack = kSlack;
-        limit = 0.f;  // the first scale sets the unit
+        limit = 0;  // the first scale sets the unit
         // bounds grow with the row, so the first and last rows tell
         if (rw.n > 0) {
             int x;
@@ -315,15 +345,14 @@ struct Wave {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) s[u][t] = mfma(x[c % (F + 1)][u], q[t][c], s[u][t]);
         }
-        float ks[8], vs[8];
+        half8 w[NT];
+        float ks[8], vs[8], top[NT];
+        const uintx4 vw = blk.vs;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t kw = blk.ks[j >> 1], vw = blk.vs[j >> 1];
-            ks[j] = kv_f32<DT>(j & 1 ? kw >> 16 : kw & 0xffff);
-            vs[j] = kv_f32<DT>(j & 1 ? vw >> 16 : vw & 0xffff);
+            ks[j] = kv_f32<DT>(j & 1 ? blk.ks[j >> 1] >> 16 : blk.ks[j >> 1] & 0xffff);
+            vs[j] = kv_f32<DT>(j & 1 ? vw[j >> 1] >> 16 : vw[j >> 1] & 0xffff);
         }
-        half8 w[NT];
-        float top[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -333,17 +362,21 @@ struct Wave {
             // sees may be anything.
             asm volatile("");  // keeps this a branch: as selects it would run for every block
             const int p0 = at + 8 * g;
+            uint32_t seen = 0;  // bit j: some row of this lane sees token j
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const uint32_t span = blk.there ? hi[t] - lo[t] : 0, from = p0 - lo[t];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const bool sees = from + j < span;
+                    seen |= sees ? 1u << j : 0u;
+                    s[j >> 2][t][j & 3] = sees ? s[j >> 2][t][j & 3] : -INFINITY;
+                }
+            }
             bool nan = false;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                bool any = false;
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const bool sees = blk.there && p0 + j >= lo[t] && p0 + j < hi[t];
-                    any |= sees;
-                    if (!sees) s[j >> 2][t][j & 3] = -INFINITY;
-                }
-                if (!any) vs[j] = 0.f;
+                vs[j] = seen >> j & 1 ? vs[j] : 0.f;
                 nan |= vs[j] != vs[j];
             }
             if (__any(nan)) {
@@ -365,28 +398,30 @@ struct Wave {
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            top[t] = s[0][t][0];
-#pragma unroll
-            for (int j = 1; j < 8; ++j) top[t] = fmaxf(top[t], s[j >> 2][t][j & 3]);
+            float x = max3(s[0][t][0], s[0][t][1], s[0][t][2]);
+            x = max3(x, s[0][t][3], s[1][t][0]);
+            x = max3(x, s[1][t][1], s[1][t][2]);
+            top[t] = max2(x, s[1][t][3]);
         }
         blk.load_k(next);
         // raise the maxima by more than kSlack, keep v's scales below 2^6 units
-        float big = vs[0];
-#pragma unroll
-        for (int j = 1; j < 8; ++j) big = fmaxf(big, vs[j]);
-        bool raise = big > limit;
+        const uint32_t bits = max_u16(max_u16(vw[0], vw[1]), max_u16(vw[2], vw[3]));
+        bool raise = max_u16(bits, limit) != limit;
 #pragma unroll
         for (int t = 0; t < NT; ++t) raise |= fmaf(top[t], qs[t], -m[t]) > slack;
         if (__any(raise)) {
+            float big = vs[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) big = fmaxf(big, vs[j]);
             big = max_groups(big);
             // log2 of the unit: of the power of two below the largest scale,
             // down to 2^-96 (l holds its inverse)
             const float old = kSlack - slack;
             float unit = old;
-            if (big > limit) {
-                const int e = (int)(__builtin_bit_cast(uint32_t, big) >> 23 & 0xff) - 127;
+            const int e = (int)(__builtin_bit_cast(uint32_t, big) >> 23 & 0xff) - 127;
+            if (big > 0.f && (limit == 0 || (float)(e - 6) >= old)) {
                 unit = (float)(e < -96 ? -96 : e);
-                limit = ldexpf(64.f, (int)unit);
+                limit = pow2_bits<DT>((int)unit + 6);
                 slack = kSlack - unit;
             }
 #pragma unroll
@@ -459,12 +494,15 @@ struct Walk {
     }
     __device__ inline Source source(const AttnArgs& a, int lane) const {
         Source s;
-        s.there = page >= 0 && page < a.pages;
+        s.there = (uint32_t)page < (uint32_t)a.pages;
         const int64_t at = ((int64_t)(s.there ? page : 0) * a.Hkv + h) * 2;
-        s.k = a.codes + (at * a.bpp + in) * (16 * D) + lane * 16;
-        s.v = s.k + (int64_t)a.bpp * (16 * D);
-        s.ks = a.scales + at * a.page_size + in * kKvBlock + 8 * (lane >> 4);
-        s.vs = s.ks + a.page_size;
+        // uniform offsets, then the lane's
+        const int64_t code = (at * a.bpp + in) * (16 * D);
+        const int64_t row = at * a.page_size + in * kKvBlock;
+        s.k = a.codes + code + lane * 16;
+        s.v = a.codes + (code + (int64_t)a.bpp * (16 * D)) + lane * 16;
+        s.ks = a.scales + row + 8 * (lane >> 4);
+        s.vs = a.scales + (row + a.page_size) + 8 * (lane >> 4);
         return s;
     }
     __device__ inline void begin(const AttnArgs& a, const int32_t* row, int head, int lo, int hi,
