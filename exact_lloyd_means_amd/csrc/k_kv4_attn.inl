@@ -48,8 +48,8 @@ typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
 
 struct Rows {       // the query rows of a tile within their request
     int qlen, seq;  // of the request
+    int tok0;       // its first query token
     int r0, n;      // first row, number of rows
-    int64_t tok0;   // first query token of the request
 };
 
 // Blocks [lo, hi) that some row of the tile sees.
@@ -57,35 +57,41 @@ struct Span {
     int lo, hi;
 };
 
-__device__ inline void request_lens(const AttnArgs& a, int64_t b, int64_t& tok0, int& qlen,
-                                    int& seq) {
-    int64_t c0 = a.cu[b], c1 = a.cu[b + 1];
-    c0 = c0 < 0 ? 0 : c0 > a.T ? a.T : c0;
-    c1 = c1 < c0 ? c0 : c1 > a.T ? a.T : c1;
-    tok0 = c0;
-    qlen = (int)(c1 - c0);
+// x / y for x < 2^24 with magic = ceil(2^32 / y), y <= 256.
+__device__ inline int divide(int x, uint32_t y, uint32_t magic) {
+    return y == 1 ? x : (int)(((uint64_t)(uint32_t)x * magic) >> 32);
+}
+
+__device__ inline void request_lens(const AttnArgs& a, int b, Rows& rw) {
+    const int T = (int)a.T;
+    int c0 = a.cu[b], c1 = a.cu[b + 1];
     const int s = a.seq[b];
-    seq = s < 0 ? 0 : s;
+    c0 = c0 < 0 ? 0 : c0 > T ? T : c0;
+    c1 = c1 < c0 ? c0 : c1 > T ? T : c1;
+    rw.tok0 = c0;
+    rw.qlen = c1 - c0;
+    rw.seq = s < 0 ? 0 : s;
 }
 
 // First and one past the last position that query token i sees.
-__device__ inline void bounds(const AttnArgs& a, int qlen, int seq, int64_t cap, int i, int& lo,
-                              int& hi) {
-    const int64_t pos = (int64_t)seq - qlen + i;
-    int64_t h = a.causal ? pos + 1 : seq, l = a.window > 0 ? pos - a.window + 1 : 0;
-    h = h > seq ? seq : h;
-    h = h > cap ? cap : h;
-    l = l < 0 ? 0 : l;
-    hi = h < 0 ? 0 : (int)h;
-    lo = l > hi ? hi : (int)l;
+__device__ inline void bounds(const AttnArgs& a, const Rows& rw, int i, int& lo, int& hi) {
+    const int pos = rw.seq - rw.qlen + i;
+    hi = a.causal ? pos + 1 : rw.seq;
+    hi = hi > a.cap ? a.cap : hi;
+    hi = hi < 0 ? 0 : hi;
+    lo = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+    lo = lo > hi ? hi : lo;
 }
 
-__device__ inline Span tile_span(const AttnArgs& a, int qlen, int seq, int r0, int n) {
-    if (n <= 0) return {0, 0};
-    const int64_t cap = a.max_pages * a.page_size;
+// Rows r0 .. of the request in tiles of `rows`, and the blocks they see.
+__device__ inline Span tile_rows(const AttnArgs& a, Rows& rw, int r0, int rows) {
+    rw.r0 = r0;
+    const int left = rw.qlen * a.G - r0;
+    rw.n = left < 0 ? 0 : left > rows ? rows : left;
+    if (rw.n <= 0) return {0, 0};
     int lo, hi, t0, t1;
-    bounds(a, qlen, seq, cap, r0 / a.G, lo, t0);
-    bounds(a, qlen, seq, cap, (r0 + n - 1) / a.G, t1, hi);
+    bounds(a, rw, divide(r0, a.G, a.G_magic), lo, t0);
+    bounds(a, rw, divide(r0 + rw.n - 1, a.G, a.G_magic), t1, hi);
     if (hi <= lo) return {0, 0};
     return {lo / kKvBlock, (hi + kKvBlock - 1) / kKvBlock};
 }
@@ -107,7 +113,7 @@ __device__ inline half8 lookup(uint32_t codes, uint32_t lane4) {
     for (int i = 0; i < 4; ++i) {
         // bytes of the address: lane4's byte 0, byte i of the codes, zeros
         const uint32_t at = __builtin_amdgcn_perm(codes, lane4, 0x0c0c0000u | (4u + i) << 8);
-        y[i] = *((LdsWord)at + (V ? 32 : 0));
+        y[i] = *((LdsWord)(uintptr_t)at + (V ? 32 : 0));
     }
     return __builtin_bit_cast(half8, y);
 }
@@ -195,6 +201,25 @@ __device__ inline uint32_t pow2_bits(int e) {
     return b | b << 16;
 }
 
+// The halves of a dword of scales as fp32.  For fp16 by instruction: left to
+// itself the compiler folds the conversions into mixed-precision products and
+// pays with registers that the accumulators need.
+template <int DT>
+__device__ inline float low_f32(uint32_t x) {
+    if constexpr (DT == FK_BF16) return __builtin_bit_cast(float, x << 16);
+    float r;
+    asm("v_cvt_f32_f16_e32 %0, %1" : "=v"(r) : "v"(x));
+    return r;
+}
+template <int DT>
+__device__ inline float high_f32(uint32_t x) {
+    if constexpr (DT == FK_BF16) return __builtin_bit_cast(float, x & 0xffff0000u);
+    float r;
+    asm("v_cvt_f32_f16_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:WORD_1"
+        : "=v"(r) : "v"(x));
+    return r;
+}
+
 __device__ inline float max_groups(float x) {  // over the four lanes of a query row
     x = fmaxf(x, __shfl_xor(x, 16));
     return fmaxf(x, __shfl_xor(x, 32));
@@ -249,41 +274,45 @@ struct Wave {
     float slack;  // kSlack less log2 of the v scales' unit, which m contains
     int inner_lo, inner_hi;  // positions every row of the wave sees
 
-    // Query rows r0 .. r0 + n - 1 of the request (n may be <= 0).
-    __device__ inline void load(const AttnArgs& a, const Rows& rw, int h, int lane) {
+    // The tile's query rows as they are (n may be <= 0), a lane's quarter of
+    // a row each.  Separate from init() so that the first codes can be on
+    // their way before a row is waited for.
+    using Raw = uint32_t[NT][D / 8];
+    __device__ static inline void fetch(const AttnArgs& a, const Rows& rw, int h, int lane, Raw& x) {
         const int g = lane >> 4, c = lane & 15;
-        const int64_t cap = a.max_pages * a.page_size;
-        inner_lo = 0;
-        inner_hi = 0x7fffffff;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const int r = rw.r0 + t * 16 + c;
-            const bool on = t * 16 + c < rw.n;
-            const int i = on ? r / a.G : 0, head = h * a.G + (on ? r - i * a.G : 0);
-            uint32_t x[D / 8];
 #pragma unroll
-            for (int w = 0; w < D / 8; ++w) x[w] = 0;
-            lo[t] = hi[t] = 0;
-            if (on) {
-                const uint16_t* p = a.q + (rw.tok0 + i) * a.q_token + head * a.q_head + g * (D / 4);
-                if (a.q_vec) {
+            for (int w = 0; w < D / 8; ++w) x[t][w] = 0;
+            if (t * 16 + c >= rw.n) continue;
+            const int r = rw.r0 + t * 16 + c, i = divide(r, a.G, a.G_magic);
+            const uint16_t* p = a.q + (int64_t)(rw.tok0 + i) * a.q_token +
+                                (int64_t)(h * a.G + r - i * a.G) * a.q_head + g * (D / 4);
+            if (a.q_vec) {
 #pragma unroll
-                    for (int w = 0; w < D / 32; ++w) {
-                        const uintx4 y = reinterpret_cast<const uintx4*>(p)[w];
+                for (int w = 0; w < D / 32; ++w) {
+                    const uintx4 y = reinterpret_cast<const uintx4*>(p)[w];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[4 * w + e] = y[e];
-                    }
-                } else {
-#pragma unroll
-                    for (int w = 0; w < D / 8; ++w) x[w] = p[2 * w] | (uint32_t)p[2 * w + 1] << 16;
+                    for (int e = 0; e < 4; ++e) x[t][4 * w + e] = y[e];
                 }
-                bounds(a, rw.qlen, rw.seq, cap, i, lo[t], hi[t]);
+            } else {
+#pragma unroll
+                for (int w = 0; w < D / 8; ++w) x[t][w] = p[2 * w] | (uint32_t)p[2 * w + 1] << 16;
             }
+        }
+    }
+    __device__ inline void init(const AttnArgs& a, const Rows& rw, const Raw& x, int lane) {
+        const int c = lane & 15;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            lo[t] = hi[t] = 0;
+            if (t * 16 + c < rw.n)
+                bounds(a, rw, divide(rw.r0 + t * 16 + c, a.G, a.G_magic), lo[t], hi[t]);
             // the row's largest magnitude, and the power of two below it
             float big = 0.f;
 #pragma unroll
             for (int w = 0; w < D / 8; ++w)
-                big = fmaxf(big, fmaxf(fabsf(kv_f32<DT>(x[w] & 0xffff)), fabsf(kv_f32<DT>(x[w] >> 16))));
+                big = max3(big, fabsf(kv_f32<DT>(x[t][w] & 0xffff)), fabsf(kv_f32<DT>(x[t][w] >> 16)));
             big = max_groups(big);
             int e = (int)(__builtin_bit_cast(uint32_t, big) >> 23 & 0xff);
             e = big == 0.f || e == 255 ? 0 : (e < 1 ? 1 : e) - 127;
@@ -293,7 +322,7 @@ struct Wave {
             for (int s = 0; s < kKs; ++s)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t w = x[4 * s + j];
+                    const uint32_t w = x[t][4 * s + j];
                     q[t][s][2 * j] = (_Float16)(kv_f32<DT>(w & 0xffff) * f);
                     q[t][s][2 * j + 1] = (_Float16)(kv_f32<DT>(w >> 16) * f);
                 }
@@ -305,12 +334,12 @@ struct Wave {
         slack = kSlack;
         limit = 0;  // the first scale sets the unit
         // bounds grow with the row, so the first and last rows tell
+        inner_lo = 0;
+        inner_hi = 0x7fffffff;
         if (rw.n > 0) {
-            int x;
-            const int i0 = rw.r0 / a.G, i1 = (rw.r0 + rw.n - 1) / a.G;
-            bounds(a, rw.qlen, rw.seq, cap, i0, x, inner_hi);
-            int y;
-            bounds(a, rw.qlen, rw.seq, cap, i1, inner_lo, y);
+            int x0, x1;
+            bounds(a, rw, divide(rw.r0, a.G, a.G_magic), x0, inner_hi);
+            bounds(a, rw, divide(rw.r0 + rw.n - 1, a.G, a.G_magic), inner_lo, x1);
         }
     }
 
@@ -350,8 +379,8 @@ struct Wave {
         const uintx4 vw = blk.vs;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            ks[j] = kv_f32<DT>(j & 1 ? blk.ks[j >> 1] >> 16 : blk.ks[j >> 1] & 0xffff);
-            vs[j] = kv_f32<DT>(j & 1 ? vw[j >> 1] >> 16 : vw[j >> 1] & 0xffff);
+            ks[j] = j & 1 ? high_f32<DT>(blk.ks[j >> 1]) : low_f32<DT>(blk.ks[j >> 1]);
+            vs[j] = j & 1 ? high_f32<DT>(vw[j >> 1]) : low_f32<DT>(vw[j >> 1]);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -487,9 +516,8 @@ struct Walk {
 
     __device__ inline void ahead(const AttnArgs& a, int b) {
         b = b < end ? b : end - 1;
-        const uint32_t pg = a.bpp == 1 ? (uint32_t)b
-                                       : (uint32_t)(((uint64_t)(uint32_t)b * a.bpp_magic) >> 32);
-        in = b - (int)(pg * a.bpp);
+        const int pg = a.bpp == 1 ? b : (int)(((uint64_t)(uint32_t)b * a.bpp_magic) >> 32);
+        in = b - pg * (int)a.bpp;
         page = table[pg];
     }
     __device__ inline Source source(const AttnArgs& a, int lane) const {
@@ -530,13 +558,13 @@ struct Walk {
     }
 };
 
-// Inclusive scan over the threads of W waves; scratch of W int64.
+// Inclusive scan over the threads of W waves; scratch of W ints.
 template <int W>
-__device__ inline int64_t group_scan(int64_t x, int64_t* scratch, int64_t& total, int tid) {
+__device__ inline int group_scan(int x, int* scratch, int& total, int tid) {
     const int lane = tid & 63, wave = tid >> 6;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        const int64_t y = __shfl_up(x, o);
+        const int y = __shfl_up(x, o);
         if (lane >= o) x += y;
     }
     if (lane == 63) scratch[wave] = x;
@@ -544,11 +572,10 @@ __device__ inline int64_t group_scan(int64_t x, int64_t* scratch, int64_t& total
     total = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-        const int64_t y = scratch[w];
+        const int y = scratch[w];
         if (w < wave) x += y;
         total += y;
     }
-    __syncthreads();
     return x;
 }
 
@@ -571,7 +598,8 @@ __device__ inline void finish(const AttnArgs& a, const Wave<D, DT, NT>& wv, cons
         l += __shfl_xor(l, 16);
         l += __shfl_xor(l, 32);
         if (t * 16 + c >= rw.n) continue;
-        const int r = rw.r0 + t * 16 + c, i = r / a.G, head = h * a.G + r - i * a.G;
+        const int r = rw.r0 + t * 16 + c, i = divide(r, a.G, a.G_magic);
+        const int head = h * a.G + r - i * a.G;
         const int64_t tok = rw.tok0 + i;
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
@@ -610,21 +638,19 @@ __global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_attn_rows(AttnArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     constexpr int rows = 16 * NT * kAttnWaves;
     const int want = blockIdx.x / (uint32_t)a.Hkv, h = blockIdx.x - want * a.Hkv;
-    int64_t b = 0;
-    int tile = 0;
+    int b = 0, tile = 0;
     if (a.B <= kOrderB) {
         int2* req = reinterpret_cast<int2*>(tab);  // (o_b, n_b)
         int* most = reinterpret_cast<int*>(req + kOrderB);
         if (tid == 0) most[0] = most[1] = 0;
         __syncthreads();
         if (tid < a.B) {
-            int64_t tok0;
-            int qlen, seq;
-            request_lens(a, tid, tok0, qlen, seq);
-            const int n = (int)(((int64_t)qlen * a.G + rows - 1) / rows);
-            int64_t before = a.causal ? (int64_t)seq - qlen : seq;
-            before = before < 0 ? 0 : before * a.G / rows;
-            const int o = before > (1 << 29) ? 1 << 29 : (int)before;
+            Rows rw;
+            request_lens(a, tid, rw);
+            const int n = (rw.qlen * a.G + rows - 1) / rows;
+            const int before = a.causal ? rw.seq - rw.qlen : rw.seq;
+            const int64_t level = before < 0 ? 0 : (int64_t)before * a.G / rows;
+            const int o = level > 1 << 29 ? 1 << 29 : (int)level;
             req[tid] = make_int2(o, n);
             atomicMax(&most[0], o + n);
             atomicAdd(&most[1], n);
@@ -666,47 +692,46 @@ __global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_attn_rows(AttnArgs a) {
             rank -= k;
         }
     } else {
-        int64_t* scratch = reinterpret_cast<int64_t*>(tab);
-        const int per = (a.B + kAttnThreads - 1) / kAttnThreads;
-        const int64_t b0 = (int64_t)tid * per;
-        int64_t mine = 0, total, tok0;
-        int qlen, seq;
-        for (int64_t i = b0; i < b0 + per && i < a.B; ++i) {
-            request_lens(a, i, tok0, qlen, seq);
-            mine += ((int64_t)qlen * a.G + rows - 1) / rows;
+        int* scratch = reinterpret_cast<int*>(tab);
+        int* found = scratch + kAttnWaves;
+        const int per = (a.B + kAttnThreads - 1) / kAttnThreads, b0 = tid * per;
+        int mine = 0, total;
+        Rows rw;
+        for (int i = b0; i < b0 + per && i < a.B; ++i) {
+            request_lens(a, i, rw);
+            mine += (rw.qlen * a.G + rows - 1) / rows;
         }
-        int64_t before = group_scan<kAttnWaves>(mine, scratch, total, tid) - mine;
+        int before = group_scan<kAttnWaves>(mine, scratch, total, tid) - mine;
         if (want >= total) return;
         if (want >= before && want < before + mine) {
-            for (int64_t i = b0;; ++i) {
-                request_lens(a, i, tok0, qlen, seq);
-                const int64_t n = ((int64_t)qlen * a.G + rows - 1) / rows;
+            for (int i = b0;; ++i) {
+                request_lens(a, i, rw);
+                const int n = (rw.qlen * a.G + rows - 1) / rows;
                 if (want < before + n) {
-                    scratch[0] = i;
-                    scratch[1] = n - 1 - (want - before);
+                    found[0] = i;
+                    found[1] = n - 1 - (want - before);
                     break;
                 }
                 before += n;
             }
         }
         __syncthreads();
-        b = scratch[0];
-        tile = (int)scratch[1];
+        b = found[0];
+        tile = found[1];
     }
-    b = __builtin_amdgcn_readfirstlane((int)b);
+    b = __builtin_amdgcn_readfirstlane(b);
     tile = __builtin_amdgcn_readfirstlane(tile);
     __syncthreads();
-    build_table(tab, a.codebook, a.Hkv, h, tid, kAttnThreads);
     Rows rw;
-    request_lens(a, b, rw.tok0, rw.qlen, rw.seq);
-    rw.r0 = tile * rows + wave * 16 * NT;
-    const int64_t left = (int64_t)rw.qlen * a.G - rw.r0;
-    rw.n = left < 0 ? 0 : left > 16 * NT ? 16 * NT : (int)left;
-    const Span sp = tile_span(a, rw.qlen, rw.seq, rw.r0, rw.n);
+    request_lens(a, b, rw);
+    const Span sp = tile_rows(a, rw, tile * rows + wave * 16 * NT, 16 * NT);
+    typename Wave<D, DT, NT>::Raw raw;
+    Wave<D, DT, NT>::fetch(a, rw, h, lane, raw);
     Walk<D> wk;
     if (sp.hi > sp.lo) wk.begin(a, a.table + b * a.max_pages, h, sp.lo, sp.hi, 1, lane);
+    build_table(tab, a.codebook, a.Hkv, h, tid, kAttnThreads);
     Wave<D, DT, NT> wv;
-    wv.load(a, rw, h, lane);
+    wv.init(a, rw, raw, lane);
     __syncthreads();
     if (sp.hi > sp.lo) wk.run(a, wv, lane);
     finish<D, DT, NT>(a, wv, rw, h, lane);
@@ -714,18 +739,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_attn_rows(AttnArgs a) {
 
 // ---- few query rows: row tiles of requests ----------------------------------------
 
-// Row tile rt of the request whose lengths rw holds, and its visible blocks.
+// Row tile rt of request b, and its visible blocks.
 template <int NT>
-__device__ inline Span split_rows(const AttnArgs& a, int rt, Rows& rw) {
-    rw.r0 = rt * 16 * NT;
-    const int64_t left = (int64_t)rw.qlen * a.G - rw.r0;
-    rw.n = left < 0 ? 0 : left > 16 * NT ? 16 * NT : (int)left;
-    return tile_span(a, rw.qlen, rw.seq, rw.r0, rw.n);
-}
-template <int NT>
-__device__ inline Span split_span(const AttnArgs& a, int64_t b, int rt, Rows& rw) {
-    request_lens(a, b, rw.tok0, rw.qlen, rw.seq);
-    return split_rows<NT>(a, rt, rw);
+__device__ inline Span split_span(const AttnArgs& a, int b, int rt, Rows& rw) {
+    request_lens(a, b, rw);
+    return tile_rows(a, rw, rt * 16 * NT, 16 * NT);
 }
 
 // Waves of a workgroup: with one column block of at most 128 dimensions four
@@ -748,17 +766,19 @@ void k_kv4_attn_whole(AttnArgs a) {
     float2* ml = reinterpret_cast<float2*>(tab + kTabBytes / 4);  // [16 NT][W]
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t b = blockIdx.x;
+    const int b = blockIdx.x;
     const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y - h * a.row_tiles;
     Rows rw;
     const Span sp = split_span<NT>(a, b, rt, rw);
     if (rw.n <= 0) return;
     const bool some = sp.lo + wave < sp.hi;
+    typename Wave<D, DT, NT>::Raw raw;
+    Wave<D, DT, NT>::fetch(a, rw, h, lane, raw);
     Walk<D> wk;
     if (some) wk.begin(a, a.table + b * a.max_pages, h, sp.lo + wave, sp.hi, W, lane);
     build_table(tab, a.codebook, a.Hkv, h, tid, kThreads);
     Wave<D, DT, NT> wv;
-    wv.load(a, rw, h, lane);
+    wv.init(a, rw, raw, lane);
     __syncthreads();
     if (some) wk.run(a, wv, lane);
     const int c = lane & 15;
@@ -798,12 +818,12 @@ void k_kv4_attn_whole(AttnArgs a) {
 #pragma unroll
             for (int w = 0; w < W; ++w)
                 sum += ml[row * W + w].y * __builtin_amdgcn_exp2f(ml[row * W + w].x - most);
-            const int r = rw.r0 + row, q = r / a.G, head = h * a.G + r - q * a.G;
+            const int r = rw.r0 + row, q = divide(r, a.G, a.G_magic), head = h * a.G + r - q * a.G;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             const int d = (4 * ((i >> 4) & 3) + e) * (D / 16) + 4 * k;
             store_out<DT>(a, rw.tok0 + q, head, D, d, x * inv);
             if (a.lse && d == 0)
-                a.lse[(rw.tok0 + q) * a.Hq + head] =
+                a.lse[(int64_t)(rw.tok0 + q) * a.Hq + head] =
                     (most + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
         }
         if (t + 1 < NT) __syncthreads();
@@ -812,14 +832,13 @@ void k_kv4_attn_whole(AttnArgs a) {
 
 // ---- split form: shares of the keys, a wave each ----------------------------------
 
-// Blocks a wave takes of `total`: an equal share of at least kMinShare, so
-// that the results of a share do not outweigh its codes.
-#ifndef MINSHARE
-#define MINSHARE 2
-#endif
-__device__ inline int64_t split_share(int64_t total, int64_t waves) {
-    const int64_t per = (total + waves - 1) / waves;
-    return per < MINSHARE ? MINSHARE : per;
+// Blocks a wave takes of `total`: an equal share; more, up to `least`, where an
+// eighth of the waves is enough for that.
+__device__ inline int split_share(int total, int waves, int least) {
+    const int per = (total + waves - 1) / waves, eighth = (total + waves / 8) / (waves / 8 + 1);
+    const int more = eighth < least ? eighth : least;
+    const int share = per > more ? per : more;
+    return share < 2 ? 2 : share;
 }
 
 // Sums of a share of a request, for the join.
@@ -858,33 +877,31 @@ __global__ __launch_bounds__((64 * kSplitWaves<D, NT>), (kSplitWaves<D, NT> / 2)
 void k_kv4_attn_split(AttnArgs a) {
     constexpr int W = kSplitWaves<D, NT>, kThreads = 64 * W;
     extern __shared__ uint32_t tab[];
-    int64_t* scratch = reinterpret_cast<int64_t*>(tab + kTabBytes / 4);
-    struct Start {  // where a share begins
-        int64_t tok0;
-        int b, skip, qlen, seq;
+    int* scratch = reinterpret_cast<int*>(tab + kTabBytes / 4);
+    struct Start {  // where a share begins: a request, how many of its blocks lie before
+        int b, skip, tok0, qlen, seq;
     };
     Start* start = reinterpret_cast<Start*>(scratch + W);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y - h * a.row_tiles;
-    build_table(tab, a.codebook, a.Hkv, h, tid, kThreads);
-    const int per = (a.B + kThreads - 1) / kThreads;
-    const int b0 = tid * per;
+    const int per = (a.B + kThreads - 1) / kThreads, b0 = tid * per;
     Rows rw;
-    int64_t mine = 0, total;
+    int mine = 0, total;
     Span sp = {0, 0};
     for (int b = b0; b < b0 + per && b < a.B; ++b) {
         sp = split_span<NT>(a, b, rt, rw);
         mine += sp.hi - sp.lo;
     }
-    int64_t at = group_scan<W>(mine, scratch, total, tid) - mine;
-    const int64_t share = split_share(total, (int64_t)a.splits * W);
-    const int64_t first_wave = (int64_t)blockIdx.x * W;
+    build_table(tab, a.codebook, a.Hkv, h, tid, kThreads);
+    int at = group_scan<W>(mine, scratch, total, tid) - mine;
+    const int share = split_share(total, a.splits * W, a.least);
+    const int first_wave = blockIdx.x * W;
     // Where the shares of this workgroup begin, and what the join needs.
     const bool tell = blockIdx.x == 0 && h == 0;
-    const int64_t begin = first_wave * share, stop = begin + W * share;
+    const int64_t begin = (int64_t)first_wave * share, stop = begin + W * share;
     if (tell || (at < stop && at + mine > begin)) {
-        int64_t* prefix = a.prefix + (int64_t)rt * (a.B + 1);
+        int* prefix = a.prefix + (int64_t)rt * (a.B + 1);
         for (int b = b0; b < b0 + per && b < a.B; ++b) {
             if (per > 1) sp = split_span<NT>(a, b, rt, rw);
             const int n = sp.hi - sp.lo;
@@ -893,7 +910,7 @@ void k_kv4_attn_split(AttnArgs a) {
             for (int w = 0; w < W; ++w) {
                 const int64_t from = begin + w * share;
                 if (from >= at && from < at + n)
-                    start[w] = {rw.tok0, b, (int)(from - at), rw.qlen, rw.seq};
+                    start[w] = {b, (int)(from - at), rw.tok0, rw.qlen, rw.seq};
             }
             at += n;
         }
@@ -902,24 +919,26 @@ void k_kv4_attn_split(AttnArgs a) {
     if (begin >= total) return;
     __syncthreads();
 
-    int64_t left = total - (begin + wave * share);  // of the wave's share
-    left = left > share ? share : left;
+    const int64_t over = total - (begin + wave * share);  // blocks from the wave's share on
+    int left = over > share ? share : (int)over;          // of the share
     if (left <= 0) return;
     const int64_t part = ((int64_t)blockIdx.y * a.splits * W + first_wave + wave) * 2;
     int b = __builtin_amdgcn_readfirstlane(start[wave].b);
-    int skip = __builtin_amdgcn_readfirstlane(start[wave].skip);  // blocks of b before the share
-    rw.tok0 = __builtin_amdgcn_readfirstlane((int)start[wave].tok0);
+    int skip = __builtin_amdgcn_readfirstlane(start[wave].skip);
+    rw.tok0 = __builtin_amdgcn_readfirstlane(start[wave].tok0);
     rw.qlen = __builtin_amdgcn_readfirstlane(start[wave].qlen);
     rw.seq = __builtin_amdgcn_readfirstlane(start[wave].seq);
     for (int place = 0;;) {
-        sp = split_rows<NT>(a, rt, rw);
+        sp = tile_rows(a, rw, rt * 16 * NT, 16 * NT);
         const int all = sp.hi - sp.lo;
         if (all > 0) {
-            const int take = all - skip < left ? all - skip : (int)left;
+            const int take = all - skip < left ? all - skip : left;
+            typename Wave<D, DT, NT>::Raw raw;
+            Wave<D, DT, NT>::fetch(a, rw, h, lane, raw);
             Walk<D> wk;
             wk.begin(a, a.table + b * a.max_pages, h, sp.lo + skip, sp.lo + skip + take, 1, lane);
             Wave<D, DT, NT> wv;
-            wv.load(a, rw, h, lane);
+            wv.init(a, rw, raw, lane);
             wk.run(a, wv, lane);
             if (take == all) finish<D, DT, NT>(a, wv, rw, h, lane);
             else store_part<D, DT, NT>(a, wv, rw, part + place, lane);
@@ -928,8 +947,7 @@ void k_kv4_attn_split(AttnArgs a) {
             place = 1;  // the share's first request has place 0, its last place 1
             skip = 0;
         }
-        ++b;
-        request_lens(a, b, rw.tok0, rw.qlen, rw.seq);
+        request_lens(a, ++b, rw);
     }
 }
 
@@ -942,16 +960,15 @@ __global__ __launch_bounds__(kAttnThreads) void k_kv4_attn_join(AttnArgs a) {
     constexpr int kGroups = kAttnThreads / (D / 4);
     __shared__ floatx4 so[kAttnThreads];
     __shared__ float sm[kGroups], sl[kGroups];
-    const int64_t b = blockIdx.x;
+    const int b = blockIdx.x;
     const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y - h * a.row_tiles;
-    const int64_t* prefix = a.prefix + (int64_t)rt * (a.B + 1);
-    const int64_t lo = prefix[b], hi = prefix[b + 1];
-    const int64_t waves = (int64_t)a.splits * kSplitWaves<D, NT>;
-    const int64_t share = split_share(prefix[a.B], waves);
-    const int64_t w0 = lo / share, w1 = hi > lo ? (hi - 1) / share : w0;
-    if (hi > lo && w0 == w1) return;
+    const int* prefix = a.prefix + (int64_t)rt * (a.B + 1);
+    const int lo = prefix[b], hi = prefix[b + 1], total = prefix[a.B];
     Rows rw;
     split_span<NT>(a, b, rt, rw);
+    const int waves = a.splits * kSplitWaves<D, NT>, share = split_share(total, waves, a.least);
+    const int w0 = lo / share, w1 = hi > lo ? (hi - 1) / share : w0;
+    if (hi > lo && w0 == w1) return;
     const int tid = threadIdx.x, grp = tid / (D / 4), d = 4 * (tid % (D / 4));
     const int n = kGroups / a.join_rows, sub = grp % n;  // threads of a row, which of them
     for (int r0 = 0; r0 * (int)gridDim.z < rw.n; r0 += a.join_rows) {
@@ -960,13 +977,13 @@ __global__ __launch_bounds__(kAttnThreads) void k_kv4_attn_join(AttnArgs a) {
         floatx4 o = {0, 0, 0, 0};
         if (hi > lo && row < rw.n) {
             constexpr int kBatch = 4;  // shares loaded at a time
-            for (int64_t w = w0 + sub; w <= w1; w += kBatch * n) {
+            for (int w = w0 + sub; w <= w1; w += kBatch * n) {
                 float2 ml[kBatch];
                 floatx4 y[kBatch];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    const int64_t x = w + i * n <= w1 ? w + i * n : w;
-                    const int64_t part = ((blockIdx.y * waves + x) * 2 +
+                    const int x = w + i * n <= w1 ? w + i * n : w;
+                    const int64_t part = (((int64_t)blockIdx.y * waves + x) * 2 +
                                           (x == w0 && lo != x * share ? 1 : 0)) * a.part_rows + row;
                     ml[i] = *reinterpret_cast<const float2*>(a.part_ml + part * 2);
                     y[i] = *reinterpret_cast<const floatx4*>(a.part_o + part * D + d);
@@ -1009,11 +1026,11 @@ __global__ __launch_bounds__(kAttnThreads) void k_kv4_attn_join(AttnArgs a) {
             __syncthreads();
         }
         if (sub == 0 && row < rw.n) {
-            const int r = rw.r0 + row, i = r / a.G, head = h * a.G + r - i * a.G;
+            const int r = rw.r0 + row, i = divide(r, a.G, a.G_magic), head = h * a.G + r - i * a.G;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             store_out<DT>(a, rw.tok0 + i, head, D, d, o * inv);
             if (a.lse && d == 0)
-                a.lse[(rw.tok0 + i) * a.Hq + head] =
+                a.lse[(int64_t)(rw.tok0 + i) * a.Hq + head] =
                     (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
         }
     }
@@ -1063,13 +1080,11 @@ hipError_t attn_split(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
 template <int D, int DT>
 hipError_t attn_cols(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
     if (!p.split) return attn_rows<D, DT, kRowCols<D>>(a, s);
-    switch (p.col_blocks) {
-        case 1: return attn_split<D, DT, 1>(a, p, s);
-        case 2: return attn_split<D, DT, 2>(a, p, s);
-        default:
-            if constexpr (kRowCols<D> > 2) return attn_split<D, DT, kRowCols<D>>(a, p, s);
-            else return hipErrorInvalidValue;
+    if constexpr (kTileCols<D> > 1) {
+        if (p.col_blocks == 2) return attn_split<D, DT, 2>(a, p, s);
+        if (p.col_blocks == 3) return attn_split<D, DT, 3>(a, p, s);
     }
+    return attn_split<D, DT, 1>(a, p, s);
 }
 
 template <int D>

@@ -21,7 +21,7 @@ AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q,
                         int64_t max_blocks) {
     AttnPlan p{};
     const int64_t G = Hq / Hkv, rows = G * max_q;
-    p.col_blocks = rows <= 16 ? 1 : rows <= 32 ? 2 : row_cols(D);
+    p.col_blocks = (int)((rows + 15) / 16 < tile_cols(D) ? (rows + 15) / 16 : tile_cols(D));
     const int64_t tile = 16 * p.col_blocks;
     const int64_t tiles = (rows + tile - 1) / tile;
     // Waves over rows need no join, but a card full of rows; below that the
@@ -37,14 +37,31 @@ AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q,
     if (p.split && !p.whole) {
         // The join's workgroups, of 1024 / D rows at a time: about eight a CU.
         const int64_t tiles_all = B * Hkv * tiles;
-        int64_t z = 2048 / tiles_all;
+        #ifndef JZ
+#define JZ 2048
+#endif
+        int64_t z = JZ / tiles_all;
         z = z < 1 ? 1 : z > p.rows ? p.rows : z;
         p.join_z = (int)z;
         const int each = (int)((p.rows + z - 1) / z), most = 1024 / D;
         p.join_rows = 1;
         while (p.join_rows < each && p.join_rows < most) p.join_rows *= 2;
-        const int64_t s = kResident / (Hkv * tiles);
-        p.splits = s < 1 ? 1 : (int)s;
+        // Workgroups in whole rounds of the card: the fewest rounds of which
+        // 88 % are full.
+        const int64_t y = Hkv * tiles;
+        double best = 0;
+        for (int rounds = 1; rounds <= 8 && best < 0.88; ++rounds) {
+            const int64_t s = rounds * kResident / y;
+            const double full = (double)(s * y) / (rounds * kResident);
+            if (full > best) {
+                best = full;
+                p.splits = (int)s;
+            }
+        }
+        if (p.splits < 1) p.splits = 1;
+        // A share's results are rows x D fp32, a block's codes and scales 32 D +
+        // 128 bytes: at least a block for every two rows.
+        p.least = p.rows / 2;
         const size_t parts =
             (size_t)Hkv * p.row_tiles * p.splits * 8 * 2 * (size_t)p.rows;
         size_t o = 0;
@@ -53,7 +70,7 @@ AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q,
         p.part_ml = o;
         o = align256(o + parts * 2 * sizeof(float));
         p.prefix = o;
-        o = align256(o + (size_t)p.row_tiles * (size_t)(B + 1) * sizeof(int64_t));
+        o = align256(o + (size_t)p.row_tiles * (size_t)(B + 1) * sizeof(int32_t));
         p.total = o;
     }
     if (p.total < 256) p.total = 256;
@@ -153,8 +170,8 @@ fk_status check_heads(const fk_kv4_cache* c, int64_t T, int32_t q_heads, int32_t
         return fail(FK_EINVAL, "q_heads (%d) must be a multiple of kv_heads (%d)", (int)q_heads,
                     (int)c->kv_heads);
     if (q_heads / c->kv_heads > 256) return fail(FK_EUNSUPPORTED, "q_heads / kv_heads must be <= 256");
-    if (T * (q_heads / c->kv_heads) > (int64_t)1 << 30)
-        return fail(FK_EUNSUPPORTED, "T * q_heads / kv_heads must be <= 2^30");
+    if (T * (q_heads / c->kv_heads) > kMaxTokens)
+        return fail(FK_EUNSUPPORTED, "T * q_heads / kv_heads must be <= 2^24");
     if (max_q < 1) return fail(FK_EINVAL, "max_q must be >= 1");
     return FK_OK;
 }
@@ -278,6 +295,8 @@ fk_status fk_kv4_attention(const fk_kv4_cache* c, const fk_kv4_attn* p, void* ws
     if (p->max_pages < 1) return fail(FK_EINVAL, "max_pages must be >= 1");
     if (p->max_pages > 2147483647 / c->page_size)
         return fail(FK_EUNSUPPORTED, "max_pages * page_size must be <= 2^31 - 1");
+    if (p->max_pages * (c->page_size / kKvBlock) > 2147483647 / p->B)
+        return fail(FK_EUNSUPPORTED, "B * max_pages * page_size must be < 2^36");
     if (!(p->scale > 0.f) || !isfinite(p->scale))
         return fail(FK_EINVAL, "scale must be positive and finite");
     if (p->causal != 0 && p->causal != 1) return fail(FK_EINVAL, "causal must be 0 or 1");
@@ -321,6 +340,9 @@ fk_status fk_kv4_attention(const fk_kv4_cache* c, const fk_kv4_attn* p, void* ws
     a.q_vec = vec_rows(p->q, p->q_token, p->q_head);
     a.bpp = (uint32_t)(c->page_size / kKvBlock);
     a.bpp_magic = (uint32_t)((((uint64_t)1 << 32) + a.bpp - 1) / a.bpp);
+    a.G_magic = (uint32_t)((((uint64_t)1 << 32) + a.G - 1) / a.G);
+    a.cap = (int32_t)(p->max_pages * c->page_size);
+    a.least = plan.least;
     a.qk = p->scale * 1.4426950408889634f;
     a.row_tiles = plan.row_tiles;
     a.splits = plan.splits;
@@ -329,7 +351,7 @@ fk_status fk_kv4_attention(const fk_kv4_cache* c, const fk_kv4_attn* p, void* ws
     char* w = static_cast<char*>(ws);
     a.part_o = reinterpret_cast<float*>(w + plan.part_o);
     a.part_ml = reinterpret_cast<float*>(w + plan.part_ml);
-    a.prefix = reinterpret_cast<int64_t*>(w + plan.prefix);
+    a.prefix = reinterpret_cast<int32_t*>(w + plan.prefix);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const hipError_t e = c->head_dim == 64    ? launch_kv4_attn_d64(a, plan, c->dtype, s)
                          : c->head_dim == 128 ? launch_kv4_attn_d128(a, plan, c->dtype, s)

@@ -61,6 +61,9 @@ struct AttnArgs {
     int32_t B, Hq, Hkv, G, page_size, causal, window;
     int32_t q_vec;        // q rows can be read 16 bytes at a time
     uint32_t bpp, bpp_magic;  // blocks per page; ceil(2^32 / bpp)
+    uint32_t G_magic;         // ceil(2^32 / G)
+    int32_t cap;              // positions that the table has room for
+    int32_t least;            // split form: least blocks of a share
     float qk;             // scale * log2 e
     int32_t row_tiles;    // split form: tiles of query rows of one request
     int32_t splits;       // split form: workgroups per (kv head, row tile)
@@ -68,16 +71,17 @@ struct AttnArgs {
     int32_t join_rows;    // join: rows of a workgroup at a time
     float* part_o;        // split form: [Hkv * row_tiles][waves][2][part_rows][D]
     float* part_ml;       //             [Hkv * row_tiles][waves][2][part_rows][2]
-    int64_t* prefix;      //             [row_tiles][B + 1] blocks before each request
+    int32_t* prefix;      //             [row_tiles][B + 1] blocks before each request
 };
 
-#ifndef ROWS_NT
-#define ROWS_NT 3
-#endif
-// Column blocks of a wave in the rows form, by head dimension.
+// Most blocks of 16 query rows of a wave, by head dimension, in the rows form
+// and in the others: what 256 registers hold without spilling.
 template <int D>
-constexpr int kRowCols = D == 64 ? 4 : D == 128 ? ROWS_NT : 2;
+constexpr int kRowCols = D == 64 ? 4 : D == 128 ? 3 : 1;
+template <int D>
+constexpr int kTileCols = D <= 128 ? 3 : 1;
 inline int row_cols(int D) { return D == 64 ? kRowCols<64> : D == 128 ? kRowCols<128> : kRowCols<256>; }
+inline int tile_cols(int D) { return D <= 128 ? kTileCols<128> : kTileCols<256>; }
 
 // Query rows of a tile (16 per matrix column block) and the form a call runs.
 struct AttnPlan {
@@ -86,6 +90,7 @@ struct AttnPlan {
     bool whole;       // a workgroup takes a tile's keys whole, else shares
     int row_tiles, splits;
     int rows;         // split form: most rows of a tile
+    int least;        // split form: least blocks of a share
     int join_z, join_rows;  // join: workgroups of a tile, rows of one at a time
     size_t part_o, part_ml, prefix, total;  // workspace: offsets and size
 };

@@ -147,7 +147,8 @@ size_t fk_kv4_attn_workspace_bytes(const fk_kv4_cache* c, int64_t B, int64_t T, 
  * instructions: q scaled by a power of two per row (exact for bf16, to
  * 2^-25 of the row's largest value), codebook values as they are, softmax
  * weights times v's scale rounded to fp16 once.
- * Results do not depend on timing.  B <= 2^20, q_heads / kv_heads <= 256.
+ * Results do not depend on timing.  B <= 2^20, q_heads / kv_heads <= 256, T *
+ * q_heads / kv_heads <= 2^24, B * max_pages * page_size < 2^36.
  */
 fk_status fk_kv4_attention(const fk_kv4_cache* c, const fk_kv4_attn* a, void* ws, size_t ws_bytes,
                            void* stream);
