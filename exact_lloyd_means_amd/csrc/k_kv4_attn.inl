@@ -830,6 +830,33 @@ void k_kv4_attn_whole(AttnArgs a) {
     }
 }
 
+// ---- solo form: one wave a (request, row tile, kv head) ---------------------------
+
+// Grid (B / waves, row tiles x kv heads).
+template <int D, int DT, int NT>
+__global__ __launch_bounds__((64 * kSplitWaves<D, NT>), (kSplitWaves<D, NT> / 2))
+void k_kv4_attn_solo(AttnArgs a) {
+    constexpr int W = kSplitWaves<D, NT>, kThreads = 64 * W;
+    extern __shared__ uint32_t tab[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int b = blockIdx.x * W + wave;
+    const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y - h * a.row_tiles;
+    Rows rw{};
+    Span sp = {0, 0};
+    if (b < a.B) sp = split_span<NT>(a, b, rt, rw);
+    typename Wave<D, DT, NT>::Raw raw;
+    Wave<D, DT, NT>::fetch(a, rw, h, lane, raw);
+    Walk<D> wk;
+    if (sp.hi > sp.lo) wk.begin(a, a.table + b * a.max_pages, h, sp.lo, sp.hi, 1, lane);
+    build_table(tab, a.codebook, a.Hkv, h, tid, kThreads);
+    Wave<D, DT, NT> wv;
+    wv.init(a, rw, raw, lane);
+    __syncthreads();
+    if (sp.hi > sp.lo) wk.run(a, wv, lane);
+    finish<D, DT, NT>(a, wv, rw, h, lane);
+}
+
 // ---- split form: shares of the keys, a wave each ----------------------------------
 
 // Blocks a wave takes of `total`: an equal share; more, up to `least`, where an
@@ -1052,9 +1079,17 @@ hipError_t attn_rows(const AttnArgs& a, hipStream_t s) {
 
 template <int D, int DT, int NT>
 hipError_t attn_whole(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
-    static LdsAttr rec;
-    auto kern = k_kv4_attn_whole<D, DT, NT>;
+    static LdsAttr rec, solo_rec;
     constexpr int W = kSplitWaves<D, NT>, lds = kTabBytes + 16 * NT * W * 8;
+    if (p.solo) {
+        auto kern = k_kv4_attn_solo<D, DT, NT>;
+        hipError_t e = ensure_lds(solo_rec, reinterpret_cast<const void*>(kern), kTabBytes);
+        if (e != hipSuccess) return e;
+        kern<<<dim3((unsigned)((a.B + W - 1) / W), (unsigned)(a.Hkv * p.row_tiles)), dim3(64 * W),
+               kTabBytes, s>>>(a);
+        return hipGetLastError();
+    }
+    auto kern = k_kv4_attn_whole<D, DT, NT>;
     hipError_t e = ensure_lds(rec, reinterpret_cast<const void*>(kern), lds);
     if (e != hipSuccess) return e;
     kern<<<dim3((unsigned)a.B, (unsigned)(a.Hkv * p.row_tiles)), dim3(64 * W), lds, s>>>(a);

@@ -4,12 +4,6 @@
 
 #include "kv4_internal.h"
 
-#ifndef WHOLE_A
-#define WHOLE_A 32
-#endif
-#ifndef WHOLE_B
-#define WHOLE_B 0
-#endif
 namespace fk {
 
 static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -30,17 +24,20 @@ AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q,
     p.split = (rows <= tile || row_wgs < kResident) && tiles * Hkv <= 65535;
     p.row_tiles = p.split ? (int)tiles : 1;
     p.rows = (int)(rows < tile ? rows : tile);
-    // The keys of a request by one workgroup, no join: where the longest
-    // request that the table has room for is short, or the requests fill the
-    // card and none can hold it up for long.
-    if (p.split) p.whole = max_blocks <= WHOLE_A || (B * Hkv * tiles >= kResident / 2 && max_blocks <= WHOLE_B);
+    // Where the table has room for few blocks a request, the longest decides,
+    // and no launch that joins shares is worth its 8 us: one wave a request
+    // where they fill the card, else one workgroup.  Measured, 8 kv heads of
+    // 128, longest request in blocks, us as solo / whole / shares: 256 requests
+    // of 2: 10 / 30 / 25; 256 of 19: 27 / 42 / 39; 128 of 32: 42 / 31 / 31;
+    // 16 of 32: - / 12 / 21; 4 of 63: - / 16 / 20; 128 of 63: 84 / 48 / 45.
+    if (p.split) {
+        p.solo = B * Hkv * tiles >= 1024 && max_blocks <= 20;
+        p.whole = p.solo || max_blocks <= 64;
+    }
     if (p.split && !p.whole) {
-        // The join's workgroups, of 1024 / D rows at a time: about eight a CU.
+        // The join's workgroups, of 1024 / D rows at a time: about four a CU.
         const int64_t tiles_all = B * Hkv * tiles;
-        #ifndef JZ
-#define JZ 2048
-#endif
-        int64_t z = JZ / tiles_all;
+                int64_t z = 1024 / tiles_all;
         z = z < 1 ? 1 : z > p.rows ? p.rows : z;
         p.join_z = (int)z;
         const int each = (int)((p.rows + z - 1) / z), most = 1024 / D;

@@ -88,6 +88,7 @@ struct AttnPlan {
     int col_blocks;   // split form: blocks of 16 query rows per wave
     bool split;       // row tiles of requests, else rows
     bool whole;       // a workgroup takes a tile's keys whole, else shares
+    bool solo;        // with whole: a wave does
     int row_tiles, splits;
     int rows;         // split form: most rows of a tile
     int least;        // split form: least blocks of a share
