@@ -184,12 +184,6 @@ __device__ inline float max3(float x, float y, float z) {
     return r;
 }
 
-typedef unsigned short ushortx2 __attribute__((ext_vector_type(2)));
-__device__ inline uint32_t max_u16(uint32_t x, uint32_t y) {  // of both halves
-    return __builtin_bit_cast(uint32_t,
-                              __builtin_elementwise_max(__builtin_bit_cast(ushortx2, x),
-                                                        __builtin_bit_cast(ushortx2, y)));
-}
 // 2^e as bits of the cache dtype in both halves, at most infinity's.
 template <int DT>
 __device__ inline uint32_t pow2_bits(int e) {

@@ -2,11 +2,21 @@
 // fk_kv4_read).
 //
 // Sixteen lanes hold a row, D/16 consecutive dimensions each, and do its k
-// and its v.  Writing: s = max |x| over the row (an integer maximum of the
-// bits without sign, which also finds NaN and infinities), thresholds t_j s,
-// and each value's code by four comparisons of a search tree held in
-// registers.  A lane's codes are D/32 whole bytes of one token in both
-// layouts, so tokens never share a byte and no write needs an atomic.
+// and its v.
+//
+// Writing is bound by the comparisons unless they are few: one value meets 15
+// thresholds.  A value x of the cache type and a threshold t s in fp32 compare
+// as integers: with ord() the type's bits in value order, x > t s exactly
+// where ord(x) > ord(the largest 16-bit value not above t s).  Lane j of the
+// row finds that bound for threshold j, the row shares them through LDS, and
+// two values at a time walk the search tree in packed 16-bit arithmetic (a
+// saturated difference's sign is the comparison, v_bfi picks the next bound):
+// 14 instructions a value, where fp32 comparisons and selects take 22.
+// 16384 tokens x 8 heads x 128, k and v, 84 MB in and out: see fk_kv4_write in
+// the launch below.
+//
+// A lane's codes are D/32 whole bytes of one token in both layouts, so tokens
+// never share a byte and no write needs an atomic.
 #include "kv4_internal.h"
 
 #include <type_traits>
@@ -17,6 +27,17 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRowLanes = 16;
 constexpr int kRowsPerWg = kThreads / kRowLanes;
+
+// Where a slot lies: record index ((page * H + h) * 2) and place in the page.
+struct Place {
+    int64_t at;
+    int in;
+};
+__device__ inline Place place_of(const RowArgs& a, int32_t slot, int h) {
+    const uint32_t blk = (uint32_t)slot >> 5;
+    const uint32_t page = a.bpp == 1 ? blk : (uint32_t)(((uint64_t)blk * a.bpp_magic) >> 32);
+    return {((int64_t)page * a.H + h) * 2, (int)((uint32_t)slot - page * (uint32_t)a.page_size)};
+}
 
 // Byte offset of lane r's D/32 bytes of token t in its k block.
 template <int D>
@@ -47,17 +68,56 @@ __device__ inline uint32_t row_max(uint32_t x) {
     return x;
 }
 
-// Number of thresholds below x; t ascending.
-__device__ inline uint32_t code_of(float x, const float (&t)[15]) {
-    const bool c3 = t[7] < x;
-    float u[7];
+typedef short shortx2 __attribute__((ext_vector_type(2)));
+
+// Bits of two 16-bit floats as integers in the order of their values.
+__device__ inline shortx2 ordered(uint32_t x) {
+    const shortx2 v = __builtin_bit_cast(shortx2, x);
+    const shortx2 sign = v >> 15;
+    return v ^ (sign & (short)0x7fff);
+}
+
+// Lane j's bound: the order of the largest 16-bit value not above threshold j
+// times the scale, in both halves.  0x7fff, above every value, where the scale
+// is NaN: code 0.
+template <int DT>
+__device__ inline uint32_t bound(const uint16_t* cb, int j, uint32_t scale) {
+    const float lo = kv_f32<FK_F16>(cb[j]), hi = kv_f32<FK_F16>(cb[j < 15 ? j + 1 : 15]);
+    const float t = (float)(_Float16)(0.5f * (lo + hi)), s = kv_f32<DT>(scale);
+    const float v = t * s + 0.f;  // + 0: a threshold of -0 is 0
+    const uint32_t bits = kv_bits<DT>(v);
+    const int o = (int)(short)(bits ^ (bits & 0x8000 ? 0x7fff : 0)) - (kv_f32<DT>(bits) > v ? 1 : 0);
+    const uint32_t c = s == s ? (uint32_t)o & 0xffff : 0x7fff;
+    return c | c << 16;
+}
+
+// All ones in the halves where x > c: the sign of the saturated c - x.  As
+// instructions, since the compiler turns the masks back into scalar
+// comparisons and selects.
+__device__ inline uint32_t above(shortx2 x, uint32_t c) {
+    uint32_t d;
+    asm("v_pk_sub_i16 %0, %1, %2 clamp\n\tv_pk_ashrrev_i16 %0, 15, %0 op_sel_hi:[0,1]"
+        : "=&v"(d)
+        : "v"(c), "v"(x));
+    return d;
+}
+__device__ inline uint32_t pick(uint32_t m, uint32_t yes, uint32_t no) {
+    uint32_t d;
+    asm("v_bfi_b32 %0, %1, %2, %3" : "=v"(d) : "v"(m), "v"(yes), "v"(no));
+    return d;
+}
+
+// Codes of two values, in the low nibbles of the halves; c ascending.
+__device__ inline uint32_t codes_of(shortx2 x, const uint32_t (&c)[16]) {
+    const uint32_t m3 = above(x, c[7]);
+    uint32_t u[7];
 #pragma unroll
-    for (int i = 0; i < 7; ++i) u[i] = c3 ? t[8 + i] : t[i];
-    const bool c2 = u[3] < x;
-    const float v0 = c2 ? u[4] : u[0], v1 = c2 ? u[5] : u[1], v2 = c2 ? u[6] : u[2];
-    const bool c1 = v1 < x;
-    const float w = c1 ? v2 : v0;
-    return (c3 ? 8u : 0u) | (c2 ? 4u : 0u) | (c1 ? 2u : 0u) | (w < x ? 1u : 0u);
+    for (int i = 0; i < 7; ++i) u[i] = pick(m3, c[8 + i], c[i]);
+    const uint32_t m2 = above(x, u[3]);
+    const uint32_t v0 = pick(m2, u[4], u[0]), v1 = pick(m2, u[5], u[1]), v2 = pick(m2, u[6], u[2]);
+    const uint32_t m1 = above(x, v1);
+    const uint32_t m0 = above(x, pick(m1, v2, v0));
+    return (m3 & 0x00080008) | (m2 & 0x00040004) | (m1 & 0x00020002) | (m0 & 0x00010001);
 }
 
 template <int D, int DT, bool VEC>
@@ -83,39 +143,33 @@ __device__ inline void load_row(const uint16_t* p, uint32_t (&x)[D / 32]) {
     }
 }
 
-// Codes of a lane's D/16 values as D/32 bytes and the row's scale bits.
+// Codes of a lane's D/16 values as D/32 bytes and the row's scale bits.  row:
+// 16 words of LDS of this row.
 template <int D, int DT>
-__device__ inline void encode(const uint32_t (&x)[D / 32], const float* thr, uint32_t& scale,
-                              uint64_t& bytes) {
-    uint32_t m = 0;
+__device__ inline void encode(const uint32_t (&x)[D / 32], const uint16_t* cb, uint32_t* row, int r,
+                              uint32_t& scale, uint64_t& bytes) {
+    uint32_t m = x[0] & 0x7fff7fff;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-        const uint32_t lo = x[i] & 0x7fff, hi = (x[i] >> 16) & 0x7fff;
-        m = m > lo ? m : lo;
-        m = m > hi ? m : hi;
-    }
-    m = row_max(m);
+    for (int i = 1; i < D / 32; ++i) m = max_u16(m, x[i] & 0x7fff7fff);
+    m = row_max(m >> 16 > (m & 0xffff) ? m >> 16 : m & 0xffff);
     constexpr uint32_t inf = DT == FK_BF16 ? 0x7f80 : 0x7c00, nan = DT == FK_BF16 ? 0x7fc0 : 0x7e00;
     scale = m >= inf ? nan : m;
-    const float s = kv_f32<DT>(scale);
-    float t[15];
+    row[r] = bound<DT>(cb, r, scale);
+    __builtin_amdgcn_wave_barrier();  // the row's lanes are of one wave
+    uint32_t c[16];
 #pragma unroll
-    for (int j = 0; j < 15; ++j) t[j] = thr[j] * s;
+    for (int i = 0; i < 4; ++i) {
+        const uint4 y = reinterpret_cast<const uint4*>(row)[i];
+        c[4 * i] = y.x;
+        c[4 * i + 1] = y.y;
+        c[4 * i + 2] = y.z;
+        c[4 * i + 3] = y.w;
+    }
     bytes = 0;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-        const uint32_t b = code_of(kv_f32<DT>(x[i] & 0xffff), t) |
-                           code_of(kv_f32<DT>(x[i] >> 16), t) << 4;
-        bytes |= (uint64_t)b << (8 * i);
-    }
-}
-
-// Thresholds of the codebooks into LDS, [kv][H][16].
-__device__ inline void load_thresholds(const uint16_t* cb, float* thr, int H, int tid) {
-    for (int i = tid; i < 2 * H * 16; i += kThreads) {
-        const float lo = kv_f32<FK_F16>(cb[i]);
-        const float hi = (i & 15) < 15 ? kv_f32<FK_F16>(cb[i + 1]) : lo;
-        thr[i] = (float)(_Float16)(0.5f * (lo + hi));
+        const uint32_t y = codes_of(ordered(x[i]), c);
+        bytes |= (uint64_t)((y | y >> 12) & 0xff) << (8 * i);
     }
 }
 
@@ -128,32 +182,29 @@ __device__ inline void store_bytes(uint8_t* p, uint64_t b) {
 
 template <int D, int DT, bool VEC>
 __global__ __launch_bounds__(kThreads) void k_kv4_write(RowArgs a) {
-    extern __shared__ float thr[];
+    __shared__ uint32_t bounds[2][kRowsPerWg][16];
     const int tid = threadIdx.x, r = tid & 15;
-    load_thresholds(a.codebook, thr, a.H, tid);
-    __syncthreads();
-    const int64_t rows = a.T * a.H;
-    for (int64_t row = (int64_t)blockIdx.x * kRowsPerWg + (tid >> 4); row < rows;
-         row += (int64_t)gridDim.x * kRowsPerWg) {
-        const int64_t tok = row / a.H;
-        const int h = (int)(row - tok * a.H);
+    uint32_t *kc = bounds[0][tid >> 4], *vc = bounds[1][tid >> 4];
+    const int h = blockIdx.y;
+    for (int64_t tok = (int64_t)blockIdx.x * kRowsPerWg + (tid >> 4); tok < a.T;
+         tok += (int64_t)gridDim.x * kRowsPerWg) {
         const int32_t slot = a.slots[tok];
         if (slot < 0 || slot >= a.slots_total) continue;  // the whole row's lanes
         uint32_t x[D / 32], y[D / 32];
         load_row<D, DT, VEC>(a.k + tok * a.k_token + h * a.k_head + r * (D / 16), x);
         load_row<D, DT, VEC>(a.v + tok * a.v_token + h * a.v_head + r * (D / 16), y);
-        const int32_t page = (uint32_t)slot / (uint32_t)a.page_size;
-        const int in = slot - page * a.page_size;
-        const int64_t at = ((int64_t)page * a.H + h) * 2;
-        const int64_t plane = (int64_t)a.page_size / kKvBlock * (16 * D);
+        const Place p = place_of(a, slot, h);
+        const int64_t at = p.at;
+        const int in = p.in;
+        const int64_t plane = (int64_t)a.bpp * (16 * D);
         uint8_t* kb = a.codes + at * plane + (int64_t)(in >> 5) * (16 * D);
         uint8_t* vb = kb + plane;
         uint32_t s;
         uint64_t b;
-        encode<D, DT>(x, thr + h * 16, s, b);
+        encode<D, DT>(x, a.codebook + h * 16, kc, r, s, b);
         store_bytes<D>(kb + k_place<D>(in & 31, r), b);
         if (r == 0) a.scales[at * a.page_size + in] = (uint16_t)s;
-        encode<D, DT>(y, thr + (a.H + h) * 16, s, b);
+        encode<D, DT>(y, a.codebook + (a.H + h) * 16, vc, r, s, b);
         if constexpr (D == 256) {
             *reinterpret_cast<uint32_t*>(vb + v_place<D>(in & 31, r, 0)) = (uint32_t)b;
             *reinterpret_cast<uint32_t*>(vb + v_place<D>(in & 31, r, 1)) = (uint32_t)(b >> 32);
@@ -192,21 +243,18 @@ __device__ inline void decode(uint64_t b, float s, const float* cb, uint16_t* ou
 
 template <int D, int DT>
 __global__ __launch_bounds__(kThreads) void k_kv4_read(RowArgs a) {
-    extern __shared__ float cb[];  // [kv][H][16]
-    const int tid = threadIdx.x, r = tid & 15;
-    for (int i = tid; i < 2 * a.H * 16; i += kThreads) cb[i] = kv_f32<FK_F16>(a.codebook[i]);
+    __shared__ float cb[2][16];
+    const int tid = threadIdx.x, r = tid & 15, h = blockIdx.y;
+    if (tid < 32) cb[tid >> 4][tid & 15] = kv_f32<FK_F16>(a.codebook[((tid >> 4) * a.H + h) * 16 + (tid & 15)]);
     __syncthreads();
-    const int64_t rows = a.T * a.H;
-    for (int64_t row = (int64_t)blockIdx.x * kRowsPerWg + (tid >> 4); row < rows;
-         row += (int64_t)gridDim.x * kRowsPerWg) {
-        const int64_t tok = row / a.H;
-        const int h = (int)(row - tok * a.H);
+    for (int64_t tok = (int64_t)blockIdx.x * kRowsPerWg + (tid >> 4); tok < a.T;
+         tok += (int64_t)gridDim.x * kRowsPerWg) {
         const int32_t slot = a.slots[tok];
         const bool there = slot >= 0 && slot < a.slots_total;
-        const int32_t page = there ? (uint32_t)slot / (uint32_t)a.page_size : 0;
-        const int in = there ? slot - page * a.page_size : 0;
-        const int64_t at = ((int64_t)page * a.H + h) * 2;
-        const int64_t plane = (int64_t)a.page_size / kKvBlock * (16 * D);
+        const Place p = place_of(a, there ? slot : 0, h);
+        const int64_t at = p.at;
+        const int in = p.in;
+        const int64_t plane = (int64_t)a.bpp * (16 * D);
         const uint8_t* kb = a.codes + at * plane + (int64_t)(in >> 5) * (16 * D);
         const uint8_t* vb = kb + plane;
         const uint64_t k = load_bytes<D>(kb + k_place<D>(in & 31, r));
@@ -218,39 +266,28 @@ __global__ __launch_bounds__(kThreads) void k_kv4_read(RowArgs a) {
             v = load_bytes<D>(vb + v_place<D>(in & 31, r, 0));
         const float ks = there ? kv_f32<DT>(a.scales[at * a.page_size + in]) : 0.f;
         const float vs = there ? kv_f32<DT>(a.scales[(at + 1) * a.page_size + in]) : 0.f;
-        const int64_t o = row * D + r * (D / 16);
-        decode<D, DT>(k, ks, cb + h * 16, a.ko + o);
-        decode<D, DT>(v, vs, cb + (a.H + h) * 16, a.vo + o);
+        const int64_t o = (tok * a.H + h) * D + r * (D / 16);
+        decode<D, DT>(k, ks, cb[0], a.ko + o);
+        decode<D, DT>(v, vs, cb[1], a.vo + o);
     }
 }
 
-unsigned row_wgs(const RowArgs& a) {
-    const int64_t wgs = (a.T * a.H + kRowsPerWg - 1) / kRowsPerWg;
-    return (unsigned)(wgs > (1 << 20) ? (1 << 20) : wgs);
+// Sixteen tokens of one head a workgroup: neighbours in a page fill whole
+// lines of its blocks.
+dim3 row_grid(const RowArgs& a) {
+    return dim3((unsigned)((a.T + kRowsPerWg - 1) / kRowsPerWg), (unsigned)a.H);
 }
 
 template <int D, int DT>
 hipError_t write_as(const RowArgs& a, bool vec, hipStream_t s) {
-    const unsigned lds = 2u * a.H * 16 * 4;
     auto kern = vec ? k_kv4_write<D, DT, true> : k_kv4_write<D, DT, false>;
-    static LdsAttr rec[2];
-    if (lds > 65536) {
-        hipError_t e = ensure_lds(rec[vec], reinterpret_cast<const void*>(kern), 131072);
-        if (e != hipSuccess) return e;
-    }
-    kern<<<dim3(row_wgs(a)), dim3(kThreads), lds, s>>>(a);
+    kern<<<row_grid(a), dim3(kThreads), 0, s>>>(a);
     return hipGetLastError();
 }
 
 template <int D, int DT>
 hipError_t read_as(const RowArgs& a, hipStream_t s) {
-    const unsigned lds = 2u * a.H * 16 * 4;
-    static LdsAttr rec;
-    if (lds > 65536) {
-        hipError_t e = ensure_lds(rec, reinterpret_cast<const void*>(k_kv4_read<D, DT>), 131072);
-        if (e != hipSuccess) return e;
-    }
-    k_kv4_read<D, DT><<<dim3(row_wgs(a)), dim3(kThreads), lds, s>>>(a);
+    k_kv4_read<D, DT><<<row_grid(a), dim3(kThreads), 0, s>>>(a);
     return hipGetLastError();
 }
 

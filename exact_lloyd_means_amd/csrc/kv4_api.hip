@@ -144,6 +144,10 @@ fk_status check_strides(const char* name, int64_t token, int64_t head) {
     return FK_OK;
 }
 
+// ceil(2^32 / d): the high half of x times it is x / d while x d < 2^32.  (d = 1
+// does not fit; the kernels do not divide then.)
+uint32_t division_magic(uint32_t d) { return (uint32_t)((((uint64_t)1 << 32) + d - 1) / d); }
+
 // Rows that can be read in whole 16-byte pieces.
 bool vec_rows(const void* p, int64_t token, int64_t head) {
     return aligned(p, 16) && token % 8 == 0 && head % 8 == 0;
@@ -159,6 +163,8 @@ RowArgs row_args(const fk_kv4_cache* c, int64_t T, const int32_t* slots) {
     a.slots_total = c->pages * c->page_size;
     a.page_size = c->page_size;
     a.H = c->kv_heads;
+    a.bpp = (uint32_t)(c->page_size / kKvBlock);
+    a.bpp_magic = division_magic(a.bpp);
     return a;
 }
 
@@ -336,8 +342,8 @@ fk_status fk_kv4_attention(const fk_kv4_cache* c, const fk_kv4_attn* p, void* ws
     a.window = p->window;
     a.q_vec = vec_rows(p->q, p->q_token, p->q_head);
     a.bpp = (uint32_t)(c->page_size / kKvBlock);
-    a.bpp_magic = (uint32_t)((((uint64_t)1 << 32) + a.bpp - 1) / a.bpp);
-    a.G_magic = (uint32_t)((((uint64_t)1 << 32) + a.G - 1) / a.G);
+    a.bpp_magic = division_magic(a.bpp);
+    a.G_magic = division_magic((uint32_t)a.G);
     a.cap = (int32_t)(p->max_pages * c->page_size);
     a.least = plan.least;
     a.qk = p->scale * 1.4426950408889634f;

@@ -25,6 +25,12 @@ __device__ inline uint32_t kv_bits(float x) {
         return __builtin_bit_cast(uint16_t, (_Float16)x);
 }
 
+typedef unsigned short ushortx2 __attribute__((ext_vector_type(2)));
+__device__ inline uint32_t max_u16(uint32_t x, uint32_t y) {  // of both halves
+    return __builtin_bit_cast(uint32_t,
+                              __builtin_elementwise_max(__builtin_bit_cast(ushortx2, x),
+                                                        __builtin_bit_cast(ushortx2, y)));
+}
 struct PlanArgs {
     int64_t B, max_pages, free_cap, slot_cap;
     int32_t page_size;
@@ -44,6 +50,7 @@ struct RowArgs {
     int64_t k_token, k_head, v_token, v_head;
     int64_t T, slots_total;  // pages * page_size
     int32_t page_size, H;
+    uint32_t bpp, bpp_magic;  // blocks per page; ceil(2^32 / bpp)
 };
 hipError_t launch_kv4_write(const RowArgs& a, int D, int dtype, bool vec, hipStream_t s);
 hipError_t launch_kv4_read(const RowArgs& a, int D, int dtype, hipStream_t s);
