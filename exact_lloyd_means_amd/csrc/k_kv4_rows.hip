@@ -77,13 +77,18 @@ __device__ inline shortx2 ordered(uint32_t x) {
     return v ^ (sign & (short)0x7fff);
 }
 
-// Lane j's bound: the order of the largest 16-bit value not above threshold j
+// Threshold j of a codebook.
+__device__ inline float threshold(const uint16_t* cb, int j) {
+    const float lo = kv_f32<FK_F16>(cb[j]), hi = kv_f32<FK_F16>(cb[j < 15 ? j + 1 : 15]);
+    return (float)(_Float16)(0.5f * (lo + hi));
+}
+
+// A lane's bound: the order of the largest 16-bit value not above threshold t
 // times the scale, in both halves.  0x7fff, above every value, where the scale
 // is NaN: code 0.
 template <int DT>
-__device__ inline uint32_t bound(const uint16_t* cb, int j, uint32_t scale) {
-    const float lo = kv_f32<FK_F16>(cb[j]), hi = kv_f32<FK_F16>(cb[j < 15 ? j + 1 : 15]);
-    const float t = (float)(_Float16)(0.5f * (lo + hi)), s = kv_f32<DT>(scale);
+__device__ inline uint32_t bound(float t, uint32_t scale) {
+    const float s = kv_f32<DT>(scale);
     const float v = t * s + 0.f;  // + 0: a threshold of -0 is 0
     const uint32_t bits = kv_bits<DT>(v);
     const int o = (int)(short)(bits ^ (bits & 0x8000 ? 0x7fff : 0)) - (kv_f32<DT>(bits) > v ? 1 : 0);
@@ -146,7 +151,7 @@ __device__ inline void load_row(const uint16_t* p, uint32_t (&x)[D / 32]) {
 // Codes of a lane's D/16 values as D/32 bytes and the row's scale bits.  row:
 // 16 words of LDS of this row.
 template <int D, int DT>
-__device__ inline void encode(const uint32_t (&x)[D / 32], const uint16_t* cb, uint32_t* row, int r,
+__device__ inline void encode(const uint32_t (&x)[D / 32], float t, uint32_t* row, int r,
                               uint32_t& scale, uint64_t& bytes) {
     uint32_t m = x[0] & 0x7fff7fff;
 #pragma unroll
@@ -154,7 +159,7 @@ __device__ inline void encode(const uint32_t (&x)[D / 32], const uint16_t* cb, u
     m = row_max(m >> 16 > (m & 0xffff) ? m >> 16 : m & 0xffff);
     constexpr uint32_t inf = DT == FK_BF16 ? 0x7f80 : 0x7c00, nan = DT == FK_BF16 ? 0x7fc0 : 0x7e00;
     scale = m >= inf ? nan : m;
-    row[r] = bound<DT>(cb, r, scale);
+    row[r] = bound<DT>(t, scale);
     __builtin_amdgcn_wave_barrier();  // the row's lanes are of one wave
     uint32_t c[16];
 #pragma unroll
@@ -185,34 +190,33 @@ __global__ __launch_bounds__(kThreads) void k_kv4_write(RowArgs a) {
     __shared__ uint32_t bounds[2][kRowsPerWg][16];
     const int tid = threadIdx.x, r = tid & 15;
     uint32_t *kc = bounds[0][tid >> 4], *vc = bounds[1][tid >> 4];
-    const int h = blockIdx.y;
-    for (int64_t tok = (int64_t)blockIdx.x * kRowsPerWg + (tid >> 4); tok < a.T;
-         tok += (int64_t)gridDim.x * kRowsPerWg) {
-        const int32_t slot = a.slots[tok];
-        if (slot < 0 || slot >= a.slots_total) continue;  // the whole row's lanes
-        uint32_t x[D / 32], y[D / 32];
-        load_row<D, DT, VEC>(a.k + tok * a.k_token + h * a.k_head + r * (D / 16), x);
-        load_row<D, DT, VEC>(a.v + tok * a.v_token + h * a.v_head + r * (D / 16), y);
-        const Place p = place_of(a, slot, h);
-        const int64_t at = p.at;
-        const int in = p.in;
-        const int64_t plane = (int64_t)a.bpp * (16 * D);
-        uint8_t* kb = a.codes + at * plane + (int64_t)(in >> 5) * (16 * D);
-        uint8_t* vb = kb + plane;
-        uint32_t s;
-        uint64_t b;
-        encode<D, DT>(x, a.codebook + h * 16, kc, r, s, b);
-        store_bytes<D>(kb + k_place<D>(in & 31, r), b);
-        if (r == 0) a.scales[at * a.page_size + in] = (uint16_t)s;
-        encode<D, DT>(y, a.codebook + (a.H + h) * 16, vc, r, s, b);
-        if constexpr (D == 256) {
-            *reinterpret_cast<uint32_t*>(vb + v_place<D>(in & 31, r, 0)) = (uint32_t)b;
-            *reinterpret_cast<uint32_t*>(vb + v_place<D>(in & 31, r, 1)) = (uint32_t)(b >> 32);
-        } else {
-            store_bytes<D>(vb + v_place<D>(in & 31, r, 0), b);
-        }
-        if (r == 0) a.scales[(at + 1) * a.page_size + in] = (uint16_t)s;
+    const int group = blockIdx.x / (uint32_t)a.H, h = blockIdx.x - group * a.H;
+    const int tok = group * kRowsPerWg + (tid >> 4);
+    if (tok >= a.T) return;
+    uint32_t x[D / 32], y[D / 32];
+    load_row<D, DT, VEC>(a.k + tok * a.k_token + h * a.k_head + r * (D / 16), x);
+    load_row<D, DT, VEC>(a.v + tok * a.v_token + h * a.v_head + r * (D / 16), y);
+    const int32_t slot = a.slots[tok];
+    const float tk = threshold(a.codebook + h * 16, r), tv = threshold(a.codebook + (a.H + h) * 16, r);
+    if (slot < 0 || slot >= a.slots_total) return;  // the same for the whole row's lanes
+    const Place p = place_of(a, slot, h);
+    const int i = p.in & 31;
+    uint8_t* kb = a.codes + (p.at * a.bpp + (p.in >> 5)) * (16 * D);
+    uint8_t* vb = kb + a.bpp * (16 * D);
+    uint16_t* sc = a.scales + p.at * a.page_size + p.in;
+    uint32_t s;
+    uint64_t b;
+    encode<D, DT>(x, tk, kc, r, s, b);
+    store_bytes<D>(kb + k_place<D>(i, r), b);
+    if (r == 0) sc[0] = (uint16_t)s;
+    encode<D, DT>(y, tv, vc, r, s, b);
+    if constexpr (D == 256) {
+        *reinterpret_cast<uint32_t*>(vb + v_place<D>(i, r, 0)) = (uint32_t)b;
+        *reinterpret_cast<uint32_t*>(vb + v_place<D>(i, r, 1)) = (uint32_t)(b >> 32);
+    } else {
+        store_bytes<D>(vb + v_place<D>(i, r, 0), b);
     }
+    if (r == 0) sc[a.page_size] = (uint16_t)s;
 }
 
 template <int D>
@@ -244,38 +248,39 @@ __device__ inline void decode(uint64_t b, float s, const float* cb, uint16_t* ou
 template <int D, int DT>
 __global__ __launch_bounds__(kThreads) void k_kv4_read(RowArgs a) {
     __shared__ float cb[2][16];
-    const int tid = threadIdx.x, r = tid & 15, h = blockIdx.y;
+    const int tid = threadIdx.x, r = tid & 15;
+    const int group = blockIdx.x / (uint32_t)a.H, h = blockIdx.x - group * a.H;
     if (tid < 32) cb[tid >> 4][tid & 15] = kv_f32<FK_F16>(a.codebook[((tid >> 4) * a.H + h) * 16 + (tid & 15)]);
     __syncthreads();
-    for (int64_t tok = (int64_t)blockIdx.x * kRowsPerWg + (tid >> 4); tok < a.T;
-         tok += (int64_t)gridDim.x * kRowsPerWg) {
-        const int32_t slot = a.slots[tok];
-        const bool there = slot >= 0 && slot < a.slots_total;
-        const Place p = place_of(a, there ? slot : 0, h);
-        const int64_t at = p.at;
-        const int in = p.in;
-        const int64_t plane = (int64_t)a.bpp * (16 * D);
-        const uint8_t* kb = a.codes + at * plane + (int64_t)(in >> 5) * (16 * D);
-        const uint8_t* vb = kb + plane;
-        const uint64_t k = load_bytes<D>(kb + k_place<D>(in & 31, r));
-        uint64_t v;
-        if constexpr (D == 256)
-            v = *reinterpret_cast<const uint32_t*>(vb + v_place<D>(in & 31, r, 0)) |
-                (uint64_t) * reinterpret_cast<const uint32_t*>(vb + v_place<D>(in & 31, r, 1)) << 32;
-        else
-            v = load_bytes<D>(vb + v_place<D>(in & 31, r, 0));
-        const float ks = there ? kv_f32<DT>(a.scales[at * a.page_size + in]) : 0.f;
-        const float vs = there ? kv_f32<DT>(a.scales[(at + 1) * a.page_size + in]) : 0.f;
-        const int64_t o = (tok * a.H + h) * D + r * (D / 16);
-        decode<D, DT>(k, ks, cb[0], a.ko + o);
-        decode<D, DT>(v, vs, cb[1], a.vo + o);
-    }
+    const int tok = group * kRowsPerWg + (tid >> 4);
+    if (tok >= a.T) return;
+    const int32_t slot = a.slots[tok];
+    const bool there = slot >= 0 && slot < a.slots_total;
+    const Place p = place_of(a, there ? slot : 0, h);
+    const int64_t at = p.at;
+    const int in = p.in;
+    const int64_t plane = (int64_t)a.bpp * (16 * D);
+    const uint8_t* kb = a.codes + at * plane + (int64_t)(in >> 5) * (16 * D);
+    const uint8_t* vb = kb + plane;
+    const uint64_t k = load_bytes<D>(kb + k_place<D>(in & 31, r));
+    uint64_t v;
+    if constexpr (D == 256)
+        v = *reinterpret_cast<const uint32_t*>(vb + v_place<D>(in & 31, r, 0)) |
+            (uint64_t) * reinterpret_cast<const uint32_t*>(vb + v_place<D>(in & 31, r, 1)) << 32;
+    else
+        v = load_bytes<D>(vb + v_place<D>(in & 31, r, 0));
+    const float ks = there ? kv_f32<DT>(a.scales[at * a.page_size + in]) : 0.f;
+    const float vs = there ? kv_f32<DT>(a.scales[(at + 1) * a.page_size + in]) : 0.f;
+    const int64_t o = ((int64_t)tok * a.H + h) * D + r * (D / 16);
+    decode<D, DT>(k, ks, cb[0], a.ko + o);
+    decode<D, DT>(v, vs, cb[1], a.vo + o);
 }
 
-// Sixteen tokens of one head a workgroup: neighbours in a page fill whole
-// lines of its blocks.
+// Sixteen tokens of one head a workgroup, so that neighbours in a page fill
+// whole lines of its blocks; the heads of the same tokens next to each other,
+// since their rows are neighbours in k and v.
 dim3 row_grid(const RowArgs& a) {
-    return dim3((unsigned)((a.T + kRowsPerWg - 1) / kRowsPerWg), (unsigned)a.H);
+    return dim3((unsigned)((a.T + kRowsPerWg - 1) / kRowsPerWg * a.H));
 }
 
 template <int D, int DT>
