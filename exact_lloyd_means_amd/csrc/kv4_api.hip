@@ -133,6 +133,13 @@ fk_status check_tokens(int64_t T) {
     return FK_OK;
 }
 
+fk_status check_rows(int64_t T, const fk_kv4_cache* c) {
+    FK_CHECK(check_tokens(T));
+    if (T * c->kv_heads > (int64_t)1 << 27)
+        return fail(FK_EUNSUPPORTED, "T * kv_heads must be <= 2^27");
+    return FK_OK;
+}
+
 fk_status check_requests(int64_t B) {
     if (B < 1) return fail(FK_EINVAL, "B must be >= 1");
     if (B > kMaxRequests) return fail(FK_EUNSUPPORTED, "B must be <= 2^20");
@@ -168,13 +175,15 @@ RowArgs row_args(const fk_kv4_cache* c, int64_t T, const int32_t* slots) {
     return a;
 }
 
-fk_status check_heads(const fk_kv4_cache* c, int64_t T, int32_t q_heads, int32_t max_q) {
+fk_status check_heads(const fk_kv4_cache* c, int64_t B, int64_t T, int32_t q_heads, int32_t max_q) {
     if (q_heads < 1 || q_heads % c->kv_heads)
         return fail(FK_EINVAL, "q_heads (%d) must be a multiple of kv_heads (%d)", (int)q_heads,
                     (int)c->kv_heads);
     if (q_heads / c->kv_heads > 256) return fail(FK_EUNSUPPORTED, "q_heads / kv_heads must be <= 256");
     if (T * (q_heads / c->kv_heads) > kMaxTokens)
         return fail(FK_EUNSUPPORTED, "T * q_heads / kv_heads must be <= 2^24");
+    if ((T * (q_heads / c->kv_heads) / 64 + B) * c->kv_heads >= (int64_t)1 << 24)
+        return fail(FK_EUNSUPPORTED, "T * q_heads / 64 + B * kv_heads must be < 2^24");
     if (max_q < 1) return fail(FK_EINVAL, "max_q must be >= 1");
     return FK_OK;
 }
@@ -245,7 +254,7 @@ fk_status fk_kv4_write(const fk_kv4_cache* c, int64_t T, const void* k, int64_t 
                        int64_t k_head, const void* v, int64_t v_token, int64_t v_head,
                        const int32_t* slots, void* stream) {
     FK_CHECK(check_cache(c));
-    FK_CHECK(check_tokens(T));
+    FK_CHECK(check_rows(T, c));
     FK_CHECK(need(k, "k", 2));
     FK_CHECK(need(v, "v", 2));
     FK_CHECK(check_strides("k", k_token, k_head));
@@ -267,7 +276,7 @@ fk_status fk_kv4_write(const fk_kv4_cache* c, int64_t T, const void* k, int64_t 
 fk_status fk_kv4_read(const fk_kv4_cache* c, int64_t T, const int32_t* slots, void* k, void* v,
                       void* stream) {
     FK_CHECK(check_cache(c));
-    FK_CHECK(check_tokens(T));
+    FK_CHECK(check_rows(T, c));
     FK_CHECK(need(slots, "slots", 4));
     FK_CHECK(need(k, "k", 16));
     FK_CHECK(need(v, "v", 16));
@@ -281,7 +290,7 @@ fk_status fk_kv4_read(const fk_kv4_cache* c, int64_t T, const int32_t* slots, vo
 size_t fk_kv4_attn_workspace_bytes(const fk_kv4_cache* c, int64_t B, int64_t T, int32_t q_heads,
                                    int32_t max_q) {
     if (check_shape(c) != FK_OK || check_requests(B) != FK_OK || check_tokens(T) != FK_OK ||
-        check_heads(c, T, q_heads, max_q) != FK_OK)
+        check_heads(c, B, T, q_heads, max_q) != FK_OK)
         return 0;
     // as much as a call with any block table needs
     return plan_attention(B, T, q_heads, c->kv_heads, c->head_dim, clamp_max_q(T, max_q),
@@ -294,7 +303,7 @@ fk_status fk_kv4_attention(const fk_kv4_cache* c, const fk_kv4_attn* p, void* ws
     if (!p) return fail(FK_EINVAL, "arguments are NULL");
     FK_CHECK(check_requests(p->B));
     FK_CHECK(check_tokens(p->T));
-    FK_CHECK(check_heads(c, p->T, p->q_heads, p->max_q));
+    FK_CHECK(check_heads(c, p->B, p->T, p->q_heads, p->max_q));
     if (p->max_pages < 1) return fail(FK_EINVAL, "max_pages must be >= 1");
     if (p->max_pages > 2147483647 / c->page_size)
         return fail(FK_EUNSUPPORTED, "max_pages * page_size must be <= 2^31 - 1");
