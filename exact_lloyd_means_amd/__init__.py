@@ -418,5 +418,5 @@ def fk_assign_variant(X: torch.Tensor, C: torch.Tensor, bias: torch.Tensor, labe
 
 
 from .api import KMeans, batch_kmeans_euclid, initial_centroids  # noqa: E402  (uses the above)
-from .kv4 import (fk_kv4_attention, fk_kv4_read, fk_kv4_write, fk_kv_plan,  # noqa: E402
-                  kv4_attention_workspace, kv_plan_workspace)
+from .kv4 import (KV4Cache, fk_kv4_attention, fk_kv4_read, fk_kv4_write, fk_kv_plan,  # noqa: E402
+                  kv4_attention_workspace, kv_plan_workspace, learn_codebook)

@@ -28,7 +28,7 @@ import torch
 
 from . import DTYPES, _check, _need_gpu, _P, _stream, _want, _want_ws, lib
 
-__all__ = ["fk_kv_plan", "fk_kv4_write", "fk_kv4_read", "fk_kv4_attention", "kv_plan_workspace",
+__all__ = ["KV4Cache", "learn_codebook", "fk_kv_plan", "fk_kv4_write", "fk_kv4_read", "fk_kv4_attention", "kv_plan_workspace",
            "kv4_attention_workspace"]
 
 _I32, _I64, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
@@ -223,3 +223,106 @@ def fk_kv4_attention(q, cu_q, seq_lens, block_table, codebook, codes, scales, ou
         ws = kv4_attention_workspace(q, seq_lens, codes, max_q)
     _check(lib.fk_kv4_attention(c, args, *_ws_at(ws, index), _stream_of(stream, index)),
            "fk_kv4_attention")
+
+
+def learn_codebook(k, v, iters: int = 30, stream=None) -> torch.Tensor:
+    """Codebook (2, kv_heads, 16) fp16 from sample rows k, v (tokens,
+    kv_heads, head_dim) on the GPU: exact Lloyd k-means (K = 16, d = 1, one
+    problem a head, k and v) on the values over their row's largest
+    magnitude, from equally spaced levels, in the library's deterministic
+    mode.  Preparing the values is done with torch."""
+    from .api import batch_kmeans_euclid
+    T, H, D = _tensor(k, "k", 3)
+    if v.shape != k.shape:
+        raise ValueError(f"v must have shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    x = torch.stack((k, v)).float()
+    x = x / x.abs().amax(-1, keepdim=True).clamp(min=torch.finfo(torch.float32).tiny)
+    x = x.permute(0, 2, 1, 3).reshape(2 * H, T * D, 1).contiguous()
+    first = torch.linspace(-1, 1, 16, device=x.device).view(16, 1)
+    _, c, _ = batch_kmeans_euclid(x, 16, iters, init=first, deterministic=True, stream=stream)
+    return c.view(2, H, 16).sort(-1).values.half().contiguous()
+
+
+class KV4Cache:
+    """The buffers of a serving loop around the functions above.
+
+    pages x page_size tokens are shared by max_requests rows of a block table
+    with room for max_len tokens each.  A step is plan(), append(), attend();
+    release() returns a row's pages.  Lengths, tables and the list of free
+    pages live on the GPU and no call waits for it."""
+
+    def __init__(self, pages: int, page_size: int, kv_heads: int, head_dim: int,
+                 codebook: torch.Tensor, max_requests: int, max_len: int,
+                 dtype=torch.bfloat16, device="cuda"):
+        if page_size < 32 or page_size % 32:
+            raise ValueError("page_size must be a multiple of 32")
+        if dtype not in _HALVES:
+            raise ValueError("dtype must be float16 or bfloat16")
+        self.page_size = int(page_size)
+        M = -(-int(max_len) // self.page_size)
+        i32 = dict(dtype=torch.int32, device=device)
+        # every byte is a valid code and no scale may be NaN
+        self.codes = torch.zeros(pages, kv_heads, 2, page_size // 32, 16 * head_dim,
+                                 dtype=torch.uint8, device=device)
+        self.scales = torch.zeros(pages, kv_heads, 2, page_size, dtype=dtype, device=device)
+        self.codebook = codebook
+        self.block_table = torch.full((max_requests, M), -1, **i32)
+        self.free_pages = torch.arange(pages - 1, -1, -1, **i32)
+        self.free_count = torch.full((1,), pages, **i32)
+        self.status = torch.zeros(4, **i32)
+        self.cu = torch.zeros(max_requests + 1, **i32)
+        self._lens = [torch.zeros(max_requests, **i32) for _ in range(2)]
+        self._plan_ws = kv_plan_workspace(max_requests, device)
+        self.slots = self.positions = None
+
+    @property
+    def lens(self) -> torch.Tensor:
+        """Tokens of each row of the table (int32, on the GPU)."""
+        return self._lens[0]
+
+    def plan(self, new_lens: torch.Tensor, tokens: int, stream=None):
+        """Makes room for new_lens (max_requests, int32, on the GPU) more
+        tokens, `tokens` of them in all (more: the rest is padding).  Returns
+        (slots, positions, cu): self.status says how many tokens found no
+        page.  append() and attend() use this plan."""
+        device = self.codes.device
+        self.slots = torch.empty(tokens, dtype=torch.int32, device=device)
+        self.positions = torch.empty(tokens, dtype=torch.int32, device=device)
+        now, then = self._lens
+        fk_kv_plan(now, new_lens, self.page_size, self.free_pages, self.free_count,
+                   self.block_table, then, self.cu, self.slots, self.positions, self.free_count,
+                   self.status, ws=self._plan_ws, stream=stream)
+        self._lens = [then, now]
+        return self.slots, self.positions, self.cu
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
+        """Rows of the planned tokens, (tokens, kv_heads, head_dim)."""
+        fk_kv4_write(k, v, self.slots, self.codebook, self.codes, self.scales, stream=stream)
+
+    def attend(self, q: torch.Tensor, max_q: int, scale: float | None = None, causal: bool = True,
+               window: int = 0, lse: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+        """Attention of the planned tokens' queries (tokens, q_heads,
+        head_dim) over their requests, the planned tokens among them."""
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        fk_kv4_attention(q, self.cu, self.lens, self.block_table, self.codebook, self.codes,
+                         self.scales, out, max_q, scale=scale, causal=causal, window=window,
+                         lse=lse, ws=ws, stream=stream)
+        return out
+
+    def release(self, rows: torch.Tensor) -> None:
+        """Returns the pages of these rows of the table (int64 indices, on the
+        GPU) to the list and empties the rows."""
+        table, M = self.block_table, self.block_table.shape[1]
+        held = (self.lens[rows] + self.page_size - 1) // self.page_size
+        entries = table[rows]
+        mine = (torch.arange(M, device=table.device) < held[:, None]) & (entries >= 0)
+        # where each returned page goes; entries that are not go to a place past the list
+        at = self.free_count + mine.flatten().cumsum(0) - 1
+        pages = self.free_pages.numel()
+        longer = torch.cat((self.free_pages, self.free_pages.new_empty(1)))
+        longer[torch.where(mine.flatten(), at, pages)] = entries.flatten()
+        self.free_pages.copy_(longer[:pages])
+        self.free_count += mine.sum().int()
+        table[rows] = -1
+        self.lens[rows] = 0

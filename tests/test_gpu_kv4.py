@@ -275,6 +275,28 @@ def test_prompts_that_fill_the_card(D, dtype, window):
     attention_case([701, 1300, 64, 900], [701, 517, 64, 900], Hq, H, D, 64, dtype, True, window, seed=D)
 
 
+@pytest.mark.parametrize("dtype,D", [("f16", 64), ("bf16", 64), ("f16", 128), ("bf16", 128), ("f16", 256), ("bf16", 256)])
+@pytest.mark.parametrize("Hq,qlen", [(4, [1, 1, 1, 1, 1, 1]), (12, [3, 1, 0, 4, 2, 5]), (14, [5, 6, 1, 7, 2, 5])])
+@pytest.mark.parametrize("window", [0, 200])
+def test_shares_of_the_keys(dtype, D, Hq, qlen, window):
+    # a wide table: the keys are cut into equal shares whatever the lengths
+    attention_case([700, 33, 0, 1500, 64, 5], qlen, Hq, 2, D, 32, dtype, True, window, seed=D + Hq, extra=100)
+
+
+@pytest.mark.parametrize("dtype,D,P", [("f16", 128, 32), ("bf16", 256, 64), ("bf16", 64, 96)])
+def test_many_short_requests_of_several_rows(dtype, D, P):
+    # a wave a request and row tile
+    r = random.Random(D)
+    seq = [r.choice([0, 1, 31, 40, 200, 600]) for _ in range(180)]
+    attention_case(seq, [r.choice([1, 2, 5]) for _ in seq], 24, 3, D, P, dtype, True, r.choice([0, 70]), seed=D)
+
+
+def test_more_prompts_than_the_order_sorts():
+    r = random.Random(4)
+    seq = [r.randrange(20, 120) for _ in range(300)]
+    attention_case(seq, [s - r.choice([0, 0, 9]) for s in seq], 32, 8, 64, 32, "bf16", seed=2)
+
+
 def test_one_request_is_split_over_the_card():
     attention_case([20011], [1], 4, 1, 128, 64, "bf16", seed=1)
     attention_case([9001, 3], [2, 1], 40, 1, 256, 32, "f16", seed=2)
