@@ -121,18 +121,28 @@ def _ws_at(ws, index):
 
 def _cache(codebook, codes, scales):
     """The C description of a cache, its heads, head_dim, dtype and device."""
+    try:
+        pages, H, two, blocks, row = codes.shape
+        dtype, index = scales.dtype, codes.get_device()
+        if (codes.dtype is _u8 and two == 2 and not row % 16 and codes.is_contiguous()
+                and dtype in _HALVES and scales.shape == (pages, H, 2, 32 * blocks)
+                and scales.get_device() == index and scales.is_contiguous()
+                and codebook.dtype is _f16 and codebook.shape == (2, H, 16)
+                and codebook.get_device() == index and codebook.is_contiguous()):
+            return (_CACHE.pack(codes.data_ptr(), scales.data_ptr(), codebook.data_ptr(), pages,
+                                32 * blocks, H, row // 16, DTYPES[dtype]),
+                    H, row // 16, dtype, index)
+    except (AttributeError, TypeError, ValueError):
+        pass
+    # says what is wrong
     pages, H, two, blocks, row = _tensor(codes, "codes", 5)
     if codes.dtype is not _u8 or two != 2 or row % 16:
         raise ValueError("codes must be uint8 (pages, kv_heads, 2, page_size / 32, 16 * head_dim)")
     if not codes.is_contiguous():
         raise ValueError("codes must be contiguous")
-    if not isinstance(scales, torch.Tensor) or scales.dtype not in _HALVES:
-        _want(scales, "scales", _HALVES, (pages, H, 2, 32 * blocks), codes.device)
-    dtype, index = scales.dtype, codes.get_device()
-    s = _at(scales, "scales", dtype, (pages, H, 2, 32 * blocks), index)
-    c = _at(codebook, "codebook", _f16, (2, H, 16), index)
-    return (_CACHE.pack(codes.data_ptr(), s, c, pages, 32 * blocks, H, row // 16, DTYPES[dtype]),
-            H, row // 16, dtype, index)
+    _want(scales, "scales", _HALVES, (pages, H, 2, 32 * blocks), codes.device)
+    _want(codebook, "codebook", _f16, (2, H, 16), codes.device)
+    raise ValueError("codes, scales and codebook do not describe a cache")
 
 
 def kv_plan_workspace(B: int, device=None) -> torch.Tensor:

@@ -142,7 +142,8 @@ size_t fk_kv4_attn_workspace_bytes(const fk_kv4_cache* c, int64_t B, int64_t T, 
  * h / (q_heads / kv_heads).  out = sum_j softmax_j(scale q.k_j) v_j over the
  * positions j it sees, lse = ln sum_j exp(scale q.k_j); a query that sees
  * nothing gives zeros and -inf.  Positions in pages that the table does not
- * name (entry outside [0, pages)) or beyond max_pages are not seen.  Scores,
+ * name (entry outside [0, pages)) or beyond max_pages are not seen.  Rows of
+ * out and lse that belong to no request are not written.  Scores,
  * sums and the running maximum are fp32; the products run on fp16 matrix
  * instructions: q scaled by a power of two per row (exact for bf16, to
  * 2^-25 of the row's largest value), codebook values as they are, softmax
