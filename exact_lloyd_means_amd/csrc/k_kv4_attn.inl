@@ -741,40 +741,13 @@ __device__ inline Span split_span(const AttnArgs& a, int b, int rt, Rows& rw) {
     return tile_rows(a, rw, rt * 16 * NT, 16 * NT);
 }
 
-// Waves of a workgroup: with one column block of at most 128 dimensions four
-// waves fit a SIMD (128 registers), else two.
-template <int D, int NT>
-constexpr int kSplitWaves = NT == 1 && D <= 128 ? 8 : 4;
+// ---- group form: a few waves a (request, row tile, kv head) -----------------------
 
-// ---- whole form: one workgroup a (request, row tile, kv head) --------------------
-
-// Grid (B, row tiles x kv heads).  The waves take every W-th block; their
-// sums meet in LDS, over the table, which nobody needs by then.  Bound by the
-// chain lengths -> page -> codes -> merge: one context of 257 tokens 8.1 us.
-template <int D, int DT, int NT>
-__global__ __launch_bounds__((64 * kSplitWaves<D, NT>), (kSplitWaves<D, NT> / 2))
-void k_kv4_attn_whole(AttnArgs a) {
-    constexpr int W = kSplitWaves<D, NT>, kThreads = 64 * W;
-    extern __shared__ uint32_t tab[];
-    float2* ml = reinterpret_cast<float2*>(tab + kTabBytes / 4);  // [16 NT][W]
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int b = blockIdx.x;
-    const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y - h * a.row_tiles;
-    Rows rw;
-    const Span sp = split_span<NT>(a, b, rt, rw);
-    if (rw.n <= 0) return;
-    const bool some = sp.lo + wave < sp.hi;
-    typename Wave<D, DT, NT>::Raw raw;
-    Wave<D, DT, NT>::fetch(a, rw, h, lane, raw);
-    Walk<D> wk;
-    if (some) wk.begin(a, a.table + b * a.max_pages, h, sp.lo + wave, sp.hi, W, lane);
-    build_table(tab, a.codebook, a.Hkv, h, tid, kThreads);
-    Wave<D, DT, NT> wv;
-    wv.init(a, rw, raw, lane);
-    __syncthreads();
-    if (some) wk.run(a, wv, lane);
-    const int c = lane & 15;
+// Adds up the S waves of a group and writes their rows.  ml: [16 NT][W].
+template <int S, int W, int D, int DT, int NT>
+__device__ inline void group_merge(const AttnArgs& a, const Wave<D, DT, NT>& wv, const Rows& rw,
+                                   uint32_t* tab, float2* ml, int h, int wave, int lane) {
+    const int sub = wave & (S - 1), wave0 = wave - sub, c = lane & 15;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         float l = wv.l[t];
@@ -788,7 +761,7 @@ void k_kv4_attn_whole(AttnArgs a) {
     for (int t = 0; t < NT; ++t) {
         float top = kNoMax;
 #pragma unroll
-        for (int w = 0; w < W; ++w) top = fmaxf(top, ml[(t * 16 + c) * W + w].x);
+        for (int w = 0; w < S; ++w) top = fmaxf(top, ml[(t * 16 + c) * W + wave0 + w].x);
         const float f = __builtin_amdgcn_exp2f(wv.m[t] - top);
 #pragma unroll
         for (int p = 0; p < D / 16; ++p) {
@@ -799,18 +772,20 @@ void k_kv4_attn_whole(AttnArgs a) {
             buf[(wave * (D / 16) + p) * 64 + lane] = x;
         }
         __syncthreads();
-        for (int i = tid; i < 4 * D; i += kThreads) {
+        for (int i = sub * 64 + lane; i < 4 * D; i += 64 * S) {
             const int p = i >> 6, e = p / (D / 64), k = p % (D / 64), row = t * 16 + (i & 15);
             if (row >= rw.n) continue;
-            floatx4 x = buf[i];
+            floatx4 x = buf[wave0 * 4 * D + i];
 #pragma unroll
-            for (int w = 1; w < W; ++w) x += buf[w * 4 * D + i];
+            for (int w = 1; w < S; ++w) x += buf[(wave0 + w) * 4 * D + i];
             float most = kNoMax, sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < W; ++w) most = fmaxf(most, ml[row * W + w].x);
+            for (int w = 0; w < S; ++w) most = fmaxf(most, ml[row * W + wave0 + w].x);
 #pragma unroll
-            for (int w = 0; w < W; ++w)
-                sum += ml[row * W + w].y * __builtin_amdgcn_exp2f(ml[row * W + w].x - most);
+            for (int w = 0; w < S; ++w) {
+                const float2 y = ml[row * W + wave0 + w];
+                sum += y.y * __builtin_amdgcn_exp2f(y.x - most);
+            }
             const int r = rw.r0 + row, q = divide(r, a.G, a.G_magic), head = h * a.G + r - q * a.G;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             const int d = (4 * ((i >> 4) & 3) + e) * (D / 16) + 4 * k;
@@ -823,33 +798,43 @@ void k_kv4_attn_whole(AttnArgs a) {
     }
 }
 
-// ---- solo form: one wave a (request, row tile, kv head) ---------------------------
-
-// Grid (B / waves, row tiles x kv heads).  Bound by the longest request, 1.2 us
-// a block: 256 contexts of 16-600 tokens, 64 / 8 heads of 128, 27 us (a
-// workgroup a request 42 us: four rounds of its chain of latencies).
+// Grid (requests / groups, row tiles x kv heads).  A workgroup's W waves are
+// groups of a.group; the waves of a group take every a.group-th block of their
+// request and their sums meet in LDS, over the table, which nobody needs by
+// then.  Bound by the chain lengths -> page -> codes -> merge and the blocks of
+// the longest request: one context of 257 tokens 8.1 us (groups of 8), 256
+// contexts of 16-600, 64 / 8 heads of 128, 27 us (of 1).
 template <int D, int DT, int NT>
 __global__ __launch_bounds__((64 * kSplitWaves<D, NT>), (kSplitWaves<D, NT> / 2))
-void k_kv4_attn_solo(AttnArgs a) {
+void k_kv4_attn_group(AttnArgs a) {
     constexpr int W = kSplitWaves<D, NT>, kThreads = 64 * W;
     extern __shared__ uint32_t tab[];
+    float2* ml = reinterpret_cast<float2*>(tab + kTabBytes / 4);  // [16 NT][W]
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int b = blockIdx.x * W + wave;
+    const int S = a.group, sub = wave & (S - 1), wave0 = wave - sub;  // of the group
+    const int b = (blockIdx.x * W + wave0) / (uint32_t)S;
     const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y - h * a.row_tiles;
     Rows rw{};
     Span sp = {0, 0};
     if (b < a.B) sp = split_span<NT>(a, b, rt, rw);
+    const bool some = sp.lo + sub < sp.hi;
     typename Wave<D, DT, NT>::Raw raw;
     Wave<D, DT, NT>::fetch(a, rw, h, lane, raw);
     Walk<D> wk;
-    if (sp.hi > sp.lo) wk.begin(a, a.table + b * a.max_pages, h, sp.lo, sp.hi, 1, lane);
+    if (some) wk.begin(a, a.table + b * a.max_pages, h, sp.lo + sub, sp.hi, S, lane);
     build_table(tab, a.codebook, a.Hkv, h, tid, kThreads);
     Wave<D, DT, NT> wv;
     wv.init(a, rw, raw, lane);
     __syncthreads();
-    if (sp.hi > sp.lo) wk.run(a, wv, lane);
-    finish<D, DT, NT>(a, wv, rw, h, lane);
+    if (some) wk.run(a, wv, lane);
+    if (S == 1) {
+        finish<D, DT, NT>(a, wv, rw, h, lane);
+        return;
+    }
+    if (S == 2) group_merge<2, W, D, DT, NT>(a, wv, rw, tab, ml, h, wave, lane);
+    else if (S == 4) group_merge<4, W, D, DT, NT>(a, wv, rw, tab, ml, h, wave, lane);
+    else if constexpr (W == 8) group_merge<8, W, D, DT, NT>(a, wv, rw, tab, ml, h, wave, lane);
 }
 
 // ---- split form: shares of the keys, a wave each ----------------------------------
@@ -1078,27 +1063,21 @@ hipError_t attn_rows(const AttnArgs& a, hipStream_t s) {
 }
 
 template <int D, int DT, int NT>
-hipError_t attn_whole(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
-    static LdsAttr rec, solo_rec;
+hipError_t attn_group(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+    static LdsAttr rec;
     constexpr int W = kSplitWaves<D, NT>, lds = kTabBytes + 16 * NT * W * 8;
-    if (p.solo) {
-        auto kern = k_kv4_attn_solo<D, DT, NT>;
-        hipError_t e = ensure_lds(solo_rec, reinterpret_cast<const void*>(kern), kTabBytes);
-        if (e != hipSuccess) return e;
-        kern<<<dim3((unsigned)((a.B + W - 1) / W), (unsigned)(a.Hkv * p.row_tiles)), dim3(64 * W),
-               kTabBytes, s>>>(a);
-        return hipGetLastError();
-    }
-    auto kern = k_kv4_attn_whole<D, DT, NT>;
+    auto kern = k_kv4_attn_group<D, DT, NT>;
     hipError_t e = ensure_lds(rec, reinterpret_cast<const void*>(kern), lds);
     if (e != hipSuccess) return e;
-    kern<<<dim3((unsigned)a.B, (unsigned)(a.Hkv * p.row_tiles)), dim3(64 * W), lds, s>>>(a);
+    const int64_t each = W / p.group;  // requests a workgroup
+    kern<<<dim3((unsigned)((a.B + each - 1) / each), (unsigned)(a.Hkv * p.row_tiles)), dim3(64 * W),
+           lds, s>>>(a);
     return hipGetLastError();
 }
 
 template <int D, int DT, int NT>
 hipError_t attn_split(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
-    if (p.whole) return attn_whole<D, DT, NT>(a, p, s);
+    if (p.group) return attn_group<D, DT, NT>(a, p, s);
     static LdsAttr rec;
     auto kern = k_kv4_attn_split<D, DT, NT>;
     hipError_t e = ensure_lds(rec, reinterpret_cast<const void*>(kern), kSplitLds);

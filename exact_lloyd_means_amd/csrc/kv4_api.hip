@@ -26,15 +26,21 @@ AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q,
     p.rows = (int)(rows < tile ? rows : tile);
     // Where the table has room for few blocks a request, the longest decides,
     // and no launch that joins shares is worth its 8 us: one wave a request
-    // where they fill the card, else one workgroup.  Measured, 8 kv heads of
-    // 128, longest request in blocks, us as solo / whole / shares: 256 requests
-    // of 2: 10 / 30 / 25; 256 of 19: 27 / 42 / 39; 128 of 32: 42 / 31 / 31;
-    // 16 of 32: - / 12 / 21; 4 of 63: - / 16 / 20; 128 of 63: 84 / 48 / 45.
+    // where those alone nearly fill the card and are short, else as many as
+    // fit at once.  Measured with 8 kv heads of 128, the longest request in
+    // blocks, us as one wave / several / shares: 256 requests of 2: 10 / 13 /
+    // 24; 256 of 19: 27 / 27 / 37; 128 of 32: 42 / 26 / 30; 128 of 63: 84 / 41 /
+    // 44; 16 of 32: - / 12 / 20; 4 of 63: - / 16 / 19; 4 of 125: - / 26 / 21.
     if (p.split) {
-        p.solo = B * Hkv * tiles >= 1024 && max_blocks <= 20;
-        p.whole = p.solo || max_blocks <= 64;
+        const int W = split_waves(D, p.col_blocks);
+        const int64_t units = B * Hkv * tiles;
+        int g = W;
+        while (g > 1 && units * g > (int64_t)kResident * W) g /= 2;
+        if (units >= 1024 && max_blocks <= 20) g = 1;
+        const int64_t steps = (max_blocks + g - 1) / g;
+        if (max_blocks <= 64 && steps * (D > 128 ? 2 : 1) <= 20) p.group = g;
     }
-    if (p.split && !p.whole) {
+    if (p.split && !p.group) {
         // The join's workgroups, of 1024 / D rows at a time: about four a CU.
         const int64_t tiles_all = B * Hkv * tiles;
                 int64_t z = 1024 / tiles_all;
@@ -356,6 +362,7 @@ fk_status fk_kv4_attention(const fk_kv4_cache* c, const fk_kv4_attn* p, void* ws
     a.cap = (int32_t)(p->max_pages * c->page_size);
     a.least = plan.least;
     a.qk = p->scale * 1.4426950408889634f;
+    a.group = plan.group;
     a.row_tiles = plan.row_tiles;
     a.splits = plan.splits;
     a.part_rows = plan.rows;

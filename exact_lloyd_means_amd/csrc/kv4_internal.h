@@ -72,6 +72,7 @@ struct AttnArgs {
     int32_t cap;              // positions that the table has room for
     int32_t least;            // split form: least blocks of a share
     float qk;             // scale * log2 e
+    int32_t group;        // group form: waves of a request
     int32_t row_tiles;    // split form: tiles of query rows of one request
     int32_t splits;       // split form: workgroups per (kv head, row tile)
     int32_t part_rows;    // split form: most rows of a tile
@@ -90,12 +91,17 @@ constexpr int kTileCols = D <= 128 ? 3 : 1;
 inline int row_cols(int D) { return D == 64 ? kRowCols<64> : D == 128 ? kRowCols<128> : kRowCols<256>; }
 inline int tile_cols(int D) { return D <= 128 ? kTileCols<128> : kTileCols<256>; }
 
+// Waves of a workgroup of the forms for few rows: with one column block of at
+// most 128 dimensions four waves fit a SIMD (128 registers), else two.
+constexpr int split_waves(int D, int cols) { return cols == 1 && D <= 128 ? 8 : 4; }
+template <int D, int NT>
+constexpr int kSplitWaves = split_waves(D, NT);
+
 // Query rows of a tile (16 per matrix column block) and the form a call runs.
 struct AttnPlan {
     int col_blocks;   // split form: blocks of 16 query rows per wave
     bool split;       // row tiles of requests, else rows
-    bool whole;       // a workgroup takes a tile's keys whole, else shares
-    bool solo;        // with whole: a wave does
+    int group;        // group form: waves of a request, else 0: shares
     int row_tiles, splits;
     int rows;         // split form: most rows of a tile
     int least;        // split form: least blocks of a share

@@ -291,6 +291,14 @@ def test_many_short_requests_of_several_rows(dtype, D, P):
     attention_case(seq, [r.choice([1, 2, 5]) for _ in seq], 24, 3, D, P, dtype, True, r.choice([0, 70]), seed=D)
 
 
+@pytest.mark.parametrize("B,D,top", [(200, 64, 300), (200, 128, 640), (300, 128, 1200), (100, 256, 300)])
+def test_groups_of_two_and_four_waves(B, D, top):
+    r = random.Random(B + D)
+    seq = [r.choice([0, 1, 33, r.randrange(2, top)]) for _ in range(B)]
+    seq[B // 2] = top
+    attention_case(seq, [r.choice([1, 1, 3]) for _ in seq], 8, 4, D, 32, "f16", True, 0, seed=B)
+
+
 def test_more_prompts_than_the_order_sorts():
     r = random.Random(4)
     seq = [r.randrange(20, 120) for _ in range(300)]
