@@ -78,6 +78,13 @@ def _rows_at(t, name, dtype, shape, index):
     """Address and strides of a (tokens, heads, head_dim) tensor whose rows
     are contiguous; tokens and heads may be strided (a slice of a fused
     projection)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+            token, head, one = t.stride()
+            if one == 1:
+                return t.data_ptr(), token, head
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype is not dtype:
@@ -86,10 +93,7 @@ def _rows_at(t, name, dtype, shape, index):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, expected {_device_of(index)}")
-    token, head, one = t.stride()
-    if one != 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    return t.data_ptr(), token, head
+    raise ValueError(f"the last dimension of {name} must be contiguous")
 
 
 def _tensor(t, name, dims):
@@ -182,9 +186,12 @@ def fk_kv4_write(k, v, slots, codebook, codes, scales, stream=None) -> None:
     (T,) = one = _tensor(slots, "slots", 1)
     at = _at(slots, "slots", _i32, one, index)
     rows = (T, H, D)
-    args = (*_rows_at(k, "k", dtype, rows, index), *_rows_at(v, "v", dtype, rows, index))
+    ka, kt, kh = _rows_at(k, "k", dtype, rows, index)
+    va, vt, vh = _rows_at(v, "v", dtype, rows, index)
     _on_gpu(index)
-    _check(lib.fk_kv4_write(c, T, *args, at, _stream_of(stream, index)), "fk_kv4_write")
+    status = lib.fk_kv4_write(c, T, ka, kt, kh, va, vt, vh, at, _stream_of(stream, index))
+    if status:
+        _check(status, "fk_kv4_write")
 
 
 def fk_kv4_read(slots, codebook, codes, scales, k, v, stream=None) -> None:
