@@ -24,12 +24,14 @@
 // operand order.  A lane's v codes are an 8 x 8 tile (token, dimension) of
 // nibbles that is transposed in registers, half an instruction a value.
 //
-// Running maximum: kept per query row and raised only when a score exceeds
-// it by 8 (p <= 256 in between), so that most blocks need no reduction over
-// lanes and no rescaling; l is summed over lanes at the end.  m also contains
-// the log2 of a power of two, the unit of v's scales, which follows the
-// largest scale met, so that w stays in fp16's range whatever the scales; it
-// scales O and l alike and cancels.
+// m follows what a row adds up, not its scores alone: it is 3 below the log2 of
+// the row's largest p * v scale when it is set, and is raised only when a
+// weight could pass 2^15, so that most blocks need no reduction over lanes and
+// no rescaling.  A row's largest weight is therefore 8 or more, all are in
+// fp16's range, and rounding costs a weight 2^-11 of itself or 2^-28 of the
+// row's largest, whatever the scales of tokens that the row hardly counts or
+// does not see.  m scales O and l alike and cancels; l is summed over lanes at
+// the end, in fp32.
 #pragma once
 
 #include "kv4_internal.h"
@@ -42,7 +44,12 @@ constexpr int kAttnWaves = 4;
 constexpr int kTabBytes = 65536;
 constexpr int kSplitLds = kTabBytes + 512;  // and what the waves tell each other
 constexpr float kNoMax = -1e30f;   // running maximum before any key
-constexpr float kSlack = 8.f;      // how far a score may exceed it, log2
+constexpr float kFirst = 3.f;      // log2 of a row's largest weight when m is set
+constexpr float kRoom = 4.f;       // log2 of the room above a block's largest v scale
+constexpr float kTop = 15.f;       // log2 of the largest weight
+// v scales below 2^-93 count as that in m, and no p passes 2^96.5, so that l
+// stays finite over 2^31 tokens whose v is zero.
+constexpr float kLeastScale = -93.f, kMostP = 96.5f;
 
 typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
 
@@ -259,8 +266,10 @@ struct Wave {
     floatx4 o[NT][kDb];
     float m[NT], l[NT], qs[NT];
     int lo[NT], hi[NT];  // positions the lane's query row sees
-    uint32_t limit;  // 2^6 units, bits of the cache dtype in both halves
-    float slack;  // kSlack less log2 of the v scales' unit, which m contains
+    // v scales up to `limit` (bits of the cache dtype in both halves) times p up
+    // to 2^slack give weights up to 2^kTop
+    uint32_t limit;
+    float slack;
     int inner_lo, inner_hi;  // positions every row of the wave sees
 
     // The tile's query rows as they are (n may be <= 0), a lane's quarter of
@@ -320,8 +329,8 @@ struct Wave {
 #pragma unroll
             for (int i = 0; i < kDb; ++i) o[t][i] = floatx4{0, 0, 0, 0};
         }
-        slack = kSlack;
-        limit = 0;  // the first scale sets the unit
+        slack = kMostP;
+        limit = 0;  // the first block sets them
         // bounds grow with the row, so the first and last rows tell
         inner_lo = 0;
         inner_hi = 0x7fffffff;
@@ -422,29 +431,32 @@ struct Wave {
             top[t] = max2(x, s[1][t][3]);
         }
         blk.load_k(next);
-        // raise the maxima by more than kSlack, keep v's scales below 2^6 units
+        // a weight might pass 2^kTop: by bounds, largest score and largest scale
         const uint32_t bits = max_u16(max_u16(vw[0], vw[1]), max_u16(vw[2], vw[3]));
         bool raise = max_u16(bits, limit) != limit;
 #pragma unroll
         for (int t = 0; t < NT; ++t) raise |= fmaf(top[t], qs[t], -m[t]) > slack;
         if (__any(raise)) {
-            float big = vs[0];
+            // the bounds of this block's scales, then m by the weights themselves
+            float big = vs[0], most[NT];
 #pragma unroll
             for (int j = 1; j < 8; ++j) big = fmaxf(big, vs[j]);
             big = max_groups(big);
-            // log2 of the unit: of the power of two below the largest scale,
-            // down to 2^-96 (l holds its inverse)
-            const float old = kSlack - slack;
-            float unit = old;
             const int e = (int)(__builtin_bit_cast(uint32_t, big) >> 23 & 0xff) - 127;
-            if (big > 0.f && (limit == 0 || (float)(e - 6) >= old)) {
-                unit = (float)(e < -96 ? -96 : e);
-                limit = pow2_bits<DT>((int)unit + 6);
-                slack = kSlack - unit;
+            limit = big > 0.f ? pow2_bits<DT>(e + (int)kRoom) : 0;
+            slack = fminf(kTop - kRoom - (float)e, kMostP);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) most[t] = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float lv = fmaxf(__builtin_amdgcn_logf(vs[j]), kLeastScale);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    most[t] = fmaxf(most[t], fmaf(s[j >> 2][t][j & 3], qs[t], lv));
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const float nm = fmaxf(m[t] - old, max_groups(top[t] * qs[t])) + unit;
+                const float nm = fmaxf(m[t], max_groups(most[t]) - kFirst);
                 const float x = __builtin_amdgcn_exp2f(m[t] - nm);
                 m[t] = nm;
                 l[t] *= x;

@@ -145,9 +145,12 @@ size_t fk_kv4_attn_workspace_bytes(const fk_kv4_cache* c, int64_t B, int64_t T, 
  * name (entry outside [0, pages)) or beyond max_pages are not seen.  Rows of
  * out and lse that belong to no request are not written.  Scores,
  * sums and the running maximum are fp32; the products run on fp16 matrix
- * instructions: q scaled by a power of two per row (exact for bf16, to
- * 2^-25 of the row's largest value), codebook values as they are, softmax
- * weights times v's scale rounded to fp16 once.
+ * instructions: q scaled by a power of two per row (exact for values down to
+ * 2^-14 of the row's largest, in bf16 to 2^-17; below that to 2^-25 of the
+ * largest), codebook values as they are, softmax weights times v's scale
+ * rounded to fp16 once: to 2^-11 of the weight, or 2^-28 of the largest of
+ * its row where that is more.  v scales below 2^-96 or above 2^40, which only
+ * bf16 holds, may cost more.
  * Results do not depend on timing.  B <= 2^20, q_heads / kv_heads <= 256, T *
  * q_heads / kv_heads <= 2^24, B * max_pages * page_size < 2^36.
  */
