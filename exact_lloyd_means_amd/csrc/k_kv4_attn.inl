@@ -90,10 +90,12 @@ __device__ inline void bounds(const AttnArgs& a, const Rows& rw, int i, int& lo,
     lo = lo > hi ? hi : lo;
 }
 
-// Rows r0 .. of the request in tiles of `rows`, and the blocks they see.
+// Rows r0 .. of the request in tiles of `rows`, and the blocks they see.  Query
+// tokens from max_q on have no rows: tiles and workspace are laid out for max_q,
+// and what cu says is only known here.
 __device__ inline Span tile_rows(const AttnArgs& a, Rows& rw, int r0, int rows) {
     rw.r0 = r0;
-    const int left = rw.qlen * a.G - r0;
+    const int left = (rw.qlen < a.max_q ? rw.qlen : a.max_q) * a.G - r0;
     rw.n = left < 0 ? 0 : left > rows ? rows : left;
     if (rw.n <= 0) return {0, 0};
     int lo, hi, t0, t1;

@@ -326,8 +326,8 @@ fk_status fk_kv4_attention(const fk_kv4_cache* c, const fk_kv4_attn* p, void* ws
     FK_CHECK(need(p->block_table, "block_table", 4));
     FK_CHECK(need(p->out, "out", 16));
     if (p->lse) FK_CHECK(need(p->lse, "lse", 4));
-    const AttnPlan plan = plan_attention(p->B, p->T, p->q_heads, c->kv_heads, c->head_dim,
-                                         clamp_max_q(p->T, p->max_q),
+    const int max_q = clamp_max_q(p->T, p->max_q);
+    const AttnPlan plan = plan_attention(p->B, p->T, p->q_heads, c->kv_heads, c->head_dim, max_q,
                                          p->max_pages * (c->page_size / kKvBlock));
     if (!ws) return fail(FK_EWORKSPACE, "workspace is NULL");
     if (!aligned(ws, 16)) return fail(FK_EINVAL, "workspace is not 16-byte aligned");
@@ -355,6 +355,7 @@ fk_status fk_kv4_attention(const fk_kv4_cache* c, const fk_kv4_attn* p, void* ws
     a.page_size = c->page_size;
     a.causal = p->causal;
     a.window = p->window;
+    a.max_q = max_q;
     a.q_vec = vec_rows(p->q, p->q_token, p->q_head);
     a.bpp = (uint32_t)(c->page_size / kKvBlock);
     a.bpp_magic = division_magic(a.bpp);

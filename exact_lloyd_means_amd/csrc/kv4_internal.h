@@ -66,6 +66,7 @@ struct AttnArgs {
     int64_t q_token, q_head, T, max_pages;
     int64_t pages;
     int32_t B, Hq, Hkv, G, page_size, causal, window;
+    int32_t max_q;        // most query tokens of a request; more are left out
     int32_t q_vec;        // q rows can be read 16 bytes at a time
     uint32_t bpp, bpp_magic;  // blocks per page; ceil(2^32 / bpp)
     uint32_t G_magic;         // ceil(2^32 / G)

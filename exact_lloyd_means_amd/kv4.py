@@ -221,7 +221,8 @@ def fk_kv4_attention(q, cu_q, seq_lens, block_table, codebook, codes, scales, ou
     """Attention of the query tokens q (T, q_heads, head_dim), request b's at
     cu_q[b] .. cu_q[b + 1] - 1, over the cached tokens of their requests; out
     like q, contiguous; lse (T, q_heads) fp32 or None; scale None: 1 /
-    sqrt(head_dim)."""
+    sqrt(head_dim).  max_q: most query tokens of a request, or more; those
+    from max_q on get no rows of out and lse."""
     c, H, D, dtype, index = _cache(codebook, codes, scales)
     T, Hq, _ = _tensor(q, "q", 3)
     rows = (T, Hq, D)

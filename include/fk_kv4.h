@@ -117,7 +117,8 @@ typedef struct fk_kv4_attn {
     int64_t B;             /* requests */
     int64_t T;             /* query tokens of all requests */
     int32_t q_heads;       /* a multiple of kv_heads */
-    int32_t max_q;         /* most query tokens of one request, or more */
+    int32_t max_q;         /* most query tokens of one request, or more;
+                              those of a request from max_q on are left out */
     int64_t max_pages;     /* row length of block_table */
     int64_t q_token, q_head; /* strides of q in elements */
     const void* q;         /* (T, q_heads, head_dim) in the cache dtype */
@@ -143,7 +144,8 @@ size_t fk_kv4_attn_workspace_bytes(const fk_kv4_cache* c, int64_t B, int64_t T, 
  * positions j it sees, lse = ln sum_j exp(scale q.k_j); a query that sees
  * nothing gives zeros and -inf.  Positions in pages that the table does not
  * name (entry outside [0, pages)) or beyond max_pages are not seen.  Rows of
- * out and lse that belong to no request are not written.  Scores,
+ * out and lse that belong to no request, or to query tokens i >= max_q, are
+ * not written.  Scores,
  * sums and the running maximum are fp32; the products run on fp16 matrix
  * instructions: q scaled by a power of two per row (exact for values down to
  * 2^-14 of the row's largest, in bf16 to 2^-17; below that to 2^-25 of the
