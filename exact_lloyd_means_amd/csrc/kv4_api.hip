@@ -65,8 +65,8 @@ AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q,
         // A share's results are rows x D fp32, a block's codes and scales 32 D +
         // 128 bytes: at least a block for every two rows.
         p.least = p.rows / 2;
-        const size_t parts =
-            (size_t)Hkv * p.row_tiles * p.splits * 8 * 2 * (size_t)p.rows;
+        const size_t waves = (size_t)p.splits * split_waves(D, p.col_blocks);
+        const size_t parts = (size_t)Hkv * p.row_tiles * waves * 2 * (size_t)p.rows;
         size_t o = 0;
         p.part_o = o;
         o = align256(o + parts * D * sizeof(float));
