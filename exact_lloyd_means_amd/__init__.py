@@ -9,6 +9,7 @@ Importing this package loads libfk.so and fails loudly when it is missing.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -155,6 +156,18 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
+def _on(stream, dev):
+    """Context in which torch allocates on `stream` and runs there (None: the
+    current stream).  Memory that a call takes for itself must belong to the
+    stream that uses it: torch gives a freed block to the next allocation of
+    the stream that the block was made on, and waits for no other."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    return torch.cuda.stream(stream)
+
+
 def _problem_from(X: torch.Tensor, K: int, deterministic: bool = False) -> Problem:
     if not isinstance(X, torch.Tensor):
         raise TypeError("X must be a torch tensor")
@@ -181,6 +194,11 @@ def workspace(p: Problem, device=None, chunk_points: int = 0) -> torch.Tensor:
     """A caller-owned device workspace of the required size (allocated by torch)."""
     return torch.empty(workspace_size(p, chunk_points), dtype=torch.uint8,
                        device=device or "cuda")
+
+
+def _workspace_on(stream, p: Problem, dev, chunk_points: int = 0) -> torch.Tensor:
+    with _on(stream, dev):
+        return workspace(p, dev, chunk_points)
 
 
 def fk_centroid_bias(C: torch.Tensor, bias: torch.Tensor, stream=None) -> None:
@@ -214,7 +232,7 @@ def fk_assign(X: torch.Tensor, C: torch.Tensor, labels: torch.Tensor,
     p, dev = _assign_args(X, C, labels, min_dist)
     _want_ws(ws, dev)
     _need_gpu(dev)
-    ws = workspace(p, dev) if ws is None else ws
+    ws = _workspace_on(stream, p, dev) if ws is None else ws
     _check(lib.fk_assign(ctypes.byref(p), _ptr(X), _ptr(C), _ptr(labels), _ptr(min_dist),
                          _ptr(ws), ws.numel(), _stream(stream)), "fk_assign")
 
@@ -244,7 +262,7 @@ def fk_sort_labels(labels: torch.Tensor, K: int, counts: torch.Tensor, offsets: 
     _want_ws(ws, dev)
     _need_gpu(dev)
     p = problem(B, N, K, d, dtype, deterministic)
-    ws = workspace(p, dev) if ws is None else ws
+    ws = _workspace_on(stream, p, dev) if ws is None else ws
     _check(lib.fk_sort_labels(ctypes.byref(p), _ptr(labels), _ptr(counts), _ptr(offsets),
                               _ptr(sorted_idx), _ptr(ws), ws.numel(), _stream(stream)),
            "fk_sort_labels")
@@ -271,7 +289,7 @@ def fk_update(X: torch.Tensor, labels: torch.Tensor, C_prev: torch.Tensor, C_nex
     p, dev = _update_args(X, labels, C_prev, C_next, C_next_lowp, counts, deterministic)
     _want_ws(ws, dev)
     _need_gpu(dev)
-    ws = workspace(p, dev) if ws is None else ws
+    ws = _workspace_on(stream, p, dev) if ws is None else ws
     _check(lib.fk_update(ctypes.byref(p), _ptr(X), _ptr(labels), _ptr(C_prev), _ptr(C_next),
                          _ptr(C_next_lowp), _ptr(counts), _ptr(ws), ws.numel(),
                          _stream(stream)), "fk_update")
@@ -286,7 +304,7 @@ def fk_update_bias(X: torch.Tensor, labels: torch.Tensor, C_prev: torch.Tensor,
     _want(bias_next, "bias_next", torch.float32, (p.B, p.K), dev)
     _want_ws(ws, dev)
     _need_gpu(dev)
-    ws = workspace(p, dev) if ws is None else ws
+    ws = _workspace_on(stream, p, dev) if ws is None else ws
     _check(lib.fk_update_bias(ctypes.byref(p), _ptr(X), _ptr(labels), _ptr(C_prev), _ptr(C_next),
                               _ptr(C_next_lowp), _ptr(counts), _ptr(bias_next), _ptr(ws),
                               ws.numel(), _stream(stream)), "fk_update_bias")
@@ -328,7 +346,7 @@ def fk_lloyd(X: torch.Tensor, C: torch.Tensor, labels: torch.Tensor, counts: tor
     p, dev = _lloyd_args(X, C, labels, counts, deterministic)
     _want_ws(ws, dev)
     _need_gpu(dev)
-    ws = workspace(p, dev) if ws is None else ws
+    ws = _workspace_on(stream, p, dev) if ws is None else ws
     n = ctypes.c_int(0)
     _check(lib.fk_lloyd(ctypes.byref(p), _ptr(X), _ptr(C), _ptr(labels), _ptr(counts),
                         int(max_iters), float(tol), ctypes.byref(n) if want_n_iter else None,
@@ -347,7 +365,7 @@ def fk_lloyd_streamed(X_host: torch.Tensor, C: torch.Tensor, labels: torch.Tenso
         raise ValueError("X_host must be a pinned CPU tensor (pin_memory=True)")
     _want_ws(ws, dev)
     _need_gpu(dev)
-    ws = workspace(p, dev, chunk_points) if ws is None else ws
+    ws = _workspace_on(compute_stream, p, dev, chunk_points) if ws is None else ws
     cs = _stream(compute_stream)
     xs = _stream(copy_stream) if copy_stream is not None else cs
     _check(lib.fk_lloyd_streamed(ctypes.byref(p), _ptr(X_host), int(chunk_points), _ptr(C),

@@ -20,22 +20,26 @@ from __future__ import annotations
 
 import torch
 
-from . import fk_assign, fk_lloyd, fk_sort_labels
+from . import _on, fk_assign, fk_lloyd, fk_sort_labels
 
 __all__ = ["batch_kmeans_euclid", "KMeans", "initial_centroids"]
 
 
-def _as_batched(X: torch.Tensor) -> tuple[torch.Tensor, bool]:
+def _check_points(X: torch.Tensor) -> None:
     if not isinstance(X, torch.Tensor):
         raise TypeError("X must be a torch tensor")
     if X.device.type != "cuda":
         raise ValueError("X must be on the GPU")
     if X.dtype not in (torch.float32, torch.float16, torch.bfloat16):
         raise ValueError("X must be float32, float16 or bfloat16")
+    if X.dim() not in (2, 3):
+        raise ValueError("X must be (N, d) or (B, N, d)")
+
+
+def _as_batched(X: torch.Tensor) -> tuple[torch.Tensor, bool]:
+    _check_points(X)
     if X.dim() == 2:
         return X.unsqueeze(0).contiguous(), True
-    if X.dim() != 3:
-        raise ValueError("X must be (N, d) or (B, N, d)")
     return X.contiguous(), False
 
 
@@ -73,20 +77,24 @@ def batch_kmeans_euclid(X: torch.Tensor, n_clusters: int, max_iter: int = 100, t
     """Exact Lloyd k-means on each of the B problems of X (B, N, d).
 
     deterministic: the library's FK_DETERMINISTIC mode (bit-identical results
-    on every run).  Returns (labels (B, N) int32 of the last
+    on every run).  stream: where everything runs, what torch does included;
+    X must be ready there, and the results belong to it (None: the current
+    stream).  Returns (labels (B, N) int32 of the last
     assignment, centroids (B, K, d) fp32 after the last update, number of
     iterations run)."""
-    Xb, _ = _as_batched(X)
+    _check_points(X)
     if max_iter < 1:
         raise ValueError("max_iter must be >= 1")
     if tol < 0:
         raise ValueError("tol must be >= 0")
-    B, N, d = Xb.shape
-    C = initial_centroids(Xb, n_clusters, init, seed)
-    labels = torch.empty((B, N), dtype=torch.int32, device=Xb.device)
-    counts = torch.empty((B, C.shape[1]), dtype=torch.int32, device=Xb.device)
-    n = fk_lloyd(Xb, C, labels, counts, int(max_iter), float(tol), want_n_iter=tol > 0,
-                 stream=stream, deterministic=deterministic)
+    with _on(stream, X.device):
+        Xb, _ = _as_batched(X)
+        B, N, d = Xb.shape
+        C = initial_centroids(Xb, n_clusters, init, seed)
+        labels = torch.empty((B, N), dtype=torch.int32, device=Xb.device)
+        counts = torch.empty((B, C.shape[1]), dtype=torch.int32, device=Xb.device)
+        n = fk_lloyd(Xb, C, labels, counts, int(max_iter), float(tol), want_n_iter=tol > 0,
+                     stream=stream, deterministic=deterministic)
     return labels, C, (n if tol > 0 else int(max_iter))
 
 
