@@ -16,7 +16,9 @@ include/fk_kv4.h, which only check and marshal their tensors, and
     cache.append(k, v)                         # (tokens, kv_heads, head_dim)
     out = cache.attend(q, max_q)               # (tokens, q_heads, head_dim)
 
-Nothing here waits for the GPU.
+Nothing here waits for the GPU.  With stream= a call runs there, and what it
+allocates, its results among them, belongs to that stream; its inputs must be
+ready there.
 """
 from __future__ import annotations
 
@@ -26,7 +28,7 @@ import struct
 
 import torch
 
-from . import DTYPES, _check, _need_gpu, _P, _stream, _want, _want_ws, lib
+from . import DTYPES, _check, _need_gpu, _on, _P, _stream, _want, _want_ws, lib
 
 __all__ = ["KV4Cache", "learn_codebook", "fk_kv_plan", "fk_kv4_write", "fk_kv4_read", "fk_kv4_attention", "kv_plan_workspace",
            "kv4_attention_workspace"]
@@ -176,7 +178,8 @@ def fk_kv_plan(ctx_lens, new_lens, page_size: int, free_pages, free_count, block
             _at(free_left, "free_left", _i32, (1,), index), _at(status, "status", _i32, (4,), index))
     _on_gpu(index)
     if ws is None:
-        ws = kv_plan_workspace(B, ctx_lens.device)
+        with _on(stream, ctx_lens.device):
+            ws = kv_plan_workspace(B, ctx_lens.device)
     _check(lib.fk_kv_plan(*args, *_ws_at(ws, index), _stream_of(stream, index)), "fk_kv_plan")
 
 
@@ -238,7 +241,8 @@ def fk_kv4_attention(q, cu_q, seq_lens, block_table, codebook, codes, scales, ou
         0 if lse is None else _at(lse, "lse", torch.float32, (T, Hq), index))
     _on_gpu(index)
     if ws is None:
-        ws = kv4_attention_workspace(q, seq_lens, codes, max_q)
+        with _on(stream, codes.device):
+            ws = kv4_attention_workspace(q, seq_lens, codes, max_q)
     _check(lib.fk_kv4_attention(c, args, *_ws_at(ws, index), _stream_of(stream, index)),
            "fk_kv4_attention")
 
@@ -267,7 +271,8 @@ class KV4Cache:
     pages x page_size tokens are shared by max_requests rows of a block table
     with room for max_len tokens each.  A step is plan(), append(), attend();
     release() returns a row's pages.  Lengths, tables and the list of free
-    pages live on the GPU and no call waits for it."""
+    pages live on the GPU and no call waits for it.  The calls follow each
+    other on one stream; a caller that changes streams orders them."""
 
     def __init__(self, pages: int, page_size: int, kv_heads: int, head_dim: int,
                  codebook: torch.Tensor, max_requests: int, max_len: int,
@@ -304,8 +309,9 @@ class KV4Cache:
         (slots, positions, cu): self.status says how many tokens found no
         page.  append() and attend() use this plan."""
         device = self.codes.device
-        self.slots = torch.empty(tokens, dtype=torch.int32, device=device)
-        self.positions = torch.empty(tokens, dtype=torch.int32, device=device)
+        with _on(stream, device):
+            self.slots = torch.empty(tokens, dtype=torch.int32, device=device)
+            self.positions = torch.empty(tokens, dtype=torch.int32, device=device)
         now, then = self._lens
         fk_kv_plan(now, new_lens, self.page_size, self.free_pages, self.free_count,
                    self.block_table, then, self.cu, self.slots, self.positions, self.free_count,
@@ -322,15 +328,20 @@ class KV4Cache:
                stream=None) -> torch.Tensor:
         """Attention of the planned tokens' queries (tokens, q_heads,
         head_dim) over their requests, the planned tokens among them."""
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        with _on(stream, q.device):
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         fk_kv4_attention(q, self.cu, self.lens, self.block_table, self.codebook, self.codes,
                          self.scales, out, max_q, scale=scale, causal=causal, window=window,
                          lse=lse, ws=ws, stream=stream)
         return out
 
-    def release(self, rows: torch.Tensor) -> None:
+    def release(self, rows: torch.Tensor, stream=None) -> None:
         """Returns the pages of these rows of the table (int64 indices, on the
         GPU) to the list and empties the rows."""
+        with _on(stream, self.codes.device):
+            self._release(rows)
+
+    def _release(self, rows: torch.Tensor) -> None:
         table, M = self.block_table, self.block_table.shape[1]
         held = (self.lens[rows] + self.page_size - 1) // self.page_size
         entries = table[rows]
