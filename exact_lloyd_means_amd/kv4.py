@@ -252,17 +252,26 @@ def learn_codebook(k, v, iters: int = 30, stream=None) -> torch.Tensor:
     kv_heads, head_dim) on the GPU: exact Lloyd k-means (K = 16, d = 1, one
     problem a head, k and v) on the values over their row's largest
     magnitude, from equally spaced levels, in the library's deterministic
-    mode.  Preparing the values is done with torch."""
+    mode.  Preparing the values is done with torch, on `stream` too, which
+    waits for the current stream first and is waited for by it at the end."""
     from .api import batch_kmeans_euclid
     T, H, D = _tensor(k, "k", 3)
-    if v.shape != k.shape:
+    if _tensor(v, "v", 3) != k.shape:
         raise ValueError(f"v must have shape {tuple(k.shape)}, got {tuple(v.shape)}")
-    x = torch.stack((k, v)).float()
-    x = x / x.abs().amax(-1, keepdim=True).clamp(min=torch.finfo(torch.float32).tiny)
-    x = x.permute(0, 2, 1, 3).reshape(2 * H, T * D, 1).contiguous()
-    first = torch.linspace(-1, 1, 16, device=x.device).view(16, 1)
-    _, c, _ = batch_kmeans_euclid(x, 16, iters, init=first, deterministic=True, stream=stream)
-    return c.view(2, H, 16).sort(-1).values.half().contiguous()
+    _on_gpu(k.get_device())
+    here = torch.cuda.current_stream(k.device)
+    with _on(stream, k.device):
+        there = torch.cuda.current_stream(k.device)
+        there.wait_stream(here)
+        x = torch.stack((k, v)).float()
+        x = x / x.abs().amax(-1, keepdim=True).clamp(min=torch.finfo(torch.float32).tiny)
+        x = x.permute(0, 2, 1, 3).reshape(2 * H, T * D, 1).contiguous()
+        first = torch.linspace(-1, 1, 16, device=x.device).view(16, 1)
+        _, c, _ = batch_kmeans_euclid(x, 16, iters, init=first, deterministic=True, stream=stream)
+        c = c.view(2, H, 16).sort(-1).values.half().contiguous()
+    here.wait_stream(there)
+    c.record_stream(here)
+    return c
 
 
 class KV4Cache:

@@ -98,3 +98,21 @@ def test_a_serving_loop_on_a_side_stream():
     assert all(torch.equal(a, b) for a, b in zip(want, got))
     for name in ("block_table", "free_count", "lens", "codes", "scales"):
         assert torch.equal(getattr(cache, name), getattr(plain, name)), name
+
+
+@pytest.mark.parametrize("busy", ["current", "side"])
+@pytest.mark.parametrize("handle", [False, True])
+def test_codebook_learned_on_a_side_stream(handle, busy):
+    # samples still being made by the current stream, or the side stream behind
+    # with other work: the result is the same, and ready for the current stream
+    side = torch.cuda.Stream()
+    g = torch.Generator("cuda").manual_seed(3)
+    k, v = (torch.randn(500, H, D, device="cuda", generator=g).bfloat16() for _ in range(2))
+    want = fk.learn_codebook(k, v, iters=5)
+    torch.cuda.synchronize()
+    stall(side if busy == "side" else torch.cuda.current_stream())
+    k2, v2 = k * 2, v * 2                            # the same over each row's largest
+    got = fk.learn_codebook(k2, v2, iters=5, stream=side.cuda_stream if handle else side)
+    del k2, v2
+    Bystanders([500 * H * D * 2])
+    assert torch.equal(got, want)
