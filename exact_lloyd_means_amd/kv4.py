@@ -252,8 +252,9 @@ def learn_codebook(k, v, iters: int = 30, stream=None) -> torch.Tensor:
     kv_heads, head_dim) on the GPU: exact Lloyd k-means (K = 16, d = 1, one
     problem a head, k and v) on the values over their row's largest
     magnitude, from equally spaced levels, in the library's deterministic
-    mode.  Preparing the values is done with torch, on `stream` too, which
-    waits for the current stream first and is waited for by it at the end."""
+    mode.  A row with a value that is not finite counts as zeros.  Preparing
+    the values is done with torch, on `stream` too, which waits for the current
+    stream first and is waited for by it at the end."""
     from .api import batch_kmeans_euclid
     T, H, D = _tensor(k, "k", 3)
     if _tensor(v, "v", 3) != k.shape:
@@ -264,7 +265,8 @@ def learn_codebook(k, v, iters: int = 30, stream=None) -> torch.Tensor:
         there = torch.cuda.current_stream(k.device)
         there.wait_stream(here)
         x = torch.stack((k, v)).float()
-        x = x / x.abs().amax(-1, keepdim=True).clamp(min=torch.finfo(torch.float32).tiny)
+        most = x.abs().amax(-1, keepdim=True)
+        x = torch.where(most < math.inf, x / most.clamp(min=torch.finfo(torch.float32).tiny), 0.0)
         x = x.permute(0, 2, 1, 3).reshape(2 * H, T * D, 1).contiguous()
         first = torch.linspace(-1, 1, 16, device=x.device).view(16, 1)
         _, c, _ = batch_kmeans_euclid(x, 16, iters, init=first, deterministic=True, stream=stream)
