@@ -147,8 +147,10 @@ __global__ __launch_bounds__(N) void k_plan_scan(PlanArgs a) {
                 // tokens past the last of them
                 const uint32_t rest = n > p ? n - p : 0, got = rest < need[e] ? rest : need[e];
                 const int64_t end = ((held[e] < M ? held[e] : M) + got) * (int64_t)P;
-                const int64_t miss = (int64_t)ctx[e] + fresh[e] - (end > ctx[e] ? end : ctx[e]);
+                const int64_t room = end > ctx[e] ? end : ctx[e];
+                const int64_t miss = (int64_t)ctx[e] + fresh[e] - room;
                 lost = add(lost, miss > 0 ? (uint32_t)miss : 0);
+                if (a.kept) a.kept[b] = sat(miss > 0 ? room : (int64_t)ctx[e] + fresh[e]);
             }
             t = add(t, fresh[e]);
             p = add(p, need[e]);

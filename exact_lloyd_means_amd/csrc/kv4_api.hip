@@ -212,6 +212,17 @@ fk_status fk_kv_plan(int64_t B, int64_t max_pages, int32_t page_size, const int3
                      int32_t* cu_new, int32_t* slots, int32_t* positions, int64_t slot_cap,
                      int32_t* free_left, int32_t* status, void* ws, size_t ws_bytes,
                      void* stream) {
+    return fk_kv_plan_kept(B, max_pages, page_size, ctx_lens, new_lens, free_pages, free_cap,
+                           free_count, block_table, seq_lens, cu_new, slots, positions, slot_cap,
+                           free_left, status, nullptr, ws, ws_bytes, stream);
+}
+
+fk_status fk_kv_plan_kept(int64_t B, int64_t max_pages, int32_t page_size, const int32_t* ctx_lens,
+                          const int32_t* new_lens, const int32_t* free_pages, int64_t free_cap,
+                          const int32_t* free_count, int32_t* block_table, int32_t* seq_lens,
+                          int32_t* cu_new, int32_t* slots, int32_t* positions, int64_t slot_cap,
+                          int32_t* free_left, int32_t* status, int32_t* kept_lens, void* ws,
+                          size_t ws_bytes, void* stream) {
     FK_CHECK(check_requests(B));
     FK_CHECK(check_page_size(page_size));
     if (max_pages < 1 || free_cap < 0 || slot_cap < 0)
@@ -229,6 +240,7 @@ fk_status fk_kv_plan(int64_t B, int64_t max_pages, int32_t page_size, const int3
     if (positions) FK_CHECK(need(positions, "positions", 4));
     FK_CHECK(need(free_left, "free_left", 4));
     FK_CHECK(need(status, "status", 4));
+    if (kept_lens) FK_CHECK(need(kept_lens, "kept_lens", 4));
     if (!ws) return fail(FK_EWORKSPACE, "workspace is NULL");
     if (!aligned(ws, 16)) return fail(FK_EINVAL, "workspace is not 16-byte aligned");
     const size_t bytes = fk_kv_plan_workspace_bytes(B);
@@ -251,6 +263,7 @@ fk_status fk_kv_plan(int64_t B, int64_t max_pages, int32_t page_size, const int3
     a.pos = positions;
     a.free_left = free_left;
     a.status = status;
+    a.kept = kept_lens;
     a.ws = static_cast<int32_t*>(ws);
     const hipError_t e = launch_kv_plan(a, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? FK_OK : hip_fail(e, "fk_kv_plan");

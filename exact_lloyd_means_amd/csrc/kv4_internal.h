@@ -36,6 +36,7 @@ struct PlanArgs {
     int32_t page_size;
     const int32_t *ctx, *fresh, *free_pages, *free_count;
     int32_t *table, *seq, *cu, *slots, *pos, *free_left, *status;
+    int32_t* kept;  // [B] or null
     int32_t* ws;  // [B] first needed page of each request, then the list's length
 };
 hipError_t launch_kv_plan(const PlanArgs& a, hipStream_t s);

@@ -44,6 +44,8 @@ for _name, (_args, _res) in {
     "fk_kv_plan_workspace_bytes": ([_I64], _SZ),
     "fk_kv_plan": ([_I64, _I64, _I32, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _P,
                     _SZ, _P], ctypes.c_int),
+    "fk_kv_plan_kept": ([_I64, _I64, _I32, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _P,
+                         _P, _P, _SZ, _P], ctypes.c_int),
     "fk_kv4_write": ([_P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P], ctypes.c_int),
     "fk_kv4_read": ([_P, _I64, _P, _P, _P, _P], ctypes.c_int),
     "fk_kv4_attn_workspace_bytes": ([_P, _I64, _I64, _I32, _I32], _SZ),
@@ -158,11 +160,14 @@ def kv_plan_workspace(B: int, device=None) -> torch.Tensor:
 
 
 def fk_kv_plan(ctx_lens, new_lens, page_size: int, free_pages, free_count, block_table, seq_lens,
-               cu_new, slots, positions, free_left, status, ws=None, stream=None) -> None:
+               cu_new, slots, positions, free_left, status, ws=None, stream=None,
+               kept_lens=None) -> None:
     """Block tables and slot maps of one step from the lengths on the GPU
     (all int32): writes the needed entries of block_table (B, max_pages),
     seq_lens (B), cu_new (B + 1), slots and positions (any length; positions
-    may be None), free_left (1) and status (4)."""
+    may be None), free_left (1), status (4) and, unless None, kept_lens (B):
+    what the cache then holds, the next step's ctx_lens (seq_lens unless pages
+    ran out)."""
     (B,) = one = _tensor(ctx_lens, "ctx_lens", 1)
     table = _tensor(block_table, "block_table", 2)
     free = _tensor(free_pages, "free_pages", 1)
@@ -175,12 +180,13 @@ def fk_kv_plan(ctx_lens, new_lens, page_size: int, free_pages, free_count, block
             _at(seq_lens, "seq_lens", _i32, one, index), _at(cu_new, "cu_new", _i32, (B + 1,), index),
             _at(slots, "slots", _i32, cap, index),
             None if positions is None else _at(positions, "positions", _i32, cap, index), cap[0],
-            _at(free_left, "free_left", _i32, (1,), index), _at(status, "status", _i32, (4,), index))
+            _at(free_left, "free_left", _i32, (1,), index), _at(status, "status", _i32, (4,), index),
+            None if kept_lens is None else _at(kept_lens, "kept_lens", _i32, one, index))
     _on_gpu(index)
     if ws is None:
         with _on(stream, ctx_lens.device):
             ws = kv_plan_workspace(B, ctx_lens.device)
-    _check(lib.fk_kv_plan(*args, *_ws_at(ws, index), _stream_of(stream, index)), "fk_kv_plan")
+    _check(lib.fk_kv_plan_kept(*args, *_ws_at(ws, index), _stream_of(stream, index)), "fk_kv_plan")
 
 
 def fk_kv4_write(k, v, slots, codebook, codes, scales, stream=None) -> None:
@@ -306,6 +312,7 @@ class KV4Cache:
         self.status = torch.zeros(4, **i32)
         self.cu = torch.zeros(max_requests + 1, **i32)
         self._lens = [torch.zeros(max_requests, **i32) for _ in range(2)]
+        self._seq = torch.zeros(max_requests, **i32)
         self._plan_ws = kv_plan_workspace(max_requests, device)
         self.slots = self.positions = None
 
@@ -318,15 +325,17 @@ class KV4Cache:
         """Makes room for new_lens (max_requests, int32, on the GPU) more
         tokens, `tokens` of them in all (more: the rest is padding).  Returns
         (slots, positions, cu): self.status says how many tokens found no
-        page.  append() and attend() use this plan."""
+        page.  append() and attend() use this plan.  Tokens without a page are
+        the last of their request; they are not in the cache, lens does not
+        count them, and a later plan may bring them again."""
         device = self.codes.device
         with _on(stream, device):
             self.slots = torch.empty(tokens, dtype=torch.int32, device=device)
             self.positions = torch.empty(tokens, dtype=torch.int32, device=device)
         now, then = self._lens
         fk_kv_plan(now, new_lens, self.page_size, self.free_pages, self.free_count,
-                   self.block_table, then, self.cu, self.slots, self.positions, self.free_count,
-                   self.status, ws=self._plan_ws, stream=stream)
+                   self.block_table, self._seq, self.cu, self.slots, self.positions,
+                   self.free_count, self.status, ws=self._plan_ws, stream=stream, kept_lens=then)
         self._lens = [then, now]
         return self.slots, self.positions, self.cu
 
@@ -341,7 +350,7 @@ class KV4Cache:
         head_dim) over their requests, the planned tokens among them."""
         with _on(stream, q.device):
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        fk_kv4_attention(q, self.cu, self.lens, self.block_table, self.codebook, self.codes,
+        fk_kv4_attention(q, self.cu, self._seq, self.block_table, self.codebook, self.codes,
                          self.scales, out, max_q, scale=scale, causal=causal, window=window,
                          lse=lse, ws=ws, stream=stream)
         return out
@@ -366,3 +375,4 @@ class KV4Cache:
         self.free_count += mine.sum().int()
         table[rows] = -1
         self.lens[rows] = 0
+        self._seq[rows] = 0

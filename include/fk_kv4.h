@@ -95,6 +95,20 @@ fk_status fk_kv_plan(int64_t B, int64_t max_pages, int32_t page_size, const int3
                      int32_t* free_left, int32_t* status, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * fk_kv_plan_kept -- fk_kv_plan that also says what the next step's ctx_lens
+ * are: kept_lens [B] (or NULL) is ctx plus the new tokens that have a page.
+ * That is seq unless the list or the table ended.  The tokens after them have
+ * no rows in the cache: entries below ceil(seq / page_size) are then missing
+ * from the table, and a plan that took seq for ctx would never ask for them.
+ */
+fk_status fk_kv_plan_kept(int64_t B, int64_t max_pages, int32_t page_size, const int32_t* ctx_lens,
+                          const int32_t* new_lens, const int32_t* free_pages, int64_t free_cap,
+                          const int32_t* free_count, int32_t* block_table, int32_t* seq_lens,
+                          int32_t* cu_new, int32_t* slots, int32_t* positions, int64_t slot_cap,
+                          int32_t* free_left, int32_t* status, int32_t* kept_lens, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/*
  * fk_kv4_write -- rows k, v of T tokens into the cache.  Element (t, h, i)
  * of k is at k[t * k_token + h * k_head + i] (strides in elements, >= 0),
  * of v likewise.  Tokens whose slot is negative or beyond the cache are
