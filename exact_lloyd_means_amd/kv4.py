@@ -355,17 +355,29 @@ class KV4Cache:
                          lse=lse, ws=ws, stream=stream)
         return out
 
-    def release(self, rows: torch.Tensor, stream=None) -> None:
-        """Returns the pages of these rows of the table (int64 indices, on the
-        GPU) to the list and empties the rows."""
+    def release(self, rows, stream=None) -> None:
+        """Returns the pages of these rows of the table (integers, on the GPU;
+        one named twice counts once, one that is none not at all) to the list
+        and empties the rows."""
         with _on(stream, self.codes.device):
             self._release(rows)
 
-    def _release(self, rows: torch.Tensor) -> None:
-        table, M = self.block_table, self.block_table.shape[1]
-        held = (self.lens[rows] + self.page_size - 1) // self.page_size
-        entries = table[rows]
-        mine = (torch.arange(M, device=table.device) < held[:, None]) & (entries >= 0)
+    def _release(self, rows) -> None:
+        table, lens, (R, M) = self.block_table, self.lens, self.block_table.shape
+        ints = dict(dtype=torch.int64, device=table.device)
+        rows = torch.as_tensor(rows, device=table.device)
+        if rows.dtype is torch.bool:
+            rows = torch.where(rows, torch.arange(R, **ints), R)
+        rows = torch.where(rows < 0, rows + R, rows).long()
+        rows = torch.where((rows >= 0) & (rows < R), rows, R)        # R: none of them
+        n = rows.numel()
+        left = torch.cat((lens, lens.new_zeros(1))).index_fill_(0, rows, 0)
+        turn = torch.arange(n, **ints)
+        first = torch.full((R + 1,), n, **ints).scatter_reduce_(0, rows, turn, "amin")[rows] == turn
+        row, page = rows.clamp(max=R - 1), torch.arange(M, **ints)
+        entries, P = table[row], self.page_size
+        mine = (first & (rows < R))[:, None] & (page >= ((left[rows] + P - 1) // P)[:, None])
+        mine &= (page < ((lens[row] + P - 1) // P)[:, None]) & (entries >= 0)
         # where each returned page goes; entries that are not go to a place past the list
         at = self.free_count + mine.flatten().cumsum(0) - 1
         pages = self.free_pages.numel()
@@ -373,6 +385,8 @@ class KV4Cache:
         longer[torch.where(mine.flatten(), at, pages)] = entries.flatten()
         self.free_pages.copy_(longer[:pages])
         self.free_count += mine.sum().int()
-        table[rows] = -1
-        self.lens[rows] = 0
-        self._seq[rows] = 0
+        # a row named twice writes each entry as it is and as -1: the lesser stays
+        table.view(-1).scatter_reduce_(0, (row[:, None] * M + page).flatten(),
+                                       torch.where(mine, -1, entries).flatten(), "amin")
+        self._seq.copy_(torch.where(left[:R] < lens, left[:R], self._seq))
+        lens.copy_(left[:R])
