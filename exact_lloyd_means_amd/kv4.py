@@ -355,14 +355,17 @@ class KV4Cache:
                          lse=lse, ws=ws, stream=stream)
         return out
 
-    def release(self, rows, stream=None) -> None:
-        """Returns the pages of these rows of the table (integers, on the GPU;
-        one named twice counts once, one that is none not at all) to the list
-        and empties the rows."""
+    def release(self, rows, keep=None, stream=None) -> None:
+        """Shortens these rows of the table (integers, on the GPU; one named
+        twice counts once, one that is none not at all) to their first `keep`
+        tokens, a number or one for each row, and returns the pages that hold
+        none of them to the list.  None: no token is kept, the request is
+        over.  Drafts that were rejected are taken back this way; the lengths
+        are not to be lowered by hand, since the pages would be lost."""
         with _on(stream, self.codes.device):
-            self._release(rows)
+            self._release(rows, keep)
 
-    def _release(self, rows) -> None:
+    def _release(self, rows, keep) -> None:
         table, lens, (R, M) = self.block_table, self.lens, self.block_table.shape
         ints = dict(dtype=torch.int64, device=table.device)
         rows = torch.as_tensor(rows, device=table.device)
@@ -371,7 +374,9 @@ class KV4Cache:
         rows = torch.where(rows < 0, rows + R, rows).long()
         rows = torch.where((rows >= 0) & (rows < R), rows, R)        # R: none of them
         n = rows.numel()
-        left = torch.cat((lens, lens.new_zeros(1))).index_fill_(0, rows, 0)
+        keep = torch.as_tensor(0 if keep is None else keep, device=table.device)
+        keep = keep.int().clamp(min=0).expand(n)
+        left = torch.cat((lens, lens.new_zeros(1))).scatter_reduce_(0, rows, keep, "amin")
         turn = torch.arange(n, **ints)
         first = torch.full((R + 1,), n, **ints).scatter_reduce_(0, rows, turn, "amin")[rows] == turn
         row, page = rows.clamp(max=R - 1), torch.arange(M, **ints)

@@ -1,5 +1,7 @@
 """KV4Cache.release: every page is in the list or in the table, once, whatever
-rows are named."""
+rows are named; drafts are taken back and their pages used again."""
+import math
+
 import pytest
 import torch
 
@@ -7,7 +9,7 @@ import exact_lloyd_means_amd as fk
 import kv4_ref as ref
 
 pytestmark = pytest.mark.gpu
-H, D, P, PAGES, B = 2, 64, 32, 30, 4
+H, Hq, D, P, PAGES, B = 2, 4, 64, 32, 30, 4
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -50,3 +52,37 @@ def test_a_mask_of_rows():
     cache = filled([40, 100, 64, 33])
     cache.release(torch.tensor([True, False, False, True], device="cuda"))
     check(cache, [0, 100, 64, 0])
+
+
+@pytest.mark.parametrize("rows,keep,left", [
+    ([1], 65, {1: 65}), ([1], 64, {1: 64}), ([1], 97, {1: 97}), ([0, 2], 33, {0: 33, 2: 33}),
+    ([0, 1, 2, 3], [40, 96, 0, 500], {1: 96, 2: 0}), ([1, 1], [99, 31], {1: 31}), ([2], -3, {2: 0}), ([9], 0, {})])
+def test_first_tokens_are_kept(rows, keep, left):
+    lens = [40, 100, 64, 33]
+    cache = filled(lens)
+    cache.release(torch.tensor(rows, device="cuda"), keep=keep if isinstance(keep, int) else i32(keep))
+    check(cache, [left.get(b, n) for b, n in enumerate(lens)])
+
+
+def test_drafts_are_taken_back():
+    g = torch.Generator().manual_seed(0)
+    cache, cb = filled([0, 0, 0, 0]), ref.codebook(H, 0)
+    lens, rows = [0] * B, torch.arange(B, device="cuda")
+    for step in range(30):
+        new = [30, 5, 1, 62] if step == 0 else [5] * B              # pages end inside the drafts
+        T = sum(new)
+        q, k, v = (torch.randn(T, h, D, generator=g).bfloat16() for h in (Hq, H, H))
+        _, positions, cu = cache.plan(i32(new), T)
+        assert positions.tolist() == [n + i for n, m in zip(lens, new) for i in range(m)]
+        cache.append(k.cuda(), v.cuda())
+        out = cache.attend(q.cuda(), max(new))
+        seq = [a + b for a, b in zip(lens, new)]
+        want = ref.attention(q, cu.cpu(), seq, cache.block_table.cpu(), cb, cache.codes.cpu(), cache.scales.cpu(),
+                             1 / math.sqrt(D), True, 0)
+        tol, _ = ref.attention_tolerance(*want, D, torch.bfloat16)
+        assert bool(((out.cpu().double() - want[0]).abs() <= tol).all())
+        taken = new if step == 0 else torch.randint(0, 6, (B,), generator=g).tolist()
+        lens = [a + b for a, b in zip(lens, taken)]
+        cache.release(rows, keep=i32(lens))
+        check(cache, lens)
+    assert cache.status.tolist()[2:] == [0, 0]
