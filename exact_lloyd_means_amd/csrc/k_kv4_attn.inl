@@ -7,8 +7,10 @@
 //                 (16 g + n) gets rows 4 g + r of query n.  The token of row
 //                 m of tile u is 8 (m / 4) + 4 u + m % 4, so the two tiles
 //                 give a lane the eight consecutive tokens 8 g .. 8 g + 7.
-//   p, w          x = S * k scale, p = 2^(x qs - m), l += p, w = p * v scale,
-//                 all in fp32 in those lanes; w rounded to fp16 once.
+//   p, w          x = S * (k scale * scale log2 e), p = 2^(x qs - m), l += p,
+//                 w = p * v scale, all in fp32 in those lanes; w rounded to
+//                 fp16 once.  qs is a power of two, so x qs is exact and the
+//                 largest scores cancel in x qs - m however large they are.
 //   O^T += V^T w  A = 16 dimensions x 32 tokens, B = w: a lane's operand is
 //                 its own eight weights, so nothing crosses lanes.
 //
@@ -43,7 +45,7 @@ constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = 4;
 constexpr int kTabBytes = 65536;
 constexpr int kSplitLds = kTabBytes + 512;  // and what the waves tell each other
-constexpr float kNoMax = -1e30f;   // running maximum before any key
+constexpr float kNoMax = -3.402823466e38f;  // m before any key: below every score
 constexpr float kFirst = 3.f;      // log2 of a row's largest weight when m is set
 constexpr float kRoom = 4.f;       // log2 of the room above a block's largest v scale
 constexpr float kTop = 15.f;       // log2 of the largest weight
@@ -266,7 +268,7 @@ struct Wave {
 
     half8 q[NT][kKs];
     floatx4 o[NT][kDb];
-    float m[NT], l[NT], qs[NT];
+    float m[NT], l[NT], qs[NT];  // qs: the power of two that q was divided by
     int lo[NT], hi[NT];  // positions the lane's query row sees
     // v scales up to `limit` (bits of the cache dtype in both halves) times p up
     // to 2^slack give weights up to 2^kTop
@@ -317,7 +319,7 @@ struct Wave {
             int e = (int)(__builtin_bit_cast(uint32_t, big) >> 23 & 0xff);
             e = big == 0.f || e == 255 ? 0 : (e < 1 ? 1 : e) - 127;
             const float f = ldexpf(1.f, -e);
-            qs[t] = fmaxf(ldexpf(a.qk, e), 1.17549435e-38f);
+            qs[t] = ldexpf(1.f, e);
 #pragma unroll
             for (int s = 0; s < kKs; ++s)
 #pragma unroll
@@ -345,7 +347,8 @@ struct Wave {
 
     // One block; `at` is its first position.  The next block's k and v are
     // loaded into the same registers as soon as this one's are done with.
-    __device__ inline void step(Block<D>& blk, const Source& next, int at, uint32_t lane4, int g) {
+    __device__ inline void step(Block<D>& blk, const Source& next, int at, uint32_t lane4, int g,
+                                float qk) {
         // scores
         floatx4 s[2][NT];
 #pragma unroll
@@ -379,7 +382,7 @@ struct Wave {
         const uintx4 vw = blk.vs;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            ks[j] = j & 1 ? high_f32<DT>(blk.ks[j >> 1]) : low_f32<DT>(blk.ks[j >> 1]);
+            ks[j] = (j & 1 ? high_f32<DT>(blk.ks[j >> 1]) : low_f32<DT>(blk.ks[j >> 1])) * qk;
             vs[j] = j & 1 ? high_f32<DT>(vw[j >> 1]) : low_f32<DT>(vw[j >> 1]);
         }
 #pragma unroll
@@ -556,7 +559,7 @@ struct Walk {
         for (int b = first; b < end; b += stride) {
             const Source next = source(a, lane);
             ahead(a, b + 2 * stride);
-            wv.step(blk, next, b * kKvBlock, lane4, g);
+            wv.step(blk, next, b * kKvBlock, lane4, g, a.qk);
         }
     }
 };

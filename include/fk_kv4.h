@@ -166,7 +166,7 @@ size_t fk_kv4_attn_workspace_bytes(const fk_kv4_cache* c, int64_t B, int64_t T, 
  * largest), codebook values as they are, softmax weights times v's scale
  * rounded to fp16 once: to 2^-11 of the weight, or 2^-28 of the largest of
  * its row where that is more.  v scales below 2^-96 or above 2^40, which only
- * bf16 holds, may cost more.
+ * bf16 holds, may cost more, as may those above 2^15 beside scores beyond 2^24.
  * Results do not depend on timing.  B <= 2^20, q_heads / kv_heads <= 256, T *
  * q_heads / kv_heads <= 2^24, B * max_pages * page_size < 2^36.
  */
