@@ -62,13 +62,30 @@ __device__ inline Spot locate(const PlanArgs& a, int64_t t, int64_t b, int32_t c
                                                                   : nullptr;
     return s;
 }
-// Slot and, for the first token of a fresh page, table entry.
+// Slot (t < slot_cap) and, for the first token of a fresh page, table entry.
 __device__ inline void place(const PlanArgs& a, int64_t t, int64_t b, const Spot& s, int32_t page) {
     if (s.fresh && s.in == 0) a.table[b * a.max_pages + s.pg] = page;
-    if (t < a.slot_cap) {
-        const int64_t slot = (int64_t)page * a.page_size + s.in;
-        a.slots[t] = page >= 0 && slot <= kSat ? (int32_t)slot : -1;
-        if (a.pos) a.pos[t] = (int32_t)s.pos;
+    const int64_t slot = (int64_t)page * a.page_size + s.in;
+    a.slots[t] = page >= 0 && slot <= kSat ? (int32_t)slot : -1;
+    if (a.pos) a.pos[t] = (int32_t)s.pos;
+}
+
+// Table entries of needed pages first, first + stride, ...: where there are
+// more tokens than slots, so that a step's work follows its slots and pages and
+// not the tokens without a slot.  off: a request's first needed page.
+template <typename Off, typename Ctx>
+__device__ inline void place_pages(const PlanArgs& a, int64_t first, int64_t stride, int64_t wanted,
+                                   int32_t n, Off off, Ctx ctx) {
+    const uint32_t P = (uint32_t)a.page_size;
+    for (int64_t i = first; i < wanted; i += stride) {
+        int64_t lo = 0, hi = a.B;  // off(lo) <= i < off(hi): the last of those that need none is passed
+        while (hi - lo > 1) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (off(mid) <= i) lo = mid;
+            else hi = mid;
+        }
+        const uint32_t held = ((uint32_t)ctx(lo) + P - 1) / P;
+        a.table[lo * a.max_pages + held + (i - off(lo))] = i < n ? a.free_pages[n - 1 - i] : -1;
     }
 }
 
@@ -177,8 +194,8 @@ __global__ __launch_bounds__(N) void k_plan_scan(PlanArgs a) {
         if constexpr (!FILL) a.ws[a.B] = (int32_t)n;
     }
     if constexpr (FILL) {
-        const int64_t tot = low(total), last = tot > a.slot_cap ? tot : a.slot_cap;
-        for (int64_t t = tid; t < last; t += N) {
+        const int64_t tot = low(total);
+        for (int64_t t = tid; t < a.slot_cap; t += N) {
             if (t >= tot) {
                 no_token(a, t);
                 continue;
@@ -192,6 +209,9 @@ __global__ __launch_bounds__(N) void k_plan_scan(PlanArgs a) {
             const Spot sp = locate(a, t, lo, s_cu[lo], s_ctx[lo], s_off[lo], (int32_t)n);
             place(a, t, lo, sp, sp.from ? *sp.from : -1);
         }
+        if (tot > a.slot_cap)
+            place_pages(a, tid, N, low(wanted), (int32_t)n, [&](int64_t b) { return s_off[b]; },
+                        [&](int64_t b) { return s_ctx[b]; });
     }
 }
 
@@ -230,12 +250,12 @@ __global__ __launch_bounds__(kFillThreads) void k_plan_fill(PlanArgs a) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int64_t total = a.cu[a.B];
     const int32_t n = a.ws[a.B];
-    const int64_t last = total > a.slot_cap ? total : a.slot_cap;
-    for (int64_t t0 = (int64_t)blockIdx.x * kFillTokens; t0 < last;
+    for (int64_t t0 = (int64_t)blockIdx.x * kFillTokens; t0 < a.slot_cap;
          t0 += (int64_t)gridDim.x * kFillTokens) {
         int64_t b0 = 0, b1 = 0;
         if (t0 < total) {
-            const int64_t t1 = t0 + kFillTokens < total ? t0 + kFillTokens : total;
+            int64_t t1 = t0 + kFillTokens < total ? t0 + kFillTokens : total;
+            t1 = t1 < a.slot_cap ? t1 : a.slot_cap;
             wave_find(a.cu, a.B, t0, t1 - 1, lane, b0, b1);
         }
         const bool staged = b1 - b0 < kFillB;
@@ -252,7 +272,7 @@ __global__ __launch_bounds__(kFillThreads) void k_plan_fill(PlanArgs a) {
         for (int e = 0; e < kEach; ++e) {
             const int64_t t = t0 + tid + e * kFillThreads;
             sp[e].from = nullptr;
-            if (t >= total) continue;
+            if (t >= total || t >= a.slot_cap) continue;
             int64_t lo = b0, hi = b1 + 1;
             if (staged) {
                 int l = 0, h = (int)(hi - lo);
@@ -274,7 +294,7 @@ __global__ __launch_bounds__(kFillThreads) void k_plan_fill(PlanArgs a) {
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             const int64_t t = t0 + tid + e * kFillThreads;
-            if (t >= total) continue;
+            if (t >= total || t >= a.slot_cap) continue;
             const int32_t c = a.ctx[b[e]];
             sp[e] = locate(a, t, b[e], a.cu[b[e]], c < 0 ? 0 : c, a.ws[b[e]], n);
         }
@@ -283,10 +303,15 @@ __global__ __launch_bounds__(kFillThreads) void k_plan_fill(PlanArgs a) {
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             const int64_t t = t0 + tid + e * kFillThreads;
+            if (t >= a.slot_cap) continue;
             if (t < total) place(a, t, b[e], sp[e], page[e]);
-            else if (t < last) no_token(a, t);
+            else no_token(a, t);
         }
     }
+    if (total > a.slot_cap)  // pages wanted: taken and not there
+        place_pages(a, (int64_t)blockIdx.x * kFillThreads + tid, (int64_t)gridDim.x * kFillThreads,
+                    (int64_t)a.status[1] + a.status[2], n, [&](int64_t b) { return a.ws[b]; },
+                    [&](int64_t b) { return a.ctx[b] < 0 ? 0 : a.ctx[b]; });
 }
 
 }  // namespace
@@ -304,7 +329,7 @@ hipError_t launch_kv_plan(const PlanArgs& a, hipStream_t s) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     int64_t wgs = (a.slot_cap + kFillTokens - 1) / kFillTokens;
-    wgs = wgs < 1 ? 1 : wgs > 4096 ? 4096 : wgs;
+    wgs = wgs < 64 ? 64 : wgs > 4096 ? 4096 : wgs;  // few slots: there may be pages all the same
     k_plan_fill<<<dim3((unsigned)wgs), dim3(kFillThreads), 0, s>>>(a);
     return hipGetLastError();
 }
