@@ -160,7 +160,10 @@ __device__ inline void encode(const uint32_t (&x)[D / 32], float t, uint32_t* ro
     constexpr uint32_t inf = DT == FK_BF16 ? 0x7f80 : 0x7c00, nan = DT == FK_BF16 ? 0x7fc0 : 0x7e00;
     scale = m >= inf ? nan : m;
     row[r] = bound<DT>(t, scale);
-    __builtin_amdgcn_wave_barrier();  // the row's lanes are of one wave
+    // the row's lanes are of one wave: no barrier, but the reads stay behind the writes
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     uint32_t c[16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
