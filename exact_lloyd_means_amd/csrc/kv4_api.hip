@@ -188,7 +188,7 @@ fk_status check_heads(const fk_kv4_cache* c, int64_t B, int64_t T, int32_t q_hea
     if (q_heads / c->kv_heads > 256) return fail(FK_EUNSUPPORTED, "q_heads / kv_heads must be <= 256");
     if (T * (q_heads / c->kv_heads) > kMaxTokens)
         return fail(FK_EUNSUPPORTED, "T * q_heads / kv_heads must be <= 2^24");
-    if ((T * (q_heads / c->kv_heads) / 64 + B) * c->kv_heads >= (int64_t)1 << 24)
+    if (((T * (q_heads / c->kv_heads) + 63) / 64 + B) * c->kv_heads >= (int64_t)1 << 24)
         return fail(FK_EUNSUPPORTED, "T * q_heads / 64 + B * kv_heads must be < 2^24");
     if (max_q < 1) return fail(FK_EINVAL, "max_q must be >= 1");
     return FK_OK;

@@ -168,7 +168,8 @@ size_t fk_kv4_attn_workspace_bytes(const fk_kv4_cache* c, int64_t B, int64_t T, 
  * its row where that is more.  v scales below 2^-96 or above 2^40, which only
  * bf16 holds, may cost more, as may those above 2^15 beside scores beyond 2^24.
  * Results do not depend on timing.  B <= 2^20, q_heads / kv_heads <= 256, T *
- * q_heads / kv_heads <= 2^24, B * max_pages * page_size < 2^36.
+ * q_heads / kv_heads <= 2^24, B * max_pages * page_size < 2^36, (ceil(T *
+ * q_heads / kv_heads / 64) + B) * kv_heads < 2^24.
  */
 fk_status fk_kv4_attention(const fk_kv4_cache* c, const fk_kv4_attn* a, void* ws, size_t ws_bytes,
                            void* stream);
