@@ -341,6 +341,8 @@ class KV4Cache:
 
     def append(self, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
         """Rows of the planned tokens, (tokens, kv_heads, head_dim)."""
+        if self.slots is not None and not self.slots.numel() and not len(k) and not len(v):
+            return                                    # a step without tokens
         fk_kv4_write(k, v, self.slots, self.codebook, self.codes, self.scales, stream=stream)
 
     def attend(self, q: torch.Tensor, max_q: int, scale: float | None = None, causal: bool = True,
@@ -350,6 +352,8 @@ class KV4Cache:
         head_dim) over their requests, the planned tokens among them."""
         with _on(stream, q.device):
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if not len(q):
+            return out
         fk_kv4_attention(q, self.cu, self._seq, self.block_table, self.codebook, self.codes,
                          self.scales, out, max_q, scale=scale, causal=causal, window=window,
                          lse=lse, ws=ws, stream=stream)
