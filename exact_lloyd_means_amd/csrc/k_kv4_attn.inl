@@ -856,10 +856,11 @@ void k_kv4_attn_group(AttnArgs a) {
 
 // ---- split form: shares of the keys, a wave each ----------------------------------
 
-// Blocks a wave takes of `total`: an equal share; more, up to `least`, where an
-// eighth of the waves is enough for that.
-__device__ inline int split_share(int total, int waves, int least) {
-    const int per = (total + waves - 1) / waves, eighth = (total + waves / 8) / (waves / 8 + 1);
+// Blocks a wave takes of `total` (< 2^31): an equal share; more, up to `least`,
+// where an eighth of the waves is enough for that.
+__device__ inline int split_share(uint32_t total, uint32_t waves, int least) {
+    const int per = (int)((total + waves - 1) / waves);
+    const int eighth = (int)((total + waves / 8) / (waves / 8 + 1));
     const int more = eighth < least ? eighth : least;
     const int share = per > more ? per : more;
     return share < 2 ? 2 : share;
@@ -928,7 +929,7 @@ void k_kv4_attn_split(AttnArgs a) {
     const int first_wave = blockIdx.x * W;
     // Where the shares of this workgroup begin, and what the join needs.
     const bool tell = blockIdx.x == 0 && h == 0;
-    const int64_t begin = (int64_t)first_wave * share, stop = begin + W * share;
+    const int64_t begin = (int64_t)first_wave * share, stop = begin + (int64_t)W * share;
     if (tell || (at < stop && at + mine > begin)) {
         int* prefix = a.prefix + (int64_t)rt * (a.B + 1);
         for (int b = b0; b < b0 + per && b < a.B; ++b) {
