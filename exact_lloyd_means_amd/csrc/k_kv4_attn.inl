@@ -638,11 +638,11 @@ constexpr int kOrderB = 256;
 // kOrderB requests each search would cost as much as it saves: requests in
 // order, each from its last tile.
 //
-// Bound by vector instructions: 350 a block of 48 rows x 128 dimensions
-// beside 48 matrix instructions, which two waves a SIMD (255 registers) hardly
-// overlap.  Six prompts of 1000-4096 tokens, 32 / 8 heads of 128: 485 us, 757
-// TFLOP/s (in order of requests 652 us; 32 rows a wave 736 us then, 64 spill:
-// 1150 us).
+// Bound by vector instructions: 336 a block of 48 rows x 128 dimensions
+// beside 48 matrix instructions, which two waves a SIMD (251 registers) hardly
+// overlap.  Six prompts of 1000-4096 tokens, 32 / 8 heads of 128: 482 us, 763
+// TFLOP/s.  In an earlier build, tiles in order of requests took 652 us; 32 rows
+// a wave 736 us; 64 rows spill inside the loop, 1150 us.
 template <int D, int DT, int NT>
 __global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_attn_rows(AttnArgs a) {
     extern __shared__ uint32_t tab[];
@@ -898,10 +898,10 @@ __device__ inline void store_part(const AttnArgs& a, const Wave<D, DT, NT>& wv, 
 // and k_kv4_attn_join adds the shares of a request in order.  Waves meet
 // nowhere after the table is built.
 //
-// Three contexts of 66-131k tokens, 32 / 8 heads of 128: 81 us with the join,
-// 4.0 TB/s of codes and scales, near what a copy reaches.  64 contexts of
-// 512-8192: 54 us, 3.2 TB/s; 8 us of it pass before a wave has its first codes
-// and 7 us in the join.  One share a wave and no more (two rounds: 70 us).
+// Three contexts of 66-131k tokens, 32 / 8 heads of 128: 78 us with the join,
+// 4.2 TB/s of codes and scales, near what a copy reaches.  64 contexts of
+// 512-8192: 53 us, 3.3 TB/s; 8 us of it pass before a wave has its first codes
+// and 6 us in the join.  One share a wave and no more (two rounds: 70 us).
 template <int D, int DT, int NT>
 __global__ __launch_bounds__((64 * kSplitWaves<D, NT>), (kSplitWaves<D, NT> / 2))
 void k_kv4_attn_split(AttnArgs a) {

@@ -10,8 +10,8 @@
 // launches).  One workgroup does the scans.  Where the tokens are few it also
 // fills tables and slots from LDS in the same launch; else a second launch
 // fills them from many workgroups, each token's request found by a search in
-// the prefix sums.  64 requests: 6.3 us; 3000 requests and 2^20 slots, 8.5 MB:
-// 16 us, of which 10 in the second launch.
+// the prefix sums.  64 requests: 4.7 us; 3000 requests and 2^20 slots, 8.5 MB:
+// 6.4 and 9.4 us.
 #include "kv4_internal.h"
 
 namespace fk {

@@ -26,11 +26,12 @@ AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q,
     p.rows = (int)(rows < tile ? rows : tile);
     // Where the table has room for few blocks a request, the longest decides,
     // and no launch that joins shares is worth its 8 us: one wave a request
-    // where those alone nearly fill the card and are short, else as many as
-    // fit at once.  Measured with 8 kv heads of 128, the longest request in
-    // blocks, us as one wave / several / shares: 256 requests of 2: 10 / 13 /
-    // 24; 256 of 19: 27 / 27 / 37; 128 of 32: 42 / 26 / 30; 128 of 63: 84 / 41 /
-    // 44; 16 of 32: - / 12 / 20; 4 of 63: - / 16 / 19; 4 of 125: - / 26 / 21.
+    // where those alone nearly fill the card and are short (about 20 blocks is
+    // where one and several meet), else as many as fit at once.  Measured with 8
+    // kv heads of 128 alone, the longest request in blocks, us as one wave /
+    // several / shares: 256 requests of 2: 10 / 13 / 24; 256 of 19: 27 / 27 /
+    // 37; 128 of 32: 42 / 26 / 30; 128 of 63: 84 / 41 / 44; 16 of 32: - / 12 /
+    // 20; 4 of 63: - / 16 / 19; 4 of 125: - / 26 / 21.
     if (p.split) {
         const int W = split_waves(D, p.col_blocks);
         const int64_t units = B * Hkv * tiles;
@@ -43,7 +44,7 @@ AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q,
     if (p.split && !p.group) {
         // The join's workgroups, of 1024 / D rows at a time: about four a CU.
         const int64_t tiles_all = B * Hkv * tiles;
-                int64_t z = 1024 / tiles_all;
+        int64_t z = 1024 / tiles_all;
         z = z < 1 ? 1 : z > p.rows ? p.rows : z;
         p.join_z = (int)z;
         const int each = (int)((p.rows + z - 1) / z), most = 1024 / D;

@@ -85,7 +85,9 @@ struct AttnArgs {
 };
 
 // Most blocks of 16 query rows of a wave, by head dimension, in the rows form
-// and in the others: what 256 registers hold without spilling.
+// and in the others: what the loop over blocks holds in 256 registers.  Around
+// that loop the split form of 128 dimensions keeps 21 registers in scratch for
+// three blocks of rows and 2 for one; no form touches scratch inside it.
 template <int D>
 constexpr int kRowCols = D == 64 ? 4 : D == 128 ? 3 : 1;
 template <int D>

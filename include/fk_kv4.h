@@ -18,8 +18,9 @@
  *             code_i = number of j with t_j s < x_i,
  *           so a value on a threshold takes the lower code.  It stands for
  *             c_code s.
- *           t_j s has at most 22 bits and is exact in fp32: codes do not
- *           depend on rounding or order.
+ *           t_j s has at most 22 bits and is exact in fp32 from s = 2^-118
+ *           up (smaller bf16 scales may round): codes do not depend on
+ *           rounding or order.
  *  codebook [2][kv_heads][16] fp16, k then v, each ascending and finite.
  *  scales   [pages][kv_heads][2][page_size] cache dtype.
  *  codes    [pages][kv_heads][2][page_size / 32][16 D] bytes: blocks of 32
