@@ -362,8 +362,8 @@ class KV4Cache:
     def release(self, rows, keep=None, stream=None) -> None:
         """Shortens these rows of the table (integers, on the GPU; one named
         twice counts once, one that is none not at all) to their first `keep`
-        tokens, a number or one for each row, and returns the pages that hold
-        none of them to the list.  None: no token is kept, the request is
+        tokens, a number or a tensor of one for each row, and returns the
+        pages that hold none of them to the list.  None: no token is kept, the request is
         over.  Drafts that were rejected are taken back this way; the lengths
         are not to be lowered by hand, since the pages would be lost."""
         with _on(stream, self.codes.device):
@@ -378,7 +378,8 @@ class KV4Cache:
         rows = torch.where(rows < 0, rows + R, rows).long()
         rows = torch.where((rows >= 0) & (rows < R), rows, R)        # R: none of them
         n = rows.numel()
-        keep = torch.as_tensor(0 if keep is None else keep, device=table.device)
+        if not isinstance(keep, torch.Tensor):                       # filled there: a copy would wait
+            keep = lens.new_full((n,), max(0, keep or 0))
         keep = keep.int().clamp(min=0).expand(n)
         left = torch.cat((lens, lens.new_zeros(1))).scatter_reduce_(0, rows, keep, "amin")
         turn = torch.arange(n, **ints)

@@ -7,6 +7,7 @@ import torch
 
 import exact_lloyd_means_amd as fk
 import kv4_ref as ref
+from test_gpu_streams import stall
 
 pytestmark = pytest.mark.gpu
 H, Hq, D, P, PAGES, B = 2, 4, 64, 32, 30, 4
@@ -86,3 +87,20 @@ def test_drafts_are_taken_back():
         cache.release(rows, keep=i32(lens))
         check(cache, lens)
     assert cache.status.tolist()[2:] == [0, 0]
+
+
+@pytest.mark.parametrize("keep,lens", [(None, [40, 0, 64, 0]), (33, [40, 33, 64, 33]), ([33, 0], [40, 33, 64, 0])])
+def test_release_does_not_wait(keep, lens):
+    keep = i32(keep) if isinstance(keep, list) else keep
+    rows = torch.tensor([1, 3], device="cuda")
+    for busy in (False, True):                       # the first call loads the kernels
+        cache, done = filled([40, 100, 64, 33]), torch.cuda.Event()
+        torch.cuda.synchronize()
+        if busy:
+            left = stall(torch.cuda.current_stream())
+        done.record()
+        cache.release(rows, keep=keep)
+        if busy:
+            assert not done.query()
+            del left
+    check(cache, lens)
