@@ -238,13 +238,16 @@ def fk_kv4_attention(q, cu_q, seq_lens, block_table, codebook, codes, scales, ou
     at, token, head = _rows_at(q, "q", dtype, rows, index)
     (B,) = one = _tensor(seq_lens, "seq_lens", 1)
     table = _tensor(block_table, "block_table", 2)
-    args = _ATTN.pack(
-        B, T, Hq, max_q, table[1], token, head, at, _at(cu_q, "cu_q", _i32, (B + 1,), index),
-        _at(seq_lens, "seq_lens", _i32, one, index),
-        _at(block_table, "block_table", _i32, (B, table[1]), index),
-        1.0 / math.sqrt(D) if scale is None else scale, bool(causal), window,
-        _at(out, "out", dtype, rows, index),
-        0 if lse is None else _at(lse, "lse", torch.float32, (T, Hq), index))
+    try:
+        args = _ATTN.pack(
+            B, T, Hq, max_q, table[1], token, head, at, _at(cu_q, "cu_q", _i32, (B + 1,), index),
+            _at(seq_lens, "seq_lens", _i32, one, index),
+            _at(block_table, "block_table", _i32, (B, table[1]), index),
+            1.0 / math.sqrt(D) if scale is None else scale, bool(causal), window,
+            _at(out, "out", dtype, rows, index),
+            0 if lse is None else _at(lse, "lse", torch.float32, (T, Hq), index))
+    except struct.error as e:
+        raise ValueError(f"max_q, window or scale is no number of its range: {e}") from None
     _on_gpu(index)
     if ws is None:
         with _on(stream, codes.device):
@@ -323,7 +326,8 @@ class KV4Cache:
 
     def plan(self, new_lens: torch.Tensor, tokens: int, stream=None):
         """Makes room for new_lens (max_requests, int32, on the GPU) more
-        tokens, `tokens` of them in all (more: the rest is padding).  Returns
+        tokens, `tokens` of them in all or more (the rest is padding), never
+        fewer (the last would have pages and no rows).  Returns
         (slots, positions, cu): self.status says how many tokens found no
         page.  append() and attend() use this plan.  Tokens without a page are
         the last of their request; they are not in the cache, lens does not
