@@ -438,3 +438,5 @@ def fk_assign_variant(X: torch.Tensor, C: torch.Tensor, bias: torch.Tensor, labe
 from .api import KMeans, batch_kmeans_euclid, initial_centroids  # noqa: E402  (uses the above)
 from .kv4 import (KV4Cache, fk_kv4_attention, fk_kv4_read, fk_kv4_write, fk_kv_plan,  # noqa: E402
                   kv4_attention_workspace, kv_plan_workspace, learn_codebook)
+from .serve import (fk_kv4_attention_shared, fk_kv4_copy, fk_kv_compact, fk_kv_fork, fk_rope, fk_verify,  # noqa: E402
+                    kv4_attention_shared_workspace, kv_compact_workspace, kv_fork_workspace, rope_turns, verify_workspace)

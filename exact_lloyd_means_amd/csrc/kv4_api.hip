@@ -200,6 +200,10 @@ int clamp_max_q(int64_t T, int32_t max_q) { return T < max_q ? (int)T : max_q; }
 
 }  // namespace
 
+namespace fk {
+fk_status kv4_check_cache(const fk_kv4_cache* c) { return check_cache(c); }
+}  // namespace fk
+
 extern "C" {
 
 size_t fk_kv_plan_workspace_bytes(int64_t B) {

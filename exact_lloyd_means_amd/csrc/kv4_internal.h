@@ -115,6 +115,9 @@ struct AttnPlan {
 AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q,
                         int64_t max_blocks);
 
+// Checks of a cache's shape and addresses.
+fk_status kv4_check_cache(const fk_kv4_cache* c);
+
 hipError_t launch_kv4_attn_d64(const AttnArgs& a, const AttnPlan& p, int dtype, hipStream_t s);
 hipError_t launch_kv4_attn_d128(const AttnArgs& a, const AttnPlan& p, int dtype, hipStream_t s);
 hipError_t launch_kv4_attn_d256(const AttnArgs& a, const AttnPlan& p, int dtype, hipStream_t s);

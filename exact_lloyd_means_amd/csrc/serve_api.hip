@@ -1,0 +1,347 @@
+// serve_api.hip -- host side of include/fk_serve.h: argument checks (before
+// anything is enqueued) and workspace layouts.
+#include <math.h>
+
+#include "serve_internal.h"
+
+namespace {
+
+using namespace fk;
+
+bool aligned(const void* p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+fk_status need(const void* p, const char* name, unsigned to) {
+    if (!p) return fail(FK_EINVAL, "%s is NULL", name);
+    if (!aligned(p, to)) return fail(FK_EINVAL, "%s is not %u-byte aligned", name, to);
+    return FK_OK;
+}
+
+fk_status need_ws(const void* ws, size_t have, size_t want) {
+    if (!ws) return fail(FK_EWORKSPACE, "workspace is NULL");
+    if (!aligned(ws, 16)) return fail(FK_EINVAL, "workspace is not 16-byte aligned");
+    if (have < want) return fail(FK_EWORKSPACE, "workspace has %zu bytes, needs %zu", have, want);
+    return FK_OK;
+}
+
+#define FK_CHECK(expr)                    \
+    do {                                  \
+        fk_status fk_s_ = (expr);         \
+        if (fk_s_ != FK_OK) return fk_s_; \
+    } while (0)
+
+constexpr int64_t kMaxRequests = 1 << 20, kMaxTokens = 1 << 24;
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+fk_status check_dtype(int32_t dtype) {
+    if (dtype != FK_F32 && dtype != FK_F16 && dtype != FK_BF16)
+        return fail(FK_EUNSUPPORTED, "dtype must be fp32, fp16 or bf16, got %d", (int)dtype);
+    return FK_OK;
+}
+
+// ---- verification -----------------------------------------------------------------------
+
+fk_status check_verify_sizes(int64_t B, int64_t T, int64_t V) {
+    if (B < 1 || T < 1 || V < 1)
+        return fail(FK_EINVAL, "sizes must be >= 1 (B=%lld T=%lld V=%lld)", (long long)B,
+                    (long long)T, (long long)V);
+    if (B > kMaxRequests) return fail(FK_EUNSUPPORTED, "B must be <= 2^20");
+    if (T > kMaxTokens) return fail(FK_EUNSUPPORTED, "T must be <= 2^24");
+    if (V > 1 << 20) return fail(FK_EUNSUPPORTED, "V must be <= 2^20");
+    return FK_OK;
+}
+
+// Elements of a piece of a row where `rows` of them are read: whole 16-byte
+// accesses, and then the pieces that are left.
+void verify_pieces(int64_t rows, int64_t V, int32_t& chunks, int32_t& len) {
+    const int64_t c = verify_chunks(rows, V);
+    len = (int32_t)(((V + c - 1) / c + 7) / 8 * 8);
+    chunks = (int32_t)((V + len - 1) / len);
+}
+
+// ---- pages --------------------------------------------------------------------------------
+
+fk_status check_pool_sizes(const fk_kv_pool* p) {
+    if (!p) return fail(FK_EINVAL, "pool is NULL");
+    if (p->R < 1 || p->max_pages < 1 || p->pages < 1)
+        return fail(FK_EINVAL, "sizes must be >= 1 (R=%lld max_pages=%lld pages=%lld)",
+                    (long long)p->R, (long long)p->max_pages, (long long)p->pages);
+    if (p->R > kMaxRequests) return fail(FK_EUNSUPPORTED, "R must be <= 2^20");
+    if (p->page_size < 32 || p->page_size > 1024 || p->page_size % 32)
+        return fail(FK_EUNSUPPORTED, "page_size must be a multiple of 32 up to 1024, got %d",
+                    (int)p->page_size);
+    if (p->max_pages > 2147483647 / p->page_size)
+        return fail(FK_EUNSUPPORTED, "max_pages * page_size must be <= 2^31 - 1");
+    if (p->pages > 2147483647 / p->page_size)
+        return fail(FK_EUNSUPPORTED, "pages * page_size must be <= 2^31 - 1");
+    if (p->reserved) return fail(FK_EINVAL, "reserved must be 0");
+    return FK_OK;
+}
+
+fk_status check_pool(const fk_kv_pool* p) {
+    FK_CHECK(check_pool_sizes(p));
+    FK_CHECK(need(p->block_table, "block_table", 4));
+    FK_CHECK(need(p->lens, "lens", 4));
+    FK_CHECK(need(p->shares, "shares", 4));
+    FK_CHECK(need(p->free_pages, "free_pages", 4));
+    return need(p->free_count, "free_count", 4);
+}
+
+fk_status check_pairs(int64_t n, const fk_kv_pool* p) {
+    if (n < 1) return fail(FK_EINVAL, "n must be >= 1");
+    if (n > 65536) return fail(FK_EUNSUPPORTED, "n must be <= 65536");
+    if (p->max_pages > 2147483647 / n)
+        return fail(FK_EUNSUPPORTED, "n * max_pages must be <= 2^31 - 1");
+    return FK_OK;
+}
+
+// Places in the workspace; base NULL: sizes only.
+size_t fork_layout(int64_t n, const fk_kv_pool* p, char* base, ForkArgs& a) {
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        char* x = base ? base + at : nullptr;
+        at = align256(at + bytes);
+        return x;
+    };
+    a.info = reinterpret_cast<int32_t*>(take((size_t)n * 8 * sizeof(int32_t)));
+    a.fresh = reinterpret_cast<int32_t*>(take((size_t)n * (size_t)p->max_pages * sizeof(int32_t)));
+    a.have = reinterpret_cast<int32_t*>(take(2 * sizeof(int32_t)));
+    a.count = reinterpret_cast<int32_t*>(take((size_t)p->pages * sizeof(int32_t)));
+    a.tail = reinterpret_cast<int32_t*>(take((size_t)p->pages * sizeof(int32_t)));
+    a.next = reinterpret_cast<int32_t*>(take((size_t)p->pages * sizeof(int32_t)));
+    a.first = reinterpret_cast<uint64_t*>(take((size_t)p->pages * sizeof(uint64_t)));
+    return at;
+}
+
+fk_status check_compact_pages(int64_t pages) {
+    if (pages < 1) return fail(FK_EINVAL, "pages must be >= 1");
+    if (pages > 1 << 20) return fail(FK_EUNSUPPORTED, "pages must be <= 2^20");
+    return FK_OK;
+}
+
+size_t compact_layout(int64_t pages, char* base, CompactArgs& a) {
+    const size_t words = (size_t)(pages + 31) / 32;
+    a.bits = reinterpret_cast<uint32_t*>(base);
+    const size_t at = align256(words * sizeof(uint32_t));
+    a.before = base ? reinterpret_cast<int32_t*>(base + at) : nullptr;
+    return at + (words + 1) * sizeof(int32_t);
+}
+
+}  // namespace
+
+extern "C" {
+
+fk_status fk_rope(const fk_rope_args* p, int32_t n, const fk_rope_rows* rows, void* stream) {
+    if (!p || !rows) return fail(FK_EINVAL, "arguments are NULL");
+    if (n != 1 && n != 2) return fail(FK_EINVAL, "n must be 1 or 2");
+    if (p->T < 1) return fail(FK_EINVAL, "T must be >= 1");
+    if (p->T > kMaxTokens) return fail(FK_EUNSUPPORTED, "T must be <= 2^24");
+    FK_CHECK(check_dtype(p->dtype));
+    if (p->head_dim < 2 || p->head_dim % 2 || p->head_dim > 1024)
+        return fail(FK_EUNSUPPORTED, "head_dim must be even, 2 to 1024, got %d", (int)p->head_dim);
+    if (p->rot_dim < 2 || p->rot_dim % 2 || p->rot_dim > p->head_dim)
+        return fail(FK_EINVAL, "rot_dim must be even, 2 to head_dim, got %d", (int)p->rot_dim);
+    if ((p->interleaved != 0 && p->interleaved != 1) || (p->inverse != 0 && p->inverse != 1))
+        return fail(FK_EINVAL, "interleaved and inverse must be 0 or 1");
+    if (!isfinite(p->factor)) return fail(FK_EINVAL, "factor must be finite");
+    FK_CHECK(need(p->positions, "positions", 4));
+    FK_CHECK(need(p->turns, "turns", 8));
+    RopeArgs a{};
+    const unsigned size = p->dtype == FK_F32 ? 4 : 2;
+    for (int i = 0; i < n; ++i) {
+        const fk_rope_rows& r = rows[i];
+        if (r.heads < 1) return fail(FK_EINVAL, "heads must be >= 1");
+        if (r.heads > 65536) return fail(FK_EUNSUPPORTED, "heads must be <= 2^16");
+        FK_CHECK(need(r.x, "x", size));
+        FK_CHECK(need(r.y, "y", size));
+        if (r.x_token < 0 || r.x_head < 0 || r.y_token < 0 || r.y_head < 0)
+            return fail(FK_EINVAL, "strides must be >= 0");
+        if (r.x == r.y && (r.x_token != r.y_token || r.x_head != r.y_head))
+            return fail(FK_EINVAL, "rows rotated in place must have the same strides");
+        if (r.reserved) return fail(FK_EINVAL, "reserved must be 0");
+        a.set[i] = {r.x, r.y, r.x_token, r.x_head, r.y_token, r.y_head};
+        a.heads[i] = r.heads;
+    }
+    if (n == 1) a.set[1] = a.set[0];  // without heads
+    a.T = p->T;
+    a.D = p->head_dim;
+    a.R = p->rot_dim;
+    a.pos = p->positions;
+    a.turns = p->turns;
+    a.factor = p->factor;
+    a.sin_factor = p->inverse ? -p->factor : p->factor;
+    const hipError_t e = launch_rope(a, p->dtype, p->interleaved, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? FK_OK : hip_fail(e, "fk_rope");
+}
+
+size_t fk_verify_workspace_bytes(int64_t B, int64_t T, int64_t V) {
+    if (check_verify_sizes(B, T, V) != FK_OK) return 0;
+    int32_t by_request, by_row, len;
+    verify_pieces(B, V, by_request, len);
+    verify_pieces(T, V, by_row, len);
+    const size_t sampling = (size_t)B * by_request * 2, greedy = (size_t)T * by_row;
+    return (sampling > greedy ? sampling : greedy) * sizeof(uint64_t);
+}
+
+fk_status fk_verify(const fk_verify_args* p, void* ws, size_t ws_bytes, void* stream) {
+    if (!p) return fail(FK_EINVAL, "arguments are NULL");
+    FK_CHECK(check_verify_sizes(p->B, p->T, p->V));
+    FK_CHECK(check_dtype(p->dtype));
+    if (p->reserved) return fail(FK_EINVAL, "reserved must be 0");
+    const unsigned size = p->dtype == FK_F32 ? 4 : 2;
+    FK_CHECK(need(p->cu, "cu", 4));
+    FK_CHECK(need(p->tokens, "tokens", 4));
+    FK_CHECK(need(p->target, "target", size));
+    if (p->draft) FK_CHECK(need(p->draft, "draft", size));
+    if (p->target_row < 0 || p->draft_row < 0) return fail(FK_EINVAL, "strides must be >= 0");
+    if (p->accept) {
+        FK_CHECK(need(p->accept, "accept", 4));
+        FK_CHECK(need(p->pick, "pick", 4));
+    } else if (p->pick || p->draft) {
+        return fail(FK_EINVAL, "pick and draft come with accept: greedy decoding draws nothing");
+    }
+    FK_CHECK(need(p->accepted, "accepted", 4));
+    FK_CHECK(need(p->emitted, "emitted", 4));
+    if (p->keep) {
+        FK_CHECK(need(p->keep, "keep", 4));
+        FK_CHECK(need(p->seq_lens, "seq_lens", 4));
+    }
+    FK_CHECK(need_ws(ws, ws_bytes, fk_verify_workspace_bytes(p->B, p->T, p->V)));
+    VerifyArgs a{};
+    a.B = p->B;
+    a.T = p->T;
+    a.V = p->V;
+    a.cu = p->cu;
+    a.tokens = p->tokens;
+    a.seq = p->seq_lens;
+    a.p = p->target;
+    a.q = p->draft;
+    a.p_row = p->target_row;
+    a.q_row = p->draft_row;
+    a.u = p->accept;
+    a.pick = p->pick;
+    a.accepted = p->accepted;
+    a.emitted = p->emitted;
+    a.keep = p->keep;
+    verify_pieces(p->accept ? p->B : p->T, p->V, a.chunks, a.len);
+    a.sums = static_cast<uint64_t*>(ws);
+    const hipError_t e = launch_verify(a, p->dtype, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? FK_OK : hip_fail(e, "fk_verify");
+}
+
+size_t fk_kv_fork_workspace_bytes(int64_t n, const fk_kv_pool* p) {
+    if (check_pool_sizes(p) != FK_OK || check_pairs(n, p) != FK_OK) return 0;
+    ForkArgs a{};
+    return fork_layout(n, p, nullptr, a);
+}
+
+fk_status fk_kv_fork(const fk_kv_pool* p, int64_t n, const int32_t* rows, const int32_t* sources,
+                     const int32_t* keep, int32_t* copies, int32_t* seq, void* ws,
+                     size_t ws_bytes, void* stream) {
+    FK_CHECK(check_pool(p));
+    FK_CHECK(check_pairs(n, p));
+    FK_CHECK(need(rows, "rows", 4));
+    if (sources) FK_CHECK(need(sources, "sources", 4));
+    FK_CHECK(need(keep, "keep", 4));
+    FK_CHECK(need(copies, "copies", 4));
+    if (seq) FK_CHECK(need(seq, "seq", 4));
+    FK_CHECK(need_ws(ws, ws_bytes, fk_kv_fork_workspace_bytes(n, p)));
+    ForkArgs a{};
+    fork_layout(n, p, static_cast<char*>(ws), a);
+    a.R = p->R;
+    a.M = p->max_pages;
+    a.N = p->pages;
+    a.n = (int32_t)n;
+    a.P = p->page_size;
+    a.rows = rows;
+    a.sources = sources;
+    a.keep = keep;
+    a.table = p->block_table;
+    a.lens = p->lens;
+    a.shares = p->shares;
+    a.free_pages = p->free_pages;
+    a.free_count = p->free_count;
+    a.copies = copies;
+    a.seq = seq;
+    const hipError_t e = launch_kv_fork(a, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? FK_OK : hip_fail(e, "fk_kv_fork");
+}
+
+size_t fk_kv_compact_workspace_bytes(int64_t pages) {
+    if (check_compact_pages(pages) != FK_OK) return 0;
+    CompactArgs a{};
+    return compact_layout(pages, nullptr, a);
+}
+
+fk_status fk_kv_compact(const fk_kv_pool* p, int32_t* new_table, int32_t* new_shares,
+                        int32_t* new_free, int32_t* free_left, int32_t* moves, int64_t n_moves,
+                        void* ws, size_t ws_bytes, void* stream) {
+    FK_CHECK(check_pool(p));
+    FK_CHECK(check_compact_pages(p->pages));
+    FK_CHECK(need(new_table, "new_table", 4));
+    FK_CHECK(need(new_shares, "new_shares", 4));
+    FK_CHECK(need(new_free, "new_free", 4));
+    FK_CHECK(need(free_left, "free_left", 4));
+    if (n_moves < p->pages / 2) return fail(FK_EINVAL, "n_moves must be >= pages / 2");
+    if (n_moves > 1 << 20) return fail(FK_EUNSUPPORTED, "n_moves must be <= 2^20");
+    if (n_moves > 0) FK_CHECK(need(moves, "moves", 4));
+    FK_CHECK(need_ws(ws, ws_bytes, fk_kv_compact_workspace_bytes(p->pages)));
+    CompactArgs a{};
+    compact_layout(p->pages, static_cast<char*>(ws), a);
+    a.R = p->R;
+    a.M = p->max_pages;
+    a.N = p->pages;
+    a.n_moves = n_moves;
+    a.P = p->page_size;
+    a.table = p->block_table;
+    a.lens = p->lens;
+    a.shares = p->shares;
+    a.free_pages = p->free_pages;
+    a.free_count = p->free_count;
+    a.new_table = new_table;
+    a.new_shares = new_shares;
+    a.new_free = new_free;
+    a.free_left = free_left;
+    a.moves = moves;
+    const hipError_t e = launch_kv_compact(a, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? FK_OK : hip_fail(e, "fk_kv_compact");
+}
+
+fk_status fk_kv4_copy(const fk_kv4_cache* c, int64_t n, const int32_t* copies, void* stream) {
+    FK_CHECK(kv4_check_cache(c));
+    if (n < 1) return fail(FK_EINVAL, "n must be >= 1");
+    if (n > 1 << 20) return fail(FK_EUNSUPPORTED, "n must be <= 2^20");
+    FK_CHECK(need(copies, "copies", 4));
+    CopyArgs a{};
+    a.codes = static_cast<uint8_t*>(c->codes);
+    a.scales = static_cast<uint16_t*>(c->scales);
+    a.copies = copies;
+    a.pages = c->pages;
+    a.n = (int32_t)n;
+    a.P = c->page_size;
+    a.H = c->kv_heads;
+    a.D = c->head_dim;
+    const hipError_t e = launch_kv4_copy(a, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? FK_OK : hip_fail(e, "fk_kv4_copy");
+}
+
+size_t fk_kv4_attn_shared_workspace_bytes(const fk_kv4_cache* c, int64_t B, int64_t T,
+                                          int32_t q_heads, int32_t max_q, int64_t groups) {
+    if (groups < 1 || groups > B) {
+        fail(FK_EINVAL, "groups must be 1 to B");
+        return 0;
+    }
+    return fk_kv4_attn_workspace_bytes(c, B, T, q_heads, max_q);
+}
+
+fk_status fk_kv4_attention_shared(const fk_kv4_cache* c, const fk_kv4_attn* p, int64_t groups,
+                                  const int32_t* cu_groups, const int32_t* prefix_lens, void* ws,
+                                  size_t ws_bytes, void* stream) {
+    if (!p) return fail(FK_EINVAL, "arguments are NULL");
+    if (groups < 1 || groups > p->B) return fail(FK_EINVAL, "groups must be 1 to B");
+    FK_CHECK(need(cu_groups, "cu_groups", 4));
+    FK_CHECK(need(prefix_lens, "prefix_lens", 4));
+    return fk_kv4_attention(c, p, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,77 @@
+// serve_internal.h -- declarations shared by the translation units of the
+// operators around a serving step (include/fk_serve.h).
+#pragma once
+
+#include "../../include/fk_serve.h"
+#include "kv4_internal.h"
+
+namespace fk {
+
+// ---- rotary positions ---------------------------------------------------------
+struct RopeSet {
+    const void* x;
+    void* y;
+    int64_t x_token, x_head, y_token, y_head;
+};
+struct RopeArgs {
+    RopeSet set[2];
+    int32_t heads[2];
+    int64_t T;
+    int32_t D, R;
+    int32_t units, turn_units;  // accesses of a row; those that are rotated
+    const int32_t* pos;
+    const uint64_t* turns;
+    float factor, sin_factor;   // the latter negative for the inverse
+};
+hipError_t launch_rope(const RopeArgs& a, int dtype, bool inter, hipStream_t s);
+
+// ---- verification of drafts -----------------------------------------------------
+struct VerifyArgs {
+    int64_t B, T, V;
+    const int32_t *cu, *tokens, *seq;
+    const void *p, *q;
+    int64_t p_row, q_row;
+    const float *u, *pick;
+    int32_t *accepted, *emitted, *keep;
+    int32_t chunks, len;  // pieces of a row, elements of one
+    uint64_t* sums;       // sampling: [B][chunks][2]; greedy: [T][chunks]
+};
+// Pieces a row of V is cut into where `rows` of them are read.
+int verify_chunks(int64_t rows, int64_t V);
+hipError_t launch_verify(const VerifyArgs& a, int dtype, hipStream_t s);
+
+// ---- pages ------------------------------------------------------------------------
+struct ForkArgs {
+    int64_t R, M, N;  // rows, max_pages, pages
+    int32_t n, P;
+    const int32_t *rows, *sources, *keep;
+    int32_t *table, *lens, *shares, *free_pages, *free_count, *copies, *seq;
+    int32_t* info;   // [n][8]
+    int32_t* fresh;  // [n][M] entries of the sources
+    int32_t* have;   // [2] pages of the list before the copies, pages taken
+    int32_t *count, *tail, *next;  // [N] change of the holders, first row that
+                                   // goes on in the page, new shares
+    uint64_t* first;               // [N] first entry that gives the page up
+};
+hipError_t launch_kv_fork(const ForkArgs& a, hipStream_t s);
+
+struct CompactArgs {
+    int64_t R, M, N, n_moves;
+    int32_t P;
+    const int32_t *table, *lens, *shares, *free_pages, *free_count;
+    int32_t *new_table, *new_shares, *new_free, *free_left, *moves;
+    uint32_t* bits;   // [words] free pages
+    int32_t* before;  // [words + 1] free pages before each word
+};
+hipError_t launch_kv_compact(const CompactArgs& a, hipStream_t s);
+
+struct CopyArgs {
+    uint8_t* codes;
+    uint16_t* scales;
+    const int32_t* copies;
+    int64_t pages;
+    int32_t n, P, H, D;
+};
+hipError_t launch_kv4_copy(const CopyArgs& a, hipStream_t s);
+
+}  // namespace fk

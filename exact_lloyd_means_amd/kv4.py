@@ -289,8 +289,9 @@ class KV4Cache:
     """The buffers of a serving loop around the functions above.
 
     pages x page_size tokens are shared by max_requests rows of a block table
-    with room for max_len tokens each.  A step is plan(), append(), attend();
-    release() returns a row's pages.  Lengths, tables and the list of free
+    with room for max_len tokens each.  A step is plan(), rotate(), append(),
+    attend(), and verify() where some of its tokens are drafts; release()
+    returns a row's pages, fork() continues rows in others.  Lengths, tables and the list of free
     pages live on the GPU and no call waits for it.  The calls follow each
     other on one stream; a caller that changes streams orders them."""
 
@@ -312,6 +313,7 @@ class KV4Cache:
         self.block_table = torch.full((max_requests, M), -1, **i32)
         self.free_pages = torch.arange(pages - 1, -1, -1, **i32)
         self.free_count = torch.full((1,), pages, **i32)
+        self.shares = torch.zeros(pages, **i32)                      # rows that hold a page, beyond the first
         self.status = torch.zeros(4, **i32)
         self.cu = torch.zeros(max_requests + 1, **i32)
         self._lens = [torch.zeros(max_requests, **i32) for _ in range(2)]
@@ -351,56 +353,118 @@ class KV4Cache:
 
     def attend(self, q: torch.Tensor, max_q: int, scale: float | None = None, causal: bool = True,
                window: int = 0, lse: torch.Tensor | None = None, ws: torch.Tensor | None = None,
-               stream=None) -> torch.Tensor:
+               stream=None, shared=None) -> torch.Tensor:
         """Attention of the planned tokens' queries (tokens, q_heads,
-        head_dim) over their requests, the planned tokens among them."""
+        head_dim) over their requests, the planned tokens among them.  shared:
+        (cu_groups, prefix_lens), int32 on the GPU, where neighbouring rows have
+        their first tokens in common (fk_kv4_attention_shared); they are read
+        once for all rows of a group."""
         with _on(stream, q.device):
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if not len(q):
+            return out
+        if shared is not None:
+            from .serve import fk_kv4_attention_shared
+            fk_kv4_attention_shared(q, self.cu, self._seq, self.block_table, *shared, self.codebook, self.codes, self.scales,
+                                    out, max_q, scale=scale, causal=causal, window=window, lse=lse, ws=ws, stream=stream)
             return out
         fk_kv4_attention(q, self.cu, self._seq, self.block_table, self.codebook, self.codes,
                          self.scales, out, max_q, scale=scale, causal=causal, window=window,
                          lse=lse, ws=ws, stream=stream)
         return out
 
-    def release(self, rows, keep=None, stream=None) -> None:
+    def release(self, rows, keep=None, stream=None) -> torch.Tensor:
         """Shortens these rows of the table (integers, on the GPU; one named
         twice counts once, one that is none not at all) to their first `keep`
         tokens, a number or a tensor of one for each row, and returns the
-        pages that hold none of them to the list.  None: no token is kept, the request is
+        pages that no row holds any more to the list.  None: no token is kept, the request is
         over.  Drafts that were rejected are taken back this way; the lengths
-        are not to be lowered by hand, since the pages would be lost."""
+        are not to be lowered by hand, since the pages would be lost.  What is
+        returned are the copies of fork(): there are some where a row ends
+        within a page that another holds too."""
         with _on(stream, self.codes.device):
-            self._release(rows, keep)
+            rows = self._rows(rows)
+            if not isinstance(keep, torch.Tensor):                   # filled there: a copy would wait
+                keep = self.lens.new_full((rows.numel(),), max(0, keep or 0))
+            keep = keep.int().clamp(min=0).expand(rows.numel()).contiguous()
+            # as many at a time as one call takes: a row's least length is what it comes to
+            most = min(65536, (2 ** 31 - 1) // self.block_table.shape[1])
+            parts = [self._fork(rows[i:i + most], None, keep[i:i + most]) for i in range(0, max(1, rows.numel()), most)]
+            return torch.cat(parts) if len(parts) != 1 else parts[0]
 
-    def _release(self, rows, keep) -> None:
-        table, lens, (R, M) = self.block_table, self.lens, self.block_table.shape
-        ints = dict(dtype=torch.int64, device=table.device)
+    def fork(self, rows, sources, keep=None, stream=None) -> torch.Tensor:
+        """These rows of the table become the first `keep` tokens (a number,
+        a tensor of one for each, None: all) of the rows `sources`, all at
+        once: a prompt is continued in several ways, beams follow their best
+        parents.  Whole pages are shared until a row gives them up; partly
+        filled ones are copied, and where the list has no page for that, the row
+        ends with its last whole page (lens says so).  What the rows held before
+        is returned to the list.  Returns the copies (n, 3), which
+        fk_kv4_copy must make in every other cache that goes by this table.
+        Between steps: slots of a plan hold no longer."""
+        with _on(stream, self.codes.device):
+            rows = self._rows(rows)
+            sources = self._rows(sources)
+            if sources.shape != rows.shape:
+                raise ValueError(f"rows and sources must have one length, got {rows.numel()} and {sources.numel()}")
+            if keep is None or not isinstance(keep, torch.Tensor):
+                keep = self.lens.new_full((rows.numel(),), 2 ** 31 - 1 if keep is None else min(max(0, keep), 2 ** 31 - 1))
+            return self._fork(rows, sources, keep.int().clamp(min=0).expand(rows.numel()).contiguous())
+
+    def _rows(self, rows) -> torch.Tensor:
+        """Rows of the table as int32; R: none of them."""
+        table = self.block_table
+        R = table.shape[0]
         rows = torch.as_tensor(rows, device=table.device)
         if rows.dtype is torch.bool:
-            rows = torch.where(rows, torch.arange(R, **ints), R)
-        rows = torch.where(rows < 0, rows + R, rows).long()
-        rows = torch.where((rows >= 0) & (rows < R), rows, R)        # R: none of them
-        n = rows.numel()
-        if not isinstance(keep, torch.Tensor):                       # filled there: a copy would wait
-            keep = lens.new_full((n,), max(0, keep or 0))
-        keep = keep.int().clamp(min=0).expand(n)
-        left = torch.cat((lens, lens.new_zeros(1))).scatter_reduce_(0, rows, keep, "amin")
-        turn = torch.arange(n, **ints)
-        first = torch.full((R + 1,), n, **ints).scatter_reduce_(0, rows, turn, "amin")[rows] == turn
-        row, page = rows.clamp(max=R - 1), torch.arange(M, **ints)
-        entries, P = table[row], self.page_size
-        mine = (first & (rows < R))[:, None] & (page >= ((left[rows] + P - 1) // P)[:, None])
-        mine &= (page < ((lens[row] + P - 1) // P)[:, None]) & (entries >= 0)
-        # where each returned page goes; entries that are not go to a place past the list
-        at = self.free_count + mine.flatten().cumsum(0) - 1
-        pages = self.free_pages.numel()
-        longer = torch.cat((self.free_pages, self.free_pages.new_empty(1)))
-        longer[torch.where(mine.flatten(), at, pages)] = entries.flatten()
-        self.free_pages.copy_(longer[:pages])
-        self.free_count += mine.sum().int()
-        # a row named twice writes each entry as it is and as -1: the lesser stays
-        table.view(-1).scatter_reduce_(0, (row[:, None] * M + page).flatten(),
-                                       torch.where(mine, -1, entries).flatten(), "amin")
-        self._seq.copy_(torch.where(left[:R] < lens, left[:R], self._seq))
-        lens.copy_(left[:R])
+            return torch.where(rows, torch.arange(R, dtype=torch.int32, device=table.device), R)
+        rows = torch.where(rows < 0, rows + R, rows)
+        return torch.where((rows >= 0) & (rows < R), rows, R).int().flatten()
+
+    def _fork(self, rows, sources, keep) -> torch.Tensor:
+        from .serve import fk_kv4_copy, fk_kv_fork
+        copies = torch.empty(rows.numel(), 3, dtype=torch.int32, device=rows.device)
+        if rows.numel():
+            fk_kv_fork(rows, sources, keep, self.page_size, self.block_table, self.lens, self.shares, self.free_pages,
+                       self.free_count, copies, seq=self._seq)
+            fk_kv4_copy(copies, self.codes, self.scales)
+        return copies
+
+    def compact(self, stream=None) -> torch.Tensor:
+        """Moves the pages in use to the front of the pool, so that those from
+        the number in use on are free, and later ones are taken in ascending
+        order.  Returns the moves (n, 3), which fk_kv4_copy must make in every
+        other cache that goes by this table.  Between steps: slots of a plan
+        hold no longer."""
+        from .serve import fk_kv4_copy, fk_kv_compact
+        with _on(stream, self.codes.device):
+            moves = torch.empty((self.shares.numel() + 1) // 2, 3, dtype=torch.int32, device=self.codes.device)
+            fk_kv_compact(self.page_size, self.block_table, self.lens, self.shares, self.free_pages, self.free_count,
+                          self.block_table, self.shares, self.free_pages, self.free_count, moves)
+            fk_kv4_copy(moves, self.codes, self.scales)
+        return moves
+
+    def rotate(self, q: torch.Tensor, k: torch.Tensor, turns: torch.Tensor, interleaved: bool = False, factor: float = 1.0,
+               stream=None) -> None:
+        """Rotary positions of the planned tokens' queries and keys, in place;
+        turns from rope_turns."""
+        from .serve import fk_rope
+        if len(q):
+            fk_rope(q, k, self.positions, turns, interleaved=interleaved, factor=factor, stream=stream)
+
+    def verify(self, tokens: torch.Tensor, target: torch.Tensor, draft: torch.Tensor | None = None,
+               accept: torch.Tensor | None = None, pick: torch.Tensor | None = None, stream=None):
+        """Keeps the planned tokens' drafts that the target keeps (fk_verify)
+        and takes the others back.  Returns (accepted, emitted)."""
+        from .serve import fk_verify
+        R, device = self.block_table.shape[0], self.codes.device
+        with _on(stream, device):
+            accepted, keep = (torch.empty(R, dtype=torch.int32, device=device) for _ in range(2))
+            emitted = torch.full((len(tokens),), -1, dtype=torch.int32, device=device)
+            if len(tokens):
+                fk_verify(self.cu, tokens, target, accepted, emitted, draft=draft, accept=accept, pick=pick, seq_lens=self._seq,
+                          keep=keep)
+                self.release(torch.arange(R, dtype=torch.int32, device=device), keep=keep)
+            else:
+                accepted.zero_()
+        return accepted, emitted
