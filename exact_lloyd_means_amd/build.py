@@ -24,7 +24,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["fk_api.hip", "k_update.hip", "k_baseline.hip", "k_assign_f16.hip",
            "k_assign_bf16.hip", "k_assign_f32.hip", "k_tune.hip", "kv4_api.hip", "k_kv_plan.hip",
            "k_kv4_rows.hip", "k_kv4_attn_d64.hip", "k_kv4_attn_d128.hip", "k_kv4_attn_d256.hip",
-           "serve_api.hip", "k_rope.hip", "k_verify.hip", "k_kv_pages.hip"]
+           "serve_api.hip", "k_rope.hip", "k_verify.hip", "k_kv_pages.hip",
+           "k_kv4_shared_d64.hip", "k_kv4_shared_d128.hip", "k_kv4_shared_d256.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

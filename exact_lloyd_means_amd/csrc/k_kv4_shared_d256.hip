@@ -1,0 +1,9 @@
+// Attention of shared prefixes, head dimension 256.
+#include "k_kv4_shared.inl"
+
+namespace fk {
+hipError_t launch_kv4_shared_d256(const AttnArgs& a, const SharedArgs& s, const SharedPlan& p, int dtype,
+                                 hipStream_t st) {
+    return shared_d<256>(a, s, p, dtype, st);
+}
+}  // namespace fk

@@ -202,6 +202,60 @@ int clamp_max_q(int64_t T, int32_t max_q) { return T < max_q ? (int)T : max_q; }
 
 namespace fk {
 fk_status kv4_check_cache(const fk_kv4_cache* c) { return check_cache(c); }
+
+fk_status kv4_attn_args(const fk_kv4_cache* c, const fk_kv4_attn* p, AttnArgs& a) {
+    FK_CHECK(check_cache(c));
+    if (!p) return fail(FK_EINVAL, "arguments are NULL");
+    FK_CHECK(check_requests(p->B));
+    FK_CHECK(check_tokens(p->T));
+    FK_CHECK(check_heads(c, p->B, p->T, p->q_heads, p->max_q));
+    if (p->max_pages < 1) return fail(FK_EINVAL, "max_pages must be >= 1");
+    if (p->max_pages > 2147483647 / c->page_size)
+        return fail(FK_EUNSUPPORTED, "max_pages * page_size must be <= 2^31 - 1");
+    if (p->max_pages * (c->page_size / kKvBlock) > 2147483647 / p->B)
+        return fail(FK_EUNSUPPORTED, "B * max_pages * page_size must be < 2^36");
+    if (!(p->scale > 0.f) || !isfinite(p->scale))
+        return fail(FK_EINVAL, "scale must be positive and finite");
+    if (p->causal != 0 && p->causal != 1) return fail(FK_EINVAL, "causal must be 0 or 1");
+    if (p->window < 0) return fail(FK_EINVAL, "window must be >= 0");
+    FK_CHECK(need(p->q, "q", 2));
+    FK_CHECK(check_strides("q", p->q_token, p->q_head));
+    FK_CHECK(need(p->cu_q, "cu_q", 4));
+    FK_CHECK(need(p->seq_lens, "seq_lens", 4));
+    FK_CHECK(need(p->block_table, "block_table", 4));
+    FK_CHECK(need(p->out, "out", 16));
+    if (p->lse) FK_CHECK(need(p->lse, "lse", 4));
+    a = AttnArgs{};
+    a.codes = static_cast<const uint8_t*>(c->codes);
+    a.scales = static_cast<const uint16_t*>(c->scales);
+    a.codebook = static_cast<const uint16_t*>(c->codebook);
+    a.q = static_cast<const uint16_t*>(p->q);
+    a.out = static_cast<uint16_t*>(p->out);
+    a.lse = p->lse;
+    a.cu = p->cu_q;
+    a.seq = p->seq_lens;
+    a.table = p->block_table;
+    a.q_token = p->q_token;
+    a.q_head = p->q_head;
+    a.T = p->T;
+    a.max_pages = p->max_pages;
+    a.pages = c->pages;
+    a.B = (int32_t)p->B;
+    a.Hq = p->q_heads;
+    a.Hkv = c->kv_heads;
+    a.G = p->q_heads / c->kv_heads;
+    a.page_size = c->page_size;
+    a.causal = p->causal;
+    a.window = p->window;
+    a.max_q = clamp_max_q(p->T, p->max_q);
+    a.q_vec = vec_rows(p->q, p->q_token, p->q_head);
+    a.bpp = (uint32_t)(c->page_size / kKvBlock);
+    a.bpp_magic = division_magic(a.bpp);
+    a.G_magic = division_magic((uint32_t)a.G);
+    a.cap = (int32_t)(p->max_pages * c->page_size);
+    a.qk = p->scale * 1.4426950408889634f;
+    return FK_OK;
+}
 }  // namespace fk
 
 extern "C" {
@@ -323,64 +377,15 @@ size_t fk_kv4_attn_workspace_bytes(const fk_kv4_cache* c, int64_t B, int64_t T, 
 
 fk_status fk_kv4_attention(const fk_kv4_cache* c, const fk_kv4_attn* p, void* ws, size_t ws_bytes,
                            void* stream) {
-    FK_CHECK(check_cache(c));
-    if (!p) return fail(FK_EINVAL, "arguments are NULL");
-    FK_CHECK(check_requests(p->B));
-    FK_CHECK(check_tokens(p->T));
-    FK_CHECK(check_heads(c, p->B, p->T, p->q_heads, p->max_q));
-    if (p->max_pages < 1) return fail(FK_EINVAL, "max_pages must be >= 1");
-    if (p->max_pages > 2147483647 / c->page_size)
-        return fail(FK_EUNSUPPORTED, "max_pages * page_size must be <= 2^31 - 1");
-    if (p->max_pages * (c->page_size / kKvBlock) > 2147483647 / p->B)
-        return fail(FK_EUNSUPPORTED, "B * max_pages * page_size must be < 2^36");
-    if (!(p->scale > 0.f) || !isfinite(p->scale))
-        return fail(FK_EINVAL, "scale must be positive and finite");
-    if (p->causal != 0 && p->causal != 1) return fail(FK_EINVAL, "causal must be 0 or 1");
-    if (p->window < 0) return fail(FK_EINVAL, "window must be >= 0");
-    FK_CHECK(need(p->q, "q", 2));
-    FK_CHECK(check_strides("q", p->q_token, p->q_head));
-    FK_CHECK(need(p->cu_q, "cu_q", 4));
-    FK_CHECK(need(p->seq_lens, "seq_lens", 4));
-    FK_CHECK(need(p->block_table, "block_table", 4));
-    FK_CHECK(need(p->out, "out", 16));
-    if (p->lse) FK_CHECK(need(p->lse, "lse", 4));
-    const int max_q = clamp_max_q(p->T, p->max_q);
-    const AttnPlan plan = plan_attention(p->B, p->T, p->q_heads, c->kv_heads, c->head_dim, max_q,
+    AttnArgs a;
+    FK_CHECK(kv4_attn_args(c, p, a));
+    const AttnPlan plan = plan_attention(p->B, p->T, p->q_heads, c->kv_heads, c->head_dim, a.max_q,
                                          p->max_pages * (c->page_size / kKvBlock));
     if (!ws) return fail(FK_EWORKSPACE, "workspace is NULL");
     if (!aligned(ws, 16)) return fail(FK_EINVAL, "workspace is not 16-byte aligned");
     if (ws_bytes < plan.total)
         return fail(FK_EWORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, plan.total);
-    AttnArgs a{};
-    a.codes = static_cast<const uint8_t*>(c->codes);
-    a.scales = static_cast<const uint16_t*>(c->scales);
-    a.codebook = static_cast<const uint16_t*>(c->codebook);
-    a.q = static_cast<const uint16_t*>(p->q);
-    a.out = static_cast<uint16_t*>(p->out);
-    a.lse = p->lse;
-    a.cu = p->cu_q;
-    a.seq = p->seq_lens;
-    a.table = p->block_table;
-    a.q_token = p->q_token;
-    a.q_head = p->q_head;
-    a.T = p->T;
-    a.max_pages = p->max_pages;
-    a.pages = c->pages;
-    a.B = (int32_t)p->B;
-    a.Hq = p->q_heads;
-    a.Hkv = c->kv_heads;
-    a.G = p->q_heads / c->kv_heads;
-    a.page_size = c->page_size;
-    a.causal = p->causal;
-    a.window = p->window;
-    a.max_q = max_q;
-    a.q_vec = vec_rows(p->q, p->q_token, p->q_head);
-    a.bpp = (uint32_t)(c->page_size / kKvBlock);
-    a.bpp_magic = division_magic(a.bpp);
-    a.G_magic = division_magic((uint32_t)a.G);
-    a.cap = (int32_t)(p->max_pages * c->page_size);
     a.least = plan.least;
-    a.qk = p->scale * 1.4426950408889634f;
     a.group = plan.group;
     a.row_tiles = plan.row_tiles;
     a.splits = plan.splits;

@@ -117,6 +117,8 @@ AttnPlan plan_attention(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q,
 
 // Checks of a cache's shape and addresses.
 fk_status kv4_check_cache(const fk_kv4_cache* c);
+// Checks of the attention's arguments, and what they say (all but the plan).
+fk_status kv4_attn_args(const fk_kv4_cache* c, const fk_kv4_attn* p, AttnArgs& a);
 
 hipError_t launch_kv4_attn_d64(const AttnArgs& a, const AttnPlan& p, int dtype, hipStream_t s);
 hipError_t launch_kv4_attn_d128(const AttnArgs& a, const AttnPlan& p, int dtype, hipStream_t s);

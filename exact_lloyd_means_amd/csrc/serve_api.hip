@@ -127,6 +127,63 @@ size_t compact_layout(int64_t pages, char* base, CompactArgs& a) {
     return at + (words + 1) * sizeof(int32_t);
 }
 
+// ---- attention of shared prefixes ------------------------------------------------------
+
+SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, int64_t groups,
+                       int64_t max_blocks) {
+    SharedPlan p{};
+    const int64_t G = Hq / Hkv, rows = G * max_q;
+    const int na = tile_cols(D), nb = rows <= 16 ? 1 : na;
+    p.col_blocks = nb;
+    const int64_t tiles = (rows + 16 * nb - 1) / (16 * nb);
+    p.row_tiles = (int)tiles;
+    // Rows of a request that fill their own tiles gain nothing from sharing
+    // them with others: the walk over blocks is what costs, not the bytes.
+    p.use = groups <= kSharedGroups && tiles * Hkv <= 65535 && (max_blocks + kSharedUnit) * tiles <= 2147483647 / B &&
+            (na > 1 ? rows <= 28 : 16 * tiles * 4 >= rows * 5);
+    if (!p.use) return p;
+    p.rows = (int)(rows < 16 * nb ? rows : 16 * nb);
+    p.least = p.rows / 2 < 6 ? 6 : p.rows / 2;  // blocks of a share: see the split form; a unit and two blocks
+    // two workgroups a CU; every tile of a group needs one, and the requests
+    const int64_t most = T * G / (16 * na) + groups;
+    int64_t wgs = 512 / Hkv;
+    if (wgs < most + most / 8 + 1) wgs = most + most / 8 + 1;
+    p.wgs = (int)wgs;
+    const int64_t tiles_all = B * Hkv * tiles;
+    int64_t z = 1024 / tiles_all;
+    z = z < 1 ? 1 : z > p.rows ? p.rows : z;
+    p.join_z = (int)z;
+    const int each = (int)((p.rows + z - 1) / z), fit = 1024 / D;
+    p.join_rows = 1;
+    while (p.join_rows < each && p.join_rows < fit) p.join_rows *= 2;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t x = at;
+        at = align256(at + bytes);
+        return x;
+    };
+    const size_t units = (size_t)B * tiles, own = (size_t)Hkv * (units + 8 * (size_t)wgs) * p.rows;
+    const size_t parts = (size_t)Hkv * (size_t)wgs * 16 * na;
+    p.head = take(16);
+    p.group = take((size_t)groups * 32);
+    p.req = take((size_t)B * 4);
+    p.seen = take((size_t)T * 8);
+    p.segment = take((size_t)wgs * 32);
+    p.start = take((size_t)wgs * 16);
+    p.prefix = take((units + 1) * 4);
+    p.part_o = take(parts * D * 4);
+    p.part_ml = take(parts * 8);
+    p.own_o = take(own * D * 4);
+    p.own_ml = take(own * 8);
+    p.total = at;
+    return p;
+}
+
+fk_status check_groups(int64_t groups, int64_t B) {
+    if (groups < 1 || groups > B) return fail(FK_EINVAL, "groups must be 1 to B");
+    return FK_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -327,21 +384,52 @@ fk_status fk_kv4_copy(const fk_kv4_cache* c, int64_t n, const int32_t* copies, v
 
 size_t fk_kv4_attn_shared_workspace_bytes(const fk_kv4_cache* c, int64_t B, int64_t T,
                                           int32_t q_heads, int32_t max_q, int64_t groups) {
-    if (groups < 1 || groups > B) {
-        fail(FK_EINVAL, "groups must be 1 to B");
-        return 0;
-    }
-    return fk_kv4_attn_workspace_bytes(c, B, T, q_heads, max_q);
+    const size_t plain = fk_kv4_attn_workspace_bytes(c, B, T, q_heads, max_q);
+    if (!plain || check_groups(groups, B) != FK_OK) return 0;
+    // as much as a call with any block table needs
+    const SharedPlan p = plan_shared(B, T, q_heads, c->kv_heads, c->head_dim,
+                                     (int)(T < max_q ? T : max_q), groups, 0);
+    return p.total > plain ? p.total : plain;
 }
 
 fk_status fk_kv4_attention_shared(const fk_kv4_cache* c, const fk_kv4_attn* p, int64_t groups,
                                   const int32_t* cu_groups, const int32_t* prefix_lens, void* ws,
                                   size_t ws_bytes, void* stream) {
-    if (!p) return fail(FK_EINVAL, "arguments are NULL");
-    if (groups < 1 || groups > p->B) return fail(FK_EINVAL, "groups must be 1 to B");
+    AttnArgs a;
+    FK_CHECK(kv4_attn_args(c, p, a));
+    FK_CHECK(check_groups(groups, p->B));
     FK_CHECK(need(cu_groups, "cu_groups", 4));
     FK_CHECK(need(prefix_lens, "prefix_lens", 4));
-    return fk_kv4_attention(c, p, ws, ws_bytes, stream);
+    const SharedPlan plan = plan_shared(p->B, p->T, p->q_heads, c->kv_heads, c->head_dim, a.max_q, groups,
+                                        p->max_pages * (c->page_size / kKvBlock));
+    if (!plan.use) return fk_kv4_attention(c, p, ws, ws_bytes, stream);
+    FK_CHECK(need_ws(ws, ws_bytes, plan.total));
+    char* w = static_cast<char*>(ws);
+    a.least = plan.least;
+    a.row_tiles = plan.row_tiles;
+    a.part_rows = plan.rows;
+    a.join_rows = plan.join_rows;
+    a.part_o = reinterpret_cast<float*>(w + plan.part_o);
+    a.part_ml = reinterpret_cast<float*>(w + plan.part_ml);
+    a.prefix = reinterpret_cast<int32_t*>(w + plan.prefix);
+    SharedArgs s{};
+    s.cu_groups = cu_groups;
+    s.prefix = prefix_lens;
+    s.groups = (int32_t)groups;
+    s.wgs = plan.wgs;
+    s.head = reinterpret_cast<int32_t*>(w + plan.head);
+    s.group = reinterpret_cast<int4*>(w + plan.group);
+    s.req = reinterpret_cast<int32_t*>(w + plan.req);
+    s.seen = reinterpret_cast<int2*>(w + plan.seen);
+    s.segment = reinterpret_cast<int4*>(w + plan.segment);
+    s.start = reinterpret_cast<int32_t*>(w + plan.start);
+    s.own_o = reinterpret_cast<float*>(w + plan.own_o);
+    s.own_ml = reinterpret_cast<float*>(w + plan.own_ml);
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const hipError_t e = c->head_dim == 64    ? launch_kv4_shared_d64(a, s, plan, c->dtype, st)
+                         : c->head_dim == 128 ? launch_kv4_shared_d128(a, s, plan, c->dtype, st)
+                                              : launch_kv4_shared_d256(a, s, plan, c->dtype, st);
+    return e == hipSuccess ? FK_OK : hip_fail(e, "fk_kv4_attention_shared");
 }
 
 }  // extern "C"

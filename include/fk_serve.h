@@ -179,7 +179,7 @@ size_t fk_kv4_attn_shared_workspace_bytes(const fk_kv4_cache* c, int64_t B, int6
 /*
  * fk_kv4_attention_shared -- fk_kv4_attention of requests that share their
  * first tokens.  Group g is the requests cu_groups[g] .. cu_groups[g+1] - 1
- * (ascending; requests of no group share nothing), of which the first
+ * (ascending, else nothing is shared; requests of no group share nothing), of which the first
  * prefix_lens[g] tokens are the same: they are read through the row of the
  * table of the group's first request, once for the query rows of all of them.
  * Tokens behind the prefix's last whole block of 32 are read for each request.

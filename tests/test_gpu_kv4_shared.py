@@ -174,9 +174,22 @@ def test_odd_numbers_in_pages():
     check(p)
     p["cug"] = [-3, 2, 100]
     check(p)
+    for cug in ([2, 0, 3], [0, 4, 1], [0, 2, 1]):                       # lists that descend share nothing
+        p["cug"] = cug
+        check(p)
     p["cug"], p["prefix"] = [0, 2, 3], [-5, 10 ** 9]
     p["seq"][2] = 73
     check(p)
+
+
+def test_query_lists_that_descend():
+    # tokens named by no ascending list: no row is written twice, none beyond the buffers; ascending requests are right
+    p = problem([(128, [(40, 1)] * 4), (96, [(9, 1)] * 4)], [(30, 1)], 4, 1, 128, 32, DT["bf16"], seed=20)
+    want, _ = run(p, 1)
+    p["cu"] = [0, 1, 2, 3, 1, 5, 6, 7, 8, 9]                            # request 3 has no tokens, request 4 those from 1 on
+    out, _ = run(p, 4)
+    # two roundings to bf16, and of the weights to fp16 (2 2^-11 of values up to 10)
+    assert bool(((out[5:].float() - want[5:].float()).abs() <= 2.0 ** -7 * want[5:].float().abs() + 10 * 2.0 ** -10).all())
 
 
 def test_same_bits_every_time():
