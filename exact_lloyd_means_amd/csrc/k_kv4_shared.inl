@@ -23,8 +23,6 @@
 namespace fk {
 namespace {
 
-constexpr int kPlanWaves = 16;  // at most
-
 // What balances the two kinds of work, in tenths of a microsecond at two waves a
 // SIMD with heads of 128: a block of 16 NT rows; what a segment costs beside its
 // blocks (codes on their way, waves added up); a unit of a share likewise, in
@@ -44,32 +42,39 @@ __device__ inline Span own_span(const AttnArgs& a, Rows& rw, int rt, int rows, i
     return sp;
 }
 
-// Inclusive scan over a workgroup of up to kPlanWaves waves.
-__device__ inline int64_t plan_scan(int64_t x, int64_t* scratch, int64_t& total, int tid) {
-    const int lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
+// build_table in two steps: the codebook's row of the thread's column is on its
+// way while lengths are.
+struct Codebook {
+    uintx4 x[2];
+    __device__ inline void load(const AttnArgs& a, int h, int tid) {
+        const uintx4* p = reinterpret_cast<const uintx4*>(a.codebook + ((tid >> 3 & 1) * a.Hkv + h) * 16);
+        x[0] = p[0];
+        x[1] = p[1];
+    }
+    __device__ inline void build(uint32_t* tab, int tid) const {
+        const int col = tid & 15, lo = tid >> 4 & 15;
+        uint32_t low = 0;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int64_t y = __shfl_up((long long)x, o);
-        if (lane >= o) x += y;
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t v = x[i >> 3][i >> 1 & 3] >> (16 * (i & 1)) & 0xffffu;
+            low = lo == i ? v : low;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t v = low | (x[i >> 3][i >> 1 & 3] >> (16 * (i & 1)) & 0xffffu) << 16;
+            *reinterpret_cast<uintx4*>(tab + (i * 16 + lo) * 64 + col * 4) = uintx4{v, v, v, v};
+        }
     }
-    __syncthreads();  // scratch may still be read
-    if (lane == 63) scratch[wave] = x;
-    __syncthreads();
-    total = 0;
-    for (int w = 0; w < waves; ++w) {
-        const int64_t y = scratch[w];
-        if (w < wave) x += y;
-        total += y;
-    }
-    return x;
-}
+};
 
 struct SharedGroup {  // in LDS
     int req0, req1;   // its requests
-    int tok0, tok1;   // their query tokens
-    int blocks;       // of the prefix
-    int least, most;  // first and one past the last position that a row sees
-    int tiles, lo, len, segs, base;
+    int tok0, rows;   // their first query token and their query rows
+    int blocks;       // of the prefix, 0: nothing is shared
+    int lo, len;      // blocks that some row sees (first: first and last position)
+    int base;         // its first segment
+    int mixed;        // some row does not see all of the prefix's blocks
+    int pad[3];
 };
 
 // The group of request b, -1: none.
@@ -81,18 +86,32 @@ __device__ inline int group_of(const SharedGroup* g, int groups, int b) {
         else hi = mid;
     }
     // of empty groups at one place the last is found: it is the one that may hold b
-    return groups > 0 && b >= g[lo].req0 && b < g[lo].req1 ? lo : -1;
+    return b >= g[lo].req0 && b < g[lo].req1 && g[lo].blocks > 0 ? lo : -1;
 }
 
-// A thread takes neighbouring requests (one, mostly) and groups.
+// What a wave starts with: a unit, and its place in the line.
+struct Start {
+    int unit, at;
+};
+
+struct Shares {
+    int segments;  // of all groups; workgroups from the first on take one each
+    int seg_len;   // most blocks of one
+    int total;     // the line of units: kUnitBlocks and the own blocks of each
+    int share;     // what a wave takes of it; the last workgroup's waves first
+};
+
+// Who does what.  Every workgroup finds out by itself: a launch before would
+// cost more than that.  Threads take neighbouring requests (one, mostly).  The
+// first workgroup writes down what the join needs to know.
 template <int NA, int NB>
-__global__ __launch_bounds__(64 * kPlanWaves) void k_kv4_shared_plan(AttnArgs a, SharedArgs s) {
-    extern __shared__ SharedGroup grp[];
-    __shared__ int64_t scratch[kPlanWaves];
-    __shared__ int longest, best;
-    const int tid = threadIdx.x, threads = blockDim.x;
-    constexpr int rowsA = 16 * NA, rowsB = 16 * NB;
-    const int per = (a.B + threads - 1) / threads, b0 = tid * per;
+__device__ inline Shares shared_plan(const AttnArgs& a, const SharedArgs& s, uint32_t* tab, SharedGroup* grp,
+                                     int* scratch, Start* start, int h, int x, int tid) {
+    constexpr int W = kAttnWaves, rowsA = 16 * NA, rowsB = 16 * NB;
+    int *longest = scratch + W, *tiles_all = longest + 1;
+    Codebook book;
+    book.load(a, h, tid);
+    const int per = (a.B + kAttnThreads - 1) / kAttnThreads, b0 = tid * per;
     Rows mine_rw{};
     if (b0 < a.B) request_lens(a, b0, mine_rw);
     auto rows_of = [&](int b) {
@@ -100,159 +119,219 @@ __global__ __launch_bounds__(64 * kPlanWaves) void k_kv4_shared_plan(AttnArgs a,
         if (b != b0) request_lens(a, b, rw);
         return rw;
     };
-    int64_t bound = 0, total;  // tiles; beyond what there is room for if lists descend
-    if (tid == 0) longest = 1;
-    for (int g = tid; g < s.groups; g += threads) {
+    if (tid == 0) {
+        *longest = 1;
+        *tiles_all = 0;
+    }
+    for (int g = tid; g < s.groups; g += kAttnThreads) {
         int r0 = s.cu_groups[g], r1 = s.cu_groups[g + 1], p = s.prefix[g];
-        if (r1 < r0) bound += s.wgs;
+        const bool down = r1 < r0;
         r0 = r0 < 0 ? 0 : r0 > a.B ? a.B : r0;
         r1 = r1 < r0 ? r0 : r1 > a.B ? a.B : r1;
         p = p < 0 ? 0 : p > a.cap ? a.cap : p;
-        SharedGroup x{};
-        x.req0 = r0;
-        x.req1 = r1;
+        SharedGroup y{};
+        y.req0 = r0;
+        y.req1 = r1;
         if (r1 > r0) {
-            const int T = (int)a.T, t0 = a.cu[r0], t1 = a.cu[r1];
-            x.tok0 = t0 < 0 ? 0 : t0 > T ? T : t0;
-            x.tok1 = t1 < x.tok0 ? x.tok0 : t1 > T ? T : t1;
+            const int T = (int)a.T, c0 = a.cu[r0], c1 = a.cu[r1];
+            const int t0 = c0 < 0 ? 0 : c0 > T ? T : c0, t1 = c1 < t0 ? t0 : c1 > T ? T : c1;
+            y.tok0 = t0;
+            y.rows = (t1 - t0) * a.G;  // <= 2^24
         }
-        x.blocks = p / kKvBlock;
-        // rows that one tile of their own would hold share nothing
-        const int64_t rows = (int64_t)(x.tok1 - x.tok0) * a.G;
-        if (rows <= rowsB) x.blocks = 0;
-        if (x.blocks) bound += (rows + rowsA - 1) / rowsA;
-        x.least = 0x7fffffff;
-        x.most = 0;
-        grp[g] = x;
+        // rows that one tile of their own would hold share nothing; nor do
+        // groups that descend (-1: see below)
+        y.blocks = down ? -1 : y.rows <= rowsB ? 0 : p / kKvBlock;
+        y.lo = 0x7fffffff;
+        grp[g] = y;
     }
-    plan_scan(bound, scratch, total, tid);
-    if (total >= s.wgs) {
-        // cu_groups or cu_q do not ascend: nothing is shared
-        for (int g = tid; g < s.groups; g += threads) grp[g].blocks = 0;
+    book.build(tab, tid);
+    __syncthreads();
+    {
+        // more tiles than there is room for: cu_groups or cu_q do not ascend
+        int n = 0;
+        for (int g = tid; g < s.groups; g += kAttnThreads) {
+            const int y = grp[g].blocks < 0 ? s.wgs : grp[g].blocks ? (grp[g].rows + rowsA - 1) / rowsA : 0;
+            n = n + y < s.wgs ? n + y : s.wgs;
+        }
+        if (n) atomicAdd(tiles_all, n);  // at most 256 wgs <= 2^31
+    }
+    __syncthreads();
+    if (*tiles_all >= s.wgs) {
+        for (int g = tid; g < s.groups; g += kAttnThreads) grp[g].blocks = 0;
         __syncthreads();
     }
     // what the query tokens see of the prefix, and their requests' own blocks
-    int64_t mine = 0;
-    int my_group = -1;
+    int mine = 0, my_group = -1;
     for (int b = b0; b < b0 + per && b < a.B; ++b) {
         Rows rw = rows_of(b);
-        int g = group_of(grp, s.groups, b);
-        if (g >= 0 && grp[g].blocks == 0) g = -1;
-        s.req[b] = g;
+        const int g = group_of(grp, s.groups, b);
         if (b == b0) my_group = g;
         const int prefix = g >= 0 ? grp[g].blocks : 0;
         for (int rt = 0; rt < a.row_tiles; ++rt) {
             const Span sp = own_span(a, rw, rt, rowsB, prefix);
             mine += sp.hi > sp.lo ? sp.hi - sp.lo + kUnitBlocks : 0;
         }
-        if (g < 0) continue;
-        const int end = prefix * kKvBlock, n = rw.qlen < a.max_q ? rw.qlen : a.max_q;
-        int least = 0x7fffffff, most = 0;
-        for (int i = 0; i < rw.qlen; ++i) {
-            int lo = 0, hi = 0;
-            if (i < n) {
-                bounds(a, rw, i, lo, hi);
-                hi = hi < end ? hi : end;
-                if (hi > lo) {
-                    least = lo < least ? lo : least;
-                    most = hi > most ? hi : most;
-                } else {
-                    lo = hi = 0;
-                }
-            }
-            s.seen[rw.tok0 + i] = make_int2(lo, hi);
+        const int n = rw.qlen < a.max_q ? rw.qlen : a.max_q, end = prefix * kKvBlock;
+        if (g < 0 || rw.qlen <= 0) continue;
+        int lo, hi, first_hi, last_lo;
+        bounds(a, rw, 0, lo, first_hi);  // both grow with the token
+        bounds(a, rw, n - 1, last_lo, hi);
+        hi = hi < end ? hi : end;
+        if (hi > lo) {
+            atomicMin(&grp[g].lo, lo);
+            atomicMax(&grp[g].len, hi);
         }
-        atomicMin(&grp[g].least, least);
-        atomicMax(&grp[g].most, most);
+        if (n < rw.qlen || last_lo > 0 || first_hi < end) grp[g].mixed = 1;
     }
-    int64_t blocks;  // and kUnitBlocks for each unit
-    int64_t at = plan_scan(mine, scratch, blocks, tid) - mine;
-    int64_t tiles = 0;
-    for (int g = tid; g < s.groups; g += threads) {
-        SharedGroup& x = grp[g];
-        x.lo = x.most > x.least ? x.least / kKvBlock : 0;
-        x.len = x.most > x.least ? (x.most + kKvBlock - 1) / kKvBlock - x.lo : 0;
-        x.tiles = x.len > 0 ? (int)(((int64_t)(x.tok1 - x.tok0) * a.G + rowsA - 1) / rowsA) : 0;
-        tiles += x.tiles;
-        atomicMax(&longest, x.len);
-    }
-    plan_scan(tiles, scratch, tiles, tid);
-    // The least number k of blocks that every wave of a segment takes, with shares
-    // that last as long, for which the workgroups are enough.
-    constexpr int W = kAttnWaves;
-    auto share_of = [&](int64_t k) {
-        const int64_t x = (k * kBlockTime<NA> + kSegmentTime - kShareTime) / kOwnTime<NB>;
-        return x > a.least ? x : a.least;
-    };
-    int64_t lo = 1, hi = (longest + W - 1) / W;
-    {
-        const int64_t need = (blocks + W * (s.wgs - tiles) - 1) / (W * (s.wgs - tiles));
-        const int64_t k = (need + 1) * kOwnTime<NB> / kBlockTime<NA> + 1;
-        hi = k > hi ? k : hi;  // enough: a segment a tile, and such shares
-    }
-    while (hi > lo) {
-        const int64_t step = (hi - lo + threads - 1) / threads, x = lo + tid * step;
-        if (tid == 0) best = (int)hi;
-        __syncthreads();
-        if (x < hi) {
-            const int64_t each = W * share_of(x);
-            int64_t n = (blocks + each - 1) / each;
-            for (int g = 0; g < s.groups; ++g)
-                if (grp[g].tiles) n += grp[g].tiles * ((grp[g].len + x * W - 1) / (x * W));
-            if (n <= s.wgs) atomicMin(&best, (int)x);
-        }
-        __syncthreads();
-        hi = best;
-        __syncthreads();
-        lo = hi - step + 1 > lo ? hi - step + 1 : lo;
-    }
-    const int len = (int)hi * W, share = (int)share_of(hi);
-    const int per_g = (s.groups + threads - 1) / threads, g0 = tid * per_g;
-    int64_t segs = 0, segments;
-    for (int g = g0; g < g0 + per_g && g < s.groups; ++g)
-        segs += (int64_t)grp[g].tiles * ((grp[g].len + len - 1) / len);
-    int64_t base = plan_scan(segs, scratch, segments, tid) - segs;
-    for (int g = g0; g < g0 + per_g && g < s.groups; ++g) {
-        SharedGroup& x = grp[g];
-        x.base = (int)base;
-        x.segs = (x.len + len - 1) / len;
-        base += (int64_t)x.tiles * x.segs;
-        s.group[2 * g] = make_int4(x.tok0, x.base, x.segs, x.blocks);
-        s.group[2 * g + 1] = make_int4((x.tok1 - x.tok0) * a.G, 0, 0, 0);
-    }
-    if (tid == 0) {
-        s.head[0] = (int)segments;
-        s.head[1] = (int)blocks;
-        s.head[2] = share;
-        a.prefix[a.B * a.row_tiles] = (int)blocks;
-    }
-    // where units and shares begin
-    for (int b = b0; b < b0 + per && b < a.B; ++b) {
-        Rows rw = rows_of(b);
-        const int g = b == b0 ? my_group : s.req[b], prefix = g >= 0 ? grp[g].blocks : 0;
-        for (int rt = 0; rt < a.row_tiles; ++rt) {
-            const Span sp = own_span(a, rw, rt, rowsB, prefix);
-            const int unit = b * a.row_tiles + rt, n = sp.hi > sp.lo ? sp.hi - sp.lo + kUnitBlocks : 0;
-            a.prefix[unit] = (int)at;
-            for (int64_t w = (at + share - 1) / share; w * share < at + n; ++w) s.start[w] = unit;
-            at += n;
+    int total;
+    int at = group_scan<W>(mine, scratch, total, tid) - mine;
+    if (tid == 0) *tiles_all = 0;
+    __syncthreads();
+    for (int g = tid; g < s.groups; g += kAttnThreads) {
+        SharedGroup& y = grp[g];
+        const int lo = y.lo, hi = y.len;
+        y.lo = hi > lo ? lo / kKvBlock : 0;
+        y.len = hi > lo ? (hi + kKvBlock - 1) / kKvBlock - y.lo : 0;
+        if (y.len > 0) {
+            atomicAdd(tiles_all, (y.rows + rowsA - 1) / rowsA);
+            atomicMax(longest, y.len);
         }
     }
     __syncthreads();
-    for (int i = tid; i < (int)segments; i += threads) {
-        int l = 0, h = s.groups;  // the last group with base <= i: those without tiles have the next one's
-        while (h - l > 1) {
-            const int mid = (l + h) / 2;
-            if (grp[mid].base <= i) l = mid;
-            else h = mid;
-        }
-        const SharedGroup x = grp[l];
-        const int k = i - x.base, tile = k / x.segs, seg = k - tile * x.segs;
-        const int from = x.lo + seg * len, to = from + len < x.lo + x.len ? from + len : x.lo + x.len;
-        s.segment[2 * i] = make_int4(x.req0, x.tok0, x.tok1 - x.tok0, tile);
-        s.segment[2 * i + 1] = make_int4(from, to, 0, 0);
+    // The least number k of blocks that every wave of a segment takes, with shares
+    // that last as long, for which the workgroups are enough.
+    auto share_of = [&](int k) {
+        const int y = (k * kBlockTime<NA> + kSegmentTime - kShareTime) / kOwnTime<NB>;
+        return y > a.least ? y : a.least;
+    };
+    const int tiles = *tiles_all;
+    int lo = 1, hi = (*longest + W - 1) / W;
+    {
+        const int room = W * (s.wgs - tiles), need = total / room + 2;
+        const int k = need / kBlockTime<NA> * kOwnTime<NB> + kOwnTime<NB> + 1;
+        hi = k > hi ? k : hi;  // enough: a segment a tile, and such shares
     }
+    while (hi > lo) {
+        const int step = (hi - lo + kAttnThreads - 1) / kAttnThreads, k = lo + tid * step;
+        bool enough = false;
+        if (k < hi) {
+            // each at least its ceiling: lengths are below 2^22, total below 2^27
+            const float each = 1.f / (float)(k * W);
+            int n = (int)((float)total / (float)(W * share_of(k))) + 2;
+            for (int g = 0; g < s.groups && n <= s.wgs; ++g) {
+                const int len = grp[g].len;
+                const int64_t t = (int64_t)((grp[g].rows + rowsA - 1) / rowsA) * ((int)((float)len * each) + 1);
+                if (len > 0) n = t < s.wgs ? n + (int)t : s.wgs + 1;
+            }
+            enough = n <= s.wgs;
+        }
+        const uint64_t m = __ballot(enough);
+        if ((tid & 63) == 0) scratch[tid >> 6] = m ? lo + (tid + __builtin_ctzll(m)) * step : hi;
+        __syncthreads();
+        int first = scratch[0];
+#pragma unroll
+        for (int w = 1; w < W; ++w) first = scratch[w] < first ? scratch[w] : first;
+        __syncthreads();
+        lo = first - lo >= step ? first - step + 1 : lo;
+        hi = first;
+    }
+    Shares r;
+    r.total = total;
+    r.seg_len = hi * W;
+    r.share = share_of(hi);
+    const int per_g = (s.groups + kAttnThreads - 1) / kAttnThreads, g0 = tid * per_g;
+    int segs = 0;
+    for (int g = g0; g < g0 + per_g && g < s.groups; ++g)
+        segs += (grp[g].rows + rowsA - 1) / rowsA * ((grp[g].len + r.seg_len - 1) / r.seg_len);
+    int base = group_scan<W>(segs, scratch, r.segments, tid) - segs;
+    for (int g = g0; g < g0 + per_g && g < s.groups; ++g) {
+        grp[g].base = base;
+        base += (grp[g].rows + rowsA - 1) / rowsA * ((grp[g].len + r.seg_len - 1) / r.seg_len);
+    }
+    __syncthreads();
+    const bool tell = x == 0 && h == 0;
+    const int64_t begin = (int64_t)(s.wgs - 1 - x) * W * r.share, stop = begin + (int64_t)W * r.share;
+    if (tell && tid == 0) s.head[0] = r.share;
+    if (tell || (x >= r.segments && at < stop && at + mine > begin)) {
+        for (int b = b0; b < b0 + per && b < a.B; ++b) {
+            Rows rw = rows_of(b);
+            const int g = b == b0 ? my_group : group_of(grp, s.groups, b);
+            SharedGroup y{};
+            if (g >= 0) y = grp[g];
+            for (int rt = 0; rt < a.row_tiles; ++rt) {
+                const Span sp = own_span(a, rw, rt, rowsB, y.blocks);
+                const int unit = b * a.row_tiles + rt, n = sp.hi - sp.lo;
+                if (tell) {
+                    int4* u = s.unit + 3 * (int64_t)unit;
+                    // the unit's rows among its group's; they are there unless cu_q descends
+                    const int in = (rw.tok0 - y.tok0) * a.G + rw.r0;
+                    const bool there = g >= 0 && in >= 0 && in + rw.n <= y.rows;
+                    u[0] = make_int4(rw.tok0, rw.qlen, rw.seq, g);
+                    u[1] = make_int4(at + kUnitBlocks, n, 0, 0);
+                    u[2] = make_int4(there ? in : 0, y.base, there ? (y.len + r.seg_len - 1) / r.seg_len : 0, 0);
+                }
+                if (n <= 0) continue;
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const int64_t from = begin + w * r.share;
+                    if (from >= at && from < (int64_t)at + n + kUnitBlocks) start[w] = {unit, at};
+                }
+                at += n + kUnitBlocks;
+            }
+        }
+    }
+    __syncthreads();
+    return r;
 }
+
+// Walk with DEPTH blocks on their way.  Two waves a SIMD, as many as the tiles'
+// registers leave, do not cover the way to memory with one block each; a wave of
+// few rows has the registers for more.
+template <int D, int DEPTH>
+struct DeepWalk {
+    Walk<D> at;
+    Block<D> more[DEPTH];
+
+    __device__ inline void begin(const AttnArgs& a, const int32_t* row, int head, int lo, int hi, int lane) {
+        at.table = row;
+        at.h = head;
+        at.first = lo;
+        at.end = hi;
+        at.stride = 1;
+        int page[DEPTH], in[DEPTH];
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) {
+            at.ahead(a, lo + i);
+            page[i] = at.page;
+            in[i] = at.in;
+        }
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) {
+            at.page = page[i];
+            at.in = in[i];
+            const Source src = at.source(a, lane);
+            more[i].load_k(src);
+            more[i].load_v(src);
+        }
+        at.ahead(a, lo + DEPTH);
+    }
+    template <int DT, int NT>
+    __device__ inline void run(const AttnArgs& a, Wave<D, DT, NT>& wv, int lane) {
+        const uint32_t lane4 = 4 * (lane & 31);
+        const int g = lane >> 4;
+        for (int b = at.first;;) {
+#pragma unroll
+            for (int i = 0; i < DEPTH; ++i, ++b) {
+                if (b >= at.end) return;
+                const Source next = at.source(a, lane);
+                at.ahead(a, b + DEPTH + 1);
+                wv.step(more[i], next, b * kKvBlock, lane4, g, a.qk);
+            }
+        }
+    }
+};
+template <int D, int NT>
+constexpr int kDepth = NT > 1 ? 1 : D <= 128 ? 3 : 2;
 
 // Adds up the waves of a workgroup, and stores the rows' sums.  ml: [16 NT][W].
 template <int D, int DT, int NT>
@@ -314,34 +393,63 @@ __global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_shared_walk(AttnArgs a,
     constexpr int W = kAttnWaves;
     extern __shared__ uint32_t tab[];
     float2* ml = reinterpret_cast<float2*>(tab + kTabBytes / 4);  // [16 NA][W]
+    int* scratch = reinterpret_cast<int*>(ml + 16 * NA * W);
+    Start* start = reinterpret_cast<Start*>(scratch + 8);
+    SharedGroup* grp = reinterpret_cast<SharedGroup*>(start + W);
     const int tid = threadIdx.x, lane = tid & 63, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int h = blockIdx.y, segments = s.head[0];
-    const int x = blockIdx.x;
-    if (x < segments) {
-        const int4 d0 = s.segment[2 * x], d1 = s.segment[2 * x + 1];
+    const int h = blockIdx.y, x = blockIdx.x;
+    const Shares plan = shared_plan<NA, NB>(a, s, tab, grp, scratch, start, h, x, tid);
+    if (x < plan.segments) {
+        int g = 0, end = s.groups;  // the last group with base <= x: those without segments have the next one's
+        while (end - g > 1) {
+            const int mid = (g + end) / 2;
+            if (grp[mid].base <= x) g = mid;
+            else end = mid;
+        }
+        const SharedGroup y = grp[__builtin_amdgcn_readfirstlane(g)];
+        const int segs = (y.len + plan.seg_len - 1) / plan.seg_len;
+        const int k = x - y.base, tile = k / segs, seg = k - tile * segs;
         Rows rw;
-        rw.tok0 = __builtin_amdgcn_readfirstlane(d0.y);
-        rw.qlen = __builtin_amdgcn_readfirstlane(d0.z);
+        rw.tok0 = __builtin_amdgcn_readfirstlane(y.tok0);
+        rw.qlen = 0;
         rw.seq = 0;
-        rw.r0 = __builtin_amdgcn_readfirstlane(d0.w) * 16 * NA;
-        const int left = rw.qlen * a.G - rw.r0;
+        rw.r0 = __builtin_amdgcn_readfirstlane(tile * 16 * NA);
+        const int left = __builtin_amdgcn_readfirstlane(y.rows) - rw.r0;
         rw.n = left < 16 * NA ? left : 16 * NA;
-        const int from = __builtin_amdgcn_readfirstlane(d1.x), to = __builtin_amdgcn_readfirstlane(d1.y);
+        const int each = y.len / segs, rest = y.len - each * segs;  // the first `rest` have one more
+        const int from = __builtin_amdgcn_readfirstlane(y.lo + seg * each + (seg < rest ? seg : rest));
+        const int to = __builtin_amdgcn_readfirstlane(from + each + (seg < rest ? 1 : 0));
         const bool some = from + wave < to;
         typename Wave<D, DT, NA>::Raw raw;
         Wave<D, DT, NA>::fetch(a, rw, h, lane, raw);
         Walk<D> wk;
         if (some)
-            wk.begin(a, a.table + __builtin_amdgcn_readfirstlane(d0.x) * a.max_pages, h, from + wave, to,
+            wk.begin(a, a.table + __builtin_amdgcn_readfirstlane(y.req0) * a.max_pages, h, from + wave, to,
                      W, lane);
+        // the positions of the prefix that each row's request lets it see
+        const bool mixed = __builtin_amdgcn_readfirstlane(y.mixed);
         int2 seen[NA];
 #pragma unroll
         for (int t = 0; t < NA; ++t) {
-            const int r = rw.r0 + t * 16 + c;
-            seen[t] = t * 16 + c < rw.n ? s.seen[rw.tok0 + divide(r, a.G, a.G_magic)] : make_int2(0, 0);
+            seen[t] = make_int2(0, t * 16 + c < rw.n ? y.blocks * kKvBlock : 0);
+            if (!mixed || t * 16 + c >= rw.n) continue;
+            seen[t].y = 0;
+            const int tok = rw.tok0 + divide(rw.r0 + t * 16 + c, a.G, a.G_magic);
+            int b = y.req0, e = y.req1;  // the last request that does not begin behind the token
+            while (e - b > 1) {
+                const int mid = (b + e) / 2;
+                if (a.cu[mid] <= tok) b = mid;
+                else e = mid;
+            }
+            Rows its;
+            request_lens(a, b, its);
+            const int i = tok - its.tok0, end = y.blocks * kKvBlock;
+            if (i < 0 || i >= its.qlen || i >= a.max_q) continue;
+            bounds(a, its, i, seen[t].x, seen[t].y);
+            seen[t].y = seen[t].y < end ? seen[t].y : end;
+            if (seen[t].y <= seen[t].x) seen[t] = make_int2(0, 0);
         }
-        build_table(tab, a.codebook, a.Hkv, h, tid, kAttnThreads);
         Wave<D, DT, NA> wv;
         wv.init(a, rw, raw, lane);
         // the rows are those of several requests: each sees what its own does
@@ -363,55 +471,58 @@ __global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_shared_walk(AttnArgs a,
         }
         wv.inner_lo = __builtin_amdgcn_readfirstlane(lo);
         wv.inner_hi = __builtin_amdgcn_readfirstlane(hi);
-        __syncthreads();
         if (some) wk.run(a, wv, lane);
         const int64_t row = ((int64_t)h * s.wgs + x) * (16 * NA);
         store_segment<D, DT, NA>(a, wv, rw.n, a.part_o + row * D, a.part_ml + row * 2, tab, ml, wave, lane);
         return;
     }
-    // shares of the line of units: each is kUnitBlocks without work, then its blocks
-    const int total = s.head[1], share = s.head[2];
-    const int w = (x - segments) * W + wave;
-    if ((int64_t)(x - segments) * W * share >= total) return;
-    int64_t at = (int64_t)w * share;
-    const int64_t stop = at + share < total ? at + share : total;
-    int unit = at < total ? __builtin_amdgcn_readfirstlane(s.start[w]) : 0;
-    build_table(tab, a.codebook, a.Hkv, h, tid, kAttnThreads);
-    __syncthreads();
+    const int w = (s.wgs - 1 - x) * W + wave;
+    const int64_t begin = (int64_t)w * plan.share;
+    const int64_t stop = begin + plan.share < plan.total ? begin + plan.share : plan.total;
+    if (begin >= plan.total) return;
     const int units = a.B * a.row_tiles;
     const int64_t slots = (int64_t)h * (units + 2 * s.wgs * W);
-    for (; at < stop && unit < units; ++unit) {
-        const int b = unit / a.row_tiles, rt = unit - b * a.row_tiles;
-        Rows rw;
-        request_lens(a, b, rw);
-        const int g = s.req[b], prefix = g >= 0 ? s.group[2 * g].w : 0;
-        const Span sp = own_span(a, rw, rt, 16 * NB, prefix);
+    int unit = __builtin_amdgcn_readfirstlane(start[wave].unit);
+    int64_t at = __builtin_amdgcn_readfirstlane(start[wave].at);
+    int b = unit / a.row_tiles, rt = unit - b * a.row_tiles;
+    Rows next;
+    request_lens(a, b, next);
+    while (at < stop && unit < units) {
+        Rows rw = next;
+        const int now = unit++, its = b, tile = rt;
+        if (++rt == a.row_tiles) {
+            rt = 0;
+            if (++b < a.B) request_lens(a, b, next);  // on its way while this one is walked
+        }
+        const int g = __builtin_amdgcn_readfirstlane(group_of(grp, s.groups, its));
+        const int prefix = g >= 0 ? __builtin_amdgcn_readfirstlane(grp[g].blocks) : 0;
+        const Span sp = own_span(a, rw, tile, 16 * NB, prefix);
         const int all = sp.hi - sp.lo;
         if (all <= 0) continue;
-        const int64_t first = a.prefix[unit] + kUnitBlocks;
-        const int skip = at > first ? (int)(at - first) : 0;
-        const int take = first + all < stop ? all - skip : (int)(stop - first) - skip;
-        if (take > 0) {
-            typename Wave<D, DT, NB>::Raw raw;
-            Wave<D, DT, NB>::fetch(a, rw, h, lane, raw);
-            Walk<D> wk;
-            wk.begin(a, a.table + b * a.max_pages, h, sp.lo + skip, sp.lo + skip + take, 1, lane);
-            Wave<D, DT, NB> wv;
-            wv.init(a, rw, raw, lane);
-            wk.run(a, wv, lane);
-            if (take == all && g < 0) {
-                finish<D, DT, NB>(a, wv, rw, h, lane);
-            } else {
-                // one that lies whole in a share has a place of its own; a share's
-                // first unit has place 0 of the share, one that begins in it 1
-                const int64_t slot = take == all ? unit : units + 2 * w + (first > (int64_t)w * share);
-                AttnArgs to = a;
-                to.part_o = s.own_o;
-                to.part_ml = s.own_ml;
-                store_part<D, DT, NB>(to, wv, rw, slots + slot, lane);
-            }
-        }
+        const int64_t first = at + kUnitBlocks;
         at = first + all;
+        const int skip = begin > first ? (int)(begin - first) : 0;
+        const int take = at < stop ? all - skip : (int)(stop - first) - skip;
+        if (take <= 0) continue;
+        typename Wave<D, DT, NB>::Raw raw;
+        Wave<D, DT, NB>::fetch(a, rw, h, lane, raw);
+        DeepWalk<D, kDepth<D, NB>> wk;
+        wk.begin(a, a.table + its * a.max_pages, h, sp.lo + skip, sp.lo + skip + take, lane);
+        Wave<D, DT, NB> wv;
+        wv.init(a, rw, raw, lane);
+        wk.run(a, wv, lane);
+        if (take == all && g < 0) {
+            finish<D, DT, NB>(a, wv, rw, h, lane);
+        } else {
+            // one that lies whole in a share has a place of its own; the unit that a
+            // share begins within has its place 0, one that goes on in the next
+            // share its place 1
+            const int64_t slot = take == all ? now : units + 2 * w + (first > begin);
+            AttnArgs to = a;
+            to.part_o = s.own_o;
+            to.part_ml = s.own_ml;
+            store_part<D, DT, NB>(to, wv, rw, slots + slot, lane);
+        }
     }
 }
 
@@ -426,27 +537,26 @@ __global__ __launch_bounds__(kAttnThreads) void k_kv4_shared_join(AttnArgs a, Sh
     const int b = blockIdx.x;
     const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y - h * a.row_tiles;
     const int unit = b * a.row_tiles + rt, units = a.B * a.row_tiles;
-    const int64_t lo = a.prefix[unit] + kUnitBlocks, hi = a.prefix[unit + 1];
-    const int share = s.head[2], g = s.req[b];
+    const int4 u0 = s.unit[3 * (int64_t)unit], u1 = s.unit[3 * (int64_t)unit + 1], u2 = s.unit[3 * (int64_t)unit + 2];
+    const int share = s.head[0];
+    const int64_t lo = u1.x, hi = lo + u1.y;
     const int w0 = (int)(lo / share), w1 = hi > lo ? (int)((hi - 1) / share) : w0;
     const bool whole = hi > lo && w0 == w1;
-    if (whole && g < 0) return;
+    if (whole && u0.w < 0) return;
     Rows rw;
-    request_lens(a, b, rw);
+    rw.tok0 = u0.x;
+    rw.qlen = u0.y;
+    rw.seq = u0.z;
     tile_rows(a, rw, rt * 16 * NB, 16 * NB);
-    int4 grp = g >= 0 ? s.group[2 * g] : make_int4(0, 0, 0, 0);
-    // the request's rows are among its group's unless cu_q descends
-    const int64_t in0 = (int64_t)(rw.tok0 - grp.x) * a.G + rw.r0;
-    if (g >= 0 && (in0 < 0 || in0 + rw.n > s.group[2 * g + 1].x)) grp.z = 0;
-    const int own = hi > lo ? w1 - w0 + 1 : 0, all = grp.z + own;
+    const int segs = u2.z, own = hi > lo ? w1 - w0 + 1 : 0, all = segs + own;
     const int64_t slots = (int64_t)h * (units + 2 * s.wgs * kAttnWaves);
     const int tid = threadIdx.x, grp_no = tid / (D / 4), d = 4 * (tid % (D / 4));
     const int n = kGroups / a.join_rows, sub = grp_no % n;  // threads of a row, which of them
     for (int r0 = 0; r0 * (int)gridDim.z < rw.n; r0 += a.join_rows) {
         const int row = (r0 + grp_no / n) * gridDim.z + blockIdx.z;
         // the row's place in its group's tiles
-        const int in = (int)in0 + row, tile = in / (16 * NA);
-        const int64_t first = ((int64_t)h * s.wgs + grp.y + tile * grp.z) * (16 * NA) + (in - tile * 16 * NA);
+        const int in = u2.x + row, tile = in / (16 * NA);
+        const int64_t first = ((int64_t)h * s.wgs + u2.y + tile * segs) * (16 * NA) + (in - tile * 16 * NA);
         float top = kNoMax, sum = 0.f;
         floatx4 o = {0, 0, 0, 0};
         if (row < rw.n) {
@@ -459,10 +569,10 @@ __global__ __launch_bounds__(kAttnThreads) void k_kv4_shared_join(AttnArgs a, Sh
                     const int x = w + i * n < all ? w + i * n : w;
                     const float *po = a.part_o, *pm = a.part_ml;
                     int64_t at;
-                    if (x < grp.z) {
+                    if (x < segs) {
                         at = first + (int64_t)x * (16 * NA);
                     } else {
-                        const int v = w0 + x - grp.z;
+                        const int v = w0 + x - segs;
                         po = s.own_o;
                         pm = s.own_ml;
                         at = (slots + (whole ? unit : units + 2 * v + (v == w0 && lo > (int64_t)v * share ? 1 : 0))) *
@@ -521,19 +631,14 @@ __global__ __launch_bounds__(kAttnThreads) void k_kv4_shared_join(AttnArgs a, Sh
 
 template <int D, int DT, int NA, int NB>
 hipError_t shared_run(const AttnArgs& a, const SharedArgs& s, const SharedPlan& p, hipStream_t st) {
-    static LdsAttr rec, rec_plan;
-    auto plan = k_kv4_shared_plan<NA, NB>;
+    static LdsAttr rec;
     auto walk = k_kv4_shared_walk<D, DT, NA, NB>;
-    constexpr int lds = kTabBytes + 16 * NA * kAttnWaves * 8;
-    hipError_t e = ensure_lds(rec, reinterpret_cast<const void*>(walk), lds);
+    constexpr int fixed = kTabBytes + 16 * NA * kAttnWaves * 8 + 32 + kAttnWaves * sizeof(Start);
+    static_assert(fixed + kSharedGroups * sizeof(SharedGroup) <= 80 * 1024, "two workgroups a CU");
+    hipError_t e = ensure_lds(rec, reinterpret_cast<const void*>(walk), 80 * 1024);
     if (e != hipSuccess) return e;
-    e = ensure_lds(rec_plan, reinterpret_cast<const void*>(plan), kSharedGroups * sizeof(SharedGroup));
-    if (e != hipSuccess) return e;
-    const int threads = a.B <= 256 && s.groups <= 256 ? 256 : 64 * kPlanWaves;
-    plan<<<dim3(1), dim3(threads), s.groups * sizeof(SharedGroup), st>>>(a, s);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    walk<<<dim3((unsigned)s.wgs, (unsigned)a.Hkv), dim3(kAttnThreads), lds, st>>>(a, s);
+    walk<<<dim3((unsigned)s.wgs, (unsigned)a.Hkv), dim3(kAttnThreads),
+           fixed + s.groups * sizeof(SharedGroup), st>>>(a, s);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     k_kv4_shared_join<D, DT, NA, NB>

@@ -139,7 +139,7 @@ SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, 
     p.row_tiles = (int)tiles;
     // Rows of a request that fill their own tiles gain nothing from sharing
     // them with others: the walk over blocks is what costs, not the bytes.
-    p.use = groups <= kSharedGroups && tiles * Hkv <= 65535 && (max_blocks + kSharedUnit) * tiles <= 2147483647 / B &&
+    p.use = groups <= kSharedGroups && B <= 8192 && max_blocks <= 1 << 22 && tiles * Hkv <= 65535 && (max_blocks + kSharedUnit) * tiles <= (1 << 27) / B &&
             (na > 1 ? rows <= 28 : 16 * tiles * 4 >= rows * 5);
     if (!p.use) return p;
     p.rows = (int)(rows < 16 * nb ? rows : 16 * nb);
@@ -165,12 +165,7 @@ SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, 
     const size_t units = (size_t)B * tiles, own = (size_t)Hkv * (units + 8 * (size_t)wgs) * p.rows;
     const size_t parts = (size_t)Hkv * (size_t)wgs * 16 * na;
     p.head = take(16);
-    p.group = take((size_t)groups * 32);
-    p.req = take((size_t)B * 4);
-    p.seen = take((size_t)T * 8);
-    p.segment = take((size_t)wgs * 32);
-    p.start = take((size_t)wgs * 16);
-    p.prefix = take((units + 1) * 4);
+    p.unit = take(units * 48);
     p.part_o = take(parts * D * 4);
     p.part_ml = take(parts * 8);
     p.own_o = take(own * D * 4);
@@ -411,18 +406,13 @@ fk_status fk_kv4_attention_shared(const fk_kv4_cache* c, const fk_kv4_attn* p, i
     a.join_rows = plan.join_rows;
     a.part_o = reinterpret_cast<float*>(w + plan.part_o);
     a.part_ml = reinterpret_cast<float*>(w + plan.part_ml);
-    a.prefix = reinterpret_cast<int32_t*>(w + plan.prefix);
     SharedArgs s{};
     s.cu_groups = cu_groups;
     s.prefix = prefix_lens;
     s.groups = (int32_t)groups;
     s.wgs = plan.wgs;
     s.head = reinterpret_cast<int32_t*>(w + plan.head);
-    s.group = reinterpret_cast<int4*>(w + plan.group);
-    s.req = reinterpret_cast<int32_t*>(w + plan.req);
-    s.seen = reinterpret_cast<int2*>(w + plan.seen);
-    s.segment = reinterpret_cast<int4*>(w + plan.segment);
-    s.start = reinterpret_cast<int32_t*>(w + plan.start);
+    s.unit = reinterpret_cast<int4*>(w + plan.unit);
     s.own_o = reinterpret_cast<float*>(w + plan.own_o);
     s.own_ml = reinterpret_cast<float*>(w + plan.own_ml);
     const hipStream_t st = static_cast<hipStream_t>(stream);

@@ -75,25 +75,23 @@ struct CopyArgs {
 hipError_t launch_kv4_copy(const CopyArgs& a, hipStream_t s);
 
 // ---- attention of shared prefixes -------------------------------------------------
-constexpr int kSharedGroups = 1024;  // most groups that the plan holds in LDS
+constexpr int kSharedGroups = 256;   // most groups that the plan holds in LDS
 constexpr int kSharedUnit = 4;       // what a unit of a share costs beside its blocks, in blocks
 
 struct SharedArgs {       // beside AttnArgs, whose part_o and part_ml are the segments' sums
-                          // [heads][wgs][16 NA rows], and prefix the units' first blocks
+                          // [heads][wgs][16 NA rows]
     const int32_t *cu_groups, *prefix;
     int32_t groups, wgs;  // wgs: workgroups of a head
-    int32_t* head;        // [3] segments, length of the units' line, length of a share
-    int4* group;          // [groups][2] first token, first segment, segments of a tile, blocks; rows
-    int32_t* req;         // [B] group, or -1
-    int2* seen;           // [T] positions of the prefix that a query token sees
-    int4* segment;        // [wgs][2] request, first token, tokens, tile; blocks from, to
-    int32_t* start;       // [4 wgs] the unit at the beginning of each share
+    int32_t* head;        // [1] length of a share
+    int4* unit;           // [units][3] for the join: first token, tokens, length, group or -1; place
+                          // in the line, own blocks; first row in the group's tiles, first
+                          // segment, segments of a tile
     float *own_o, *own_ml;  // sums of units and shares: [heads][units + 8 wgs][part_rows]
 };
 struct SharedPlan {
     bool use;             // else as if nothing were shared
     int col_blocks, row_tiles, rows, least, join_z, join_rows, wgs;
-    size_t head, group, req, seen, segment, start, prefix, part_o, part_ml, own_o, own_ml, total;
+    size_t head, unit, part_o, part_ml, own_o, own_ml, total;
 };
 hipError_t launch_kv4_shared_d64(const AttnArgs& a, const SharedArgs& s, const SharedPlan& p, int dtype, hipStream_t st);
 hipError_t launch_kv4_shared_d128(const AttnArgs& a, const SharedArgs& s, const SharedPlan& p, int dtype, hipStream_t st);
