@@ -138,9 +138,8 @@ __device__ inline Shares shared_plan(const AttnArgs& a, const SharedArgs& s, uin
             y.tok0 = t0;
             y.rows = (t1 - t0) * a.G;  // <= 2^24
         }
-        // rows that one tile of their own would hold share nothing; nor do
-        // groups that descend (-1: see below)
-        y.blocks = down ? -1 : y.rows <= rowsB ? 0 : p / kKvBlock;
+        // one request shares with nobody; groups that descend: -1, see below
+        y.blocks = down ? -1 : y.rows > 0 && r1 - r0 > 1 ? p / kKvBlock : 0;
         y.lo = 0x7fffffff;
         grp[g] = y;
     }
@@ -292,16 +291,17 @@ struct DeepWalk {
     Walk<D> at;
     Block<D> more[DEPTH];
 
-    __device__ inline void begin(const AttnArgs& a, const int32_t* row, int head, int lo, int hi, int lane) {
+    __device__ inline void begin(const AttnArgs& a, const int32_t* row, int head, int lo, int hi, int by,
+                                 int lane) {
         at.table = row;
         at.h = head;
         at.first = lo;
         at.end = hi;
-        at.stride = 1;
+        at.stride = by;
         int page[DEPTH], in[DEPTH];
 #pragma unroll
         for (int i = 0; i < DEPTH; ++i) {
-            at.ahead(a, lo + i);
+            at.ahead(a, lo + i * by);
             page[i] = at.page;
             in[i] = at.in;
         }
@@ -313,7 +313,7 @@ struct DeepWalk {
             more[i].load_k(src);
             more[i].load_v(src);
         }
-        at.ahead(a, lo + DEPTH);
+        at.ahead(a, lo + DEPTH * by);
     }
     template <int DT, int NT>
     __device__ inline void run(const AttnArgs& a, Wave<D, DT, NT>& wv, int lane) {
@@ -321,17 +321,17 @@ struct DeepWalk {
         const int g = lane >> 4;
         for (int b = at.first;;) {
 #pragma unroll
-            for (int i = 0; i < DEPTH; ++i, ++b) {
+            for (int i = 0; i < DEPTH; ++i, b += at.stride) {
                 if (b >= at.end) return;
                 const Source next = at.source(a, lane);
-                at.ahead(a, b + DEPTH + 1);
+                at.ahead(a, b + (DEPTH + 1) * at.stride);
                 wv.step(more[i], next, b * kKvBlock, lane4, g, a.qk);
             }
         }
     }
 };
 template <int D, int NT>
-constexpr int kDepth = NT > 1 ? 1 : D <= 128 ? 3 : 2;
+constexpr int kDepth = NT > 2 ? 1 : NT == 1 && D <= 128 ? 3 : 2;
 
 // Adds up the waves of a workgroup, and stores the rows' sums.  ml: [16 NT][W].
 template <int D, int DT, int NT>
@@ -423,7 +423,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_shared_walk(AttnArgs a,
         const bool some = from + wave < to;
         typename Wave<D, DT, NA>::Raw raw;
         Wave<D, DT, NA>::fetch(a, rw, h, lane, raw);
-        Walk<D> wk;
+        DeepWalk<D, kDepth<D, NA>> wk;
         if (some)
             wk.begin(a, a.table + __builtin_amdgcn_readfirstlane(y.req0) * a.max_pages, h, from + wave, to,
                      W, lane);
@@ -507,7 +507,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_shared_walk(AttnArgs a,
         typename Wave<D, DT, NB>::Raw raw;
         Wave<D, DT, NB>::fetch(a, rw, h, lane, raw);
         DeepWalk<D, kDepth<D, NB>> wk;
-        wk.begin(a, a.table + its * a.max_pages, h, sp.lo + skip, sp.lo + skip + take, lane);
+        wk.begin(a, a.table + its * a.max_pages, h, sp.lo + skip, sp.lo + skip + take, 1, lane);
         Wave<D, DT, NB> wv;
         wv.init(a, rw, raw, lane);
         wk.run(a, wv, lane);
@@ -649,10 +649,12 @@ hipError_t shared_run(const AttnArgs& a, const SharedArgs& s, const SharedPlan& 
 
 template <int D, int DT>
 hipError_t shared_cols(const AttnArgs& a, const SharedArgs& s, const SharedPlan& p, hipStream_t st) {
-    constexpr int NA = kTileCols<D>;
-    if constexpr (NA > 1)
-        if (p.col_blocks > 1) return shared_run<D, DT, NA, NA>(a, s, p, st);
-    return shared_run<D, DT, NA, 1>(a, s, p, st);
+    if constexpr (kTileCols<D> > 1) {
+        if (p.col_blocks > 1) return shared_run<D, DT, 3, 2>(a, s, p, st);
+        if (p.group_cols == 3) return shared_run<D, DT, 3, 1>(a, s, p, st);
+        if (p.group_cols == 2) return shared_run<D, DT, 2, 1>(a, s, p, st);
+    }
+    return shared_run<D, DT, 1, 1>(a, s, p, st);
 }
 
 template <int D>

@@ -133,14 +133,25 @@ SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, 
                        int64_t max_blocks) {
     SharedPlan p{};
     const int64_t G = Hq / Hkv, rows = G * max_q;
-    const int na = tile_cols(D), nb = rows <= 16 ? 1 : na;
+    const int most_cols = tile_cols(D), nb = rows <= 16 || most_cols == 1 ? 1 : 2;
     p.col_blocks = nb;
     const int64_t tiles = (rows + 16 * nb - 1) / (16 * nb);
     p.row_tiles = (int)tiles;
-    // Rows of a request that fill their own tiles gain nothing from sharing
-    // them with others: the walk over blocks is what costs, not the bytes.
-    p.use = groups <= kSharedGroups && B <= 8192 && max_blocks <= 1 << 22 && tiles * Hkv <= 65535 && (max_blocks + kSharedUnit) * tiles <= (1 << 27) / B &&
-            (na > 1 ? rows <= 28 : 16 * tiles * 4 >= rows * 5);
+    // Tiles of a group of mean size: those that take the least time in all, which
+    // for a block of 16 n rows goes as 3 + 5 n.
+    const int64_t mean = (T * G + groups - 1) / groups;
+    int64_t group_time = 0;
+    for (int n = most_cols; n >= nb; --n) {
+        if (nb == 2 && n < 3) break;
+        const int64_t t = (mean + 16 * n - 1) / (16 * n) * (3 + 5 * n);
+        if (!p.group_cols || t < group_time) {
+            p.group_cols = n;
+            group_time = t;
+        }
+    }
+    const int na = p.group_cols;
+    p.use = groups <= kSharedGroups && B <= 8192 && max_blocks <= 1 << 22 && tiles * Hkv <= 65535 &&
+            (max_blocks + kSharedUnit) * tiles <= (1 << 27) / B && (most_cols > 1 ? rows <= 32 : tiles <= 4);
     if (!p.use) return p;
     p.rows = (int)(rows < 16 * nb ? rows : 16 * nb);
     p.least = p.rows / 2 < 6 ? 6 : p.rows / 2;  // blocks of a share: see the split form; a unit and two blocks

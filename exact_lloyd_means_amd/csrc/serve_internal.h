@@ -76,7 +76,7 @@ hipError_t launch_kv4_copy(const CopyArgs& a, hipStream_t s);
 
 // ---- attention of shared prefixes -------------------------------------------------
 constexpr int kSharedGroups = 256;   // most groups that the plan holds in LDS
-constexpr int kSharedUnit = 4;       // what a unit of a share costs beside its blocks, in blocks
+constexpr int kSharedUnit = 6;       // what a unit of a share costs beside its blocks, in blocks
 
 struct SharedArgs {       // beside AttnArgs, whose part_o and part_ml are the segments' sums
                           // [heads][wgs][16 NA rows]
@@ -90,7 +90,8 @@ struct SharedArgs {       // beside AttnArgs, whose part_o and part_ml are the s
 };
 struct SharedPlan {
     bool use;             // else as if nothing were shared
-    int col_blocks, row_tiles, rows, least, join_z, join_rows, wgs;
+    int col_blocks, group_cols;  // blocks of 16 rows of a request's tile, a group's
+    int row_tiles, rows, least, join_z, join_rows, wgs;
     size_t head, unit, part_o, part_ml, own_o, own_ml, total;
 };
 hipError_t launch_kv4_shared_d64(const AttnArgs& a, const SharedArgs& s, const SharedPlan& p, int dtype, hipStream_t st);

@@ -172,8 +172,10 @@ def test_odd_numbers_in_pages():
     p["table"][:2, 1] = -1                                              # 32 tokens of the prefix
     p["table"][3, 0] = 10 ** 6
     check(p)
-    p["cug"] = [-3, 2, 100]
+    # bounds beyond the requests; the second group's two have nothing in common, which is said by a prefix of none
+    p["cug"], prefix, p["prefix"] = [-3, 2, 100], p["prefix"], [128, 0]
     check(p)
+    p["prefix"] = prefix
     for cug in ([2, 0, 3], [0, 4, 1], [0, 2, 1]):                       # lists that descend share nothing
         p["cug"] = cug
         check(p)
