@@ -129,8 +129,9 @@ size_t compact_layout(int64_t pages, char* base, CompactArgs& a) {
 
 // ---- attention of shared prefixes ------------------------------------------------------
 
+// max_blocks < 0: the workspace of any block table and window.
 SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, int64_t groups,
-                       int64_t max_blocks) {
+                       int64_t max_blocks, int window) {
     SharedPlan p{};
     const int64_t G = Hq / Hkv, rows = G * max_q;
     const int most_cols = tile_cols(D), nb = rows <= 16 || most_cols == 1 ? 1 : 2;
@@ -150,8 +151,22 @@ SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, 
         }
     }
     const int na = p.group_cols;
-    p.use = groups <= kSharedGroups && B <= 8192 && max_blocks <= 1 << 22 && tiles * Hkv <= 65535 &&
-            (max_blocks + kSharedUnit) * tiles <= (1 << 27) / B && (most_cols > 1 ? rows <= 32 : tiles <= 4);
+    const int64_t room = max_blocks < 0 ? 0 : max_blocks;
+    p.use = groups <= kSharedGroups && B <= 8192 && room <= 1 << 22 && tiles * Hkv <= 65535 &&
+            (room + kSharedUnit) * tiles <= (1 << 27) / B && (most_cols > 1 ? rows <= 32 : tiles <= 4);
+    if (p.use && max_blocks >= 0) {
+        // What sharing saves, in tenths of a microsecond of a wave, were all of the
+        // table's room (or the window) the prefix, against the 8 us that finding
+        // out who does what costs the walk, or 15 where the plain form is one launch.
+        // Measured over 110 mixes of groups: from 9e4 on 30 of 38 gain (up to 37 us, others
+        // lose up to 17 where the room holds no prefix), below 5 of 30 would, by 3 to 6;
+        // of tables with room for 64 blocks or less, from 3e5 on 1 of 1, below 0 of 41.
+        int64_t seen = room;
+        if (window > 0 && seen > (window + max_q) / kKvBlock + 2) seen = (window + max_q) / kKvBlock + 2;
+        const double wide = D == 64 ? 0.6 : D == 128 ? 1.0 : 2.2;  // of a block's time
+        const double saved = wide * (double)(B * tiles * (3 + 5 * nb) - groups * group_time) * Hkv * (double)seen;
+        p.use = saved >= (room <= 64 ? 3e5 : 9e4);
+    }
     if (!p.use) return p;
     p.rows = (int)(rows < 16 * nb ? rows : 16 * nb);
     p.least = p.rows / 2 < 6 ? 6 : p.rows / 2;  // blocks of a share: see the split form; a unit and two blocks
@@ -394,7 +409,7 @@ size_t fk_kv4_attn_shared_workspace_bytes(const fk_kv4_cache* c, int64_t B, int6
     if (!plain || check_groups(groups, B) != FK_OK) return 0;
     // as much as a call with any block table needs
     const SharedPlan p = plan_shared(B, T, q_heads, c->kv_heads, c->head_dim,
-                                     (int)(T < max_q ? T : max_q), groups, 0);
+                                     (int)(T < max_q ? T : max_q), groups, -1, 0);
     return p.total > plain ? p.total : plain;
 }
 
@@ -407,7 +422,7 @@ fk_status fk_kv4_attention_shared(const fk_kv4_cache* c, const fk_kv4_attn* p, i
     FK_CHECK(need(cu_groups, "cu_groups", 4));
     FK_CHECK(need(prefix_lens, "prefix_lens", 4));
     const SharedPlan plan = plan_shared(p->B, p->T, p->q_heads, c->kv_heads, c->head_dim, a.max_q, groups,
-                                        p->max_pages * (c->page_size / kKvBlock));
+                                        p->max_pages * (c->page_size / kKvBlock), p->window);
     if (!plan.use) return fk_kv4_attention(c, p, ws, ws_bytes, stream);
     FK_CHECK(need_ws(ws, ws_bytes, plan.total));
     char* w = static_cast<char*>(ws);

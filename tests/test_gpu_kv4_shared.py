@@ -23,8 +23,9 @@ def i32(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
-def problem(groups, alone, Hq, H, D, P, dtype, seed=0, copied=False, first=0, room=0):
-    """groups: (prefix tokens, [(tokens behind it, query tokens), ...]); alone: [(tokens, query tokens), ...].  copied: a
+def problem(groups, alone, Hq, H, D, P, dtype, seed=0, copied=False, first=0, room=1 << 20):
+    """Tables have room for so many tokens more than the longest request: how much
+    of a prefix there may be decides whether it is walked once for all.  groups: (prefix tokens, [(tokens behind it, query tokens), ...]); alone: [(tokens, query tokens), ...].  copied: a
     prefix's last, partly filled page is a copy of the first request's; first: requests of no group before the groups."""
     r, g = random.Random(seed), torch.Generator().manual_seed(seed)
     rows, cug, prefix = [], [], []
@@ -48,7 +49,7 @@ def problem(groups, alone, Hq, H, D, P, dtype, seed=0, copied=False, first=0, ro
     ids = list(range(need))
     r.shuffle(ids)
     of = {}
-    M = max([1] + [-(-s // P) for _, s, _ in rows]) + room
+    M = max([1] + [-(-s // P) for _, s, _ in rows]) + room // P
     table = torch.full((len(rows), M), -1, dtype=torch.int32)
     for b, (shared, s, _) in enumerate(rows):
         for e in range(-(-s // P)):
@@ -108,6 +109,26 @@ def test_windows(window, causal):
     check(problem(groups, [(50, 1)], 8, 2, 128, 64, DT["bf16"], seed=window), causal=causal, window=window)
 
 
+@pytest.mark.parametrize("window", [700, 1000, 1900])
+@pytest.mark.parametrize("causal", [True, False])
+def test_windows_of_many_heads(window, causal):
+    # so many that the window's blocks alone are worth sharing
+    groups = [(1024, [(1 + 17 * i, 1 + i % 3) for i in range(14)]), (640, [(900 - 50 * i, 1) for i in range(14)])]
+    check(problem(groups, [(50, 1)], 16, 16, 256, 64, DT["bf16"], seed=window), causal=causal, window=window)
+
+
+@pytest.mark.parametrize("room", [0, 64])
+def test_tables_without_room(room):
+    # where little can be shared the requests are taken as if nothing were
+    check(problem([(300, [(20, 1)] * 3)], [(9, 1)], 8, 2, 128, 32, DT["bf16"], seed=21, room=room))
+
+
+@pytest.mark.parametrize("G,each,D", [(1, 2, 64), (1, 16, 128), (1, 33, 128), (5, 6, 64), (3, 40, 128), (12, 2, 256), (24, 2, 128), (32, 3, 64),
+                                      (40, 2, 256), (33, 2, 128), (24, 8, 128), (20, 6, 64)])
+def test_rows_of_all_kinds_of_tiles(G, each, D):
+    check(problem([(500, [(1 + 3 * i, 1) for i in range(each)]), (96, [(40, 1)] * each)], [(70, 1)], 2 * G, 2, D, 32, DT["f16"], seed=G))
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_one_long_prefix(D):
     # shares that lie within a tile, and many tiles of rows
@@ -161,7 +182,7 @@ def test_rows_behind_the_last_request():
 
 def test_odd_numbers_in_pages():
     # scales that are infinite or NaN where nobody looks; pages that are missing; groups that are none
-    p = problem([(128, [(40, 1), (70, 1)]), (64, [(9, 1)])], [(33, 1)], 8, 2, 128, 32, DT["bf16"], seed=10, room=2)
+    p = problem([(128, [(40, 1), (70, 1)]), (64, [(9, 1)])], [(33, 1)], 8, 2, 128, 32, DT["bf16"], seed=10)
     named = set(p["table"].flatten().tolist())
     for page in range(len(p["codes"])):
         if page not in named:
@@ -230,7 +251,7 @@ def test_workspace_on_another_stream():
 
 
 def test_captured():
-    p = problem([(1000, [(100 + i, 1) for i in range(6)])], [(300, 1)], 8, 2, 128, 64, DT["bf16"], seed=14, room=3)
+    p = problem([(1000, [(100 + i, 1) for i in range(6)])], [(300, 1)], 8, 2, 128, 64, DT["bf16"], seed=14)
     dev = {k: v.cuda() for k, v in p.items() if isinstance(v, torch.Tensor)}
     cu, seq, cug, prefix = i32(p["cu"]), i32(p["seq"]), i32(p["cug"]), i32(p["prefix"])
     out = torch.empty(p["q"].shape, dtype=torch.bfloat16, device="cuda")
