@@ -21,13 +21,13 @@ constexpr int kNone = 0x7fffffff;
 // Sums are of integers and the order is that of the pairs, so timing shows
 // nowhere.  Bound by the chain of dependent reads of the five steps; they are
 // one launch where one workgroup will do, else five.
+//
+// Entries that a row holds and takes again at the same place (those before its
+// new end when it is its own source, pages that it shares with its source) give
+// and take the same page and are left out.
 
-struct Pair {
-    int act;         // whether the row changes
-    int r, s;        // row and source (-1: empty)
-    int len, held;   // new length; entries of the row now
-};
-enum { kAct, kRow, kSource, kLen, kHeld, kGone, kCopy, kEnd };  // of info[i]
+// Of info[i]; kFrom: entries before it are left out.
+enum { kAct, kRow, kFrom, kLen, kHeld, kGone, kCopy, kEnd };
 
 __device__ inline bool page_of(const ForkArgs& a, int p) { return p >= 0 && p < a.N; }
 __device__ inline int held_of(const ForkArgs& a, int len) {
@@ -52,6 +52,11 @@ __device__ inline int wave_add(int x) {
     return x;
 }
 
+// What atomics changed is read past the first cache, which they do not change.
+template <typename T>
+__device__ inline T changed(const T* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 __device__ inline void clear_page(const ForkArgs& a, int p) {
     a.count[p] = 0;
     a.tail[p] = kNone;
@@ -84,22 +89,20 @@ __device__ inline void fork_read(const ForkArgs& a, int i, int lane) {
         held = held_of(a, now);
         act = !(s == r && len == now);
     }
+    const int from = s == r ? len / a.P : 0;
     if (lane == 0) {
         info[kAct] = act;
         info[kRow] = r;
-        info[kSource] = s;
+        info[kFrom] = from;
         info[kLen] = len;
         info[kHeld] = held;
     }
     if (!act) return;
-    for (int e = lane; e < held; e += 64) {
-        const int p = a.table[r * a.M + e];
-        if (page_of(a, p)) clear_page(a, p);
-    }
     const int end = held_of(a, len);
-    for (int e = lane; e < end; e += 64) {
-        const int p = a.table[s * a.M + e];
-        a.fresh[i * a.M + e] = page_of(a, p) ? p : -1;
+    for (int e = from + lane; e < held || e < end; e += 64) {
+        const int old = e < held ? a.table[r * a.M + e] : -1, p = e < end ? a.table[s * a.M + e] : -1;
+        if (e < end) a.fresh[i * a.M + e] = page_of(a, p) ? p : -1;
+        if (page_of(a, old)) clear_page(a, old);
         if (page_of(a, p)) clear_page(a, p);
     }
 }
@@ -111,22 +114,23 @@ __device__ inline void fork_count(const ForkArgs& a, int i, int lane) {
     if (!info[kAct]) return;
     const int* row = a.table + info[kRow] * a.M;
     const int* fresh = a.fresh + i * a.M;
-    for (int e = lane; e < info[kHeld]; e += 64) {
-        const int p = row[e];
-        if (!page_of(a, p)) continue;
-        atomicAdd(&a.count[p], -1);
-        atomicMin((unsigned long long*)&a.first[p], (unsigned long long)entry_no(i, e));
+    const int whole = info[kLen] / a.P, held = info[kHeld];
+    for (int e = info[kFrom] + lane; e < held || e < whole; e += 64) {
+        const int old = e < held ? row[e] : -1, p = e < whole ? fresh[e] : -1;
+        if (old == p) continue;
+        if (page_of(a, old)) {
+            atomicAdd(&a.count[old], -1);
+            atomicMin((unsigned long long*)&a.first[old], (unsigned long long)entry_no(i, e));
+        }
+        if (p >= 0) atomicAdd(&a.count[p], 1);
     }
-    const int whole = info[kLen] / a.P;
-    for (int e = lane; e < whole; e += 64)
-        if (fresh[e] >= 0) atomicAdd(&a.count[fresh[e]], 1);
     if (lane == 0 && info[kLen] % a.P && fresh[whole] >= 0) atomicMin(&a.tail[fresh[whole]], i);
 }
 
 // Rows that hold a page whole afterwards, not counting one that goes on in it.
-__device__ inline int base_of(const ForkArgs& a, int p) { return a.shares[p] + 1 + a.count[p]; }
+__device__ inline int base_of(const ForkArgs& a, int p) { return a.shares[p] + 1 + changed(&a.count[p]); }
 __device__ inline bool gives_up(const ForkArgs& a, int p, int i, int e) {
-    return base_of(a, p) <= 0 && a.tail[p] == kNone && a.first[p] == entry_no(i, e);
+    return base_of(a, p) <= 0 && changed(&a.tail[p]) == kNone && changed(&a.first[p]) == entry_no(i, e);
 }
 
 __device__ inline void fork_sum(const ForkArgs& a, int i, int lane) {
@@ -137,7 +141,7 @@ __device__ inline void fork_sum(const ForkArgs& a, int i, int lane) {
     }
     const int* row = a.table + info[kRow] * a.M;
     int gone = 0;
-    for (int e = lane; e < info[kHeld]; e += 64) {
+    for (int e = info[kFrom] + lane; e < info[kHeld]; e += 64) {
         const int p = row[e];
         if (page_of(a, p) && gives_up(a, p, i, e)) ++gone;
     }
@@ -145,7 +149,7 @@ __device__ inline void fork_sum(const ForkArgs& a, int i, int lane) {
     if (lane) return;
     const int whole = info[kLen] / a.P;
     const int p = info[kLen] % a.P ? a.fresh[i * a.M + whole] : -1;
-    const bool mine = p >= 0 && base_of(a, p) <= 0 && a.tail[p] == i;
+    const bool mine = p >= 0 && base_of(a, p) <= 0 && changed(&a.tail[p]) == i;
     info[kGone] = gone;
     info[kCopy] = p >= 0 && !mine;
     info[kEnd] = mine ? p : -1;  // the page that the row goes on in
@@ -153,7 +157,7 @@ __device__ inline void fork_sum(const ForkArgs& a, int i, int lane) {
 
 __device__ inline int next_shares(const ForkArgs& a, int p) {
     const int base = base_of(a, p);
-    const int refs = base > 0 ? base : a.tail[p] != kNone;
+    const int refs = base > 0 ? base : changed(&a.tail[p]) != kNone;
     return refs > 1 ? refs - 1 : 0;
 }
 
@@ -193,7 +197,7 @@ __device__ inline void fork_give(const ForkArgs& a, int i, int lane) {
     if (info[kGone]) {
         before(a, kGone, i, lane, upto, all);
         int64_t at = (int64_t)list_len(a) + upto;
-        for (int e0 = 0; e0 < info[kHeld]; e0 += 64) {
+        for (int e0 = info[kFrom]; e0 < info[kHeld]; e0 += 64) {
             const int e = e0 + lane, p = e < info[kHeld] ? row[e] : -1;
             const bool gone = page_of(a, p) && gives_up(a, p, i, e);
             const uint64_t m = __ballot(gone);
@@ -202,13 +206,12 @@ __device__ inline void fork_give(const ForkArgs& a, int i, int lane) {
             at += __popcll(m);
         }
     }
-    for (int e = lane; e < info[kHeld]; e += 64) {
-        const int p = row[e];
-        if (page_of(a, p)) a.next[p] = next_shares(a, p);
-    }
     const int end = held_of(a, info[kLen]);
-    for (int e = lane; e < end; e += 64)
-        if (fresh[e] >= 0) a.next[fresh[e]] = next_shares(a, fresh[e]);
+    for (int e = info[kFrom] + lane; e < info[kHeld] || e < end; e += 64) {
+        const int old = e < info[kHeld] ? row[e] : -1, p = e < end ? fresh[e] : -1;
+        if (page_of(a, old)) a.next[old] = next_shares(a, old);
+        if (p >= 0) a.next[p] = next_shares(a, p);
+    }
 }
 
 __device__ inline void fork_take(const ForkArgs& a, int i, int lane) {
@@ -229,15 +232,13 @@ __device__ inline void fork_take(const ForkArgs& a, int i, int lane) {
                 tokens = len % a.P;
             }
         }
-        const int held = info[kHeld], n = held > whole + 1 ? held : whole + 1;
-        for (int e = lane; e < n && e < a.M; e += 64) {
-            const int p = row[e];
-            if (e < held && page_of(a, p)) a.shares[p] = a.next[p];
-            row[e] = e < whole ? fresh[e] : e == whole ? end : -1;
+        const int held = info[kHeld], n = held > whole + 1 ? held : whole + 1, mine = held_of(a, len);
+        for (int e = info[kFrom] + lane; e < n && e < a.M; e += 64) {
+            const int old = e < held ? row[e] : -1, p = e < mine ? fresh[e] : -1;
+            if (page_of(a, old)) a.shares[old] = a.next[old];
+            if (p >= 0) a.shares[p] = a.next[p];
+            row[e] = e < whole ? p : e == whole ? end : -1;
         }
-        const int mine = held_of(a, len);
-        for (int e = lane; e < mine; e += 64)
-            if (fresh[e] >= 0) a.shares[fresh[e]] = a.next[fresh[e]];
         if (lane == 0) {
             const int n = end >= 0 ? len : whole * a.P;
             a.lens[r] = n;
@@ -253,16 +254,12 @@ __global__ __launch_bounds__(kForkThreads) void k_fork_one(ForkArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     constexpr int W = kForkThreads / 64;
     for (int i = wave; i < a.n; i += W) fork_read(a, i, lane);
-    __threadfence();
     __syncthreads();
     for (int i = wave; i < a.n; i += W) fork_count(a, i, lane);
-    __threadfence();
     __syncthreads();
     for (int i = wave; i < a.n; i += W) fork_sum(a, i, lane);
-    __threadfence();
     __syncthreads();
     for (int i = wave; i < a.n; i += W) fork_give(a, i, lane);
-    __threadfence();
     __syncthreads();
     for (int i = wave; i < a.n; i += W) fork_take(a, i, lane);
 }
@@ -443,9 +440,9 @@ __global__ __launch_bounds__(kCopyThreads) void k_kv4_copy(CopyArgs a) {
 }  // namespace
 
 hipError_t launch_kv_fork(const ForkArgs& a, hipStream_t s) {
-    // One workgroup has 16 waves: up to 64 pairs its steps are shorter than
-    // four launches more.
-    if (a.n <= 64) {
+    // One workgroup has 16 waves: rows of 64 entries, four a wave, take its steps
+    // less time than four launches more.
+    if (a.n <= 64 && a.n * a.M <= 64 * 256) {
         k_fork_one<<<dim3(1), dim3(kForkThreads), 0, s>>>(a);
         return hipGetLastError();
     }

@@ -53,10 +53,10 @@ fk_status check_verify_sizes(int64_t B, int64_t T, int64_t V) {
 
 // Elements of a piece of a row where `rows` of them are read: whole 16-byte
 // accesses, and then the pieces that are left.
-void verify_pieces(int64_t rows, int64_t V, int32_t& chunks, int32_t& len) {
-    const int64_t c = verify_chunks(rows, V);
+void cut_rows(int64_t rows, int64_t V, bool greedy, int32_t& pieces, int32_t& len) {
+    const int64_t c = verify_pieces(rows, V, greedy);
     len = (int32_t)(((V + c - 1) / c + 7) / 8 * 8);
-    chunks = (int32_t)((V + len - 1) / len);
+    pieces = (int32_t)((V + len - 1) / len);
 }
 
 // ---- pages --------------------------------------------------------------------------------
@@ -153,7 +153,7 @@ SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, 
     const int na = p.group_cols;
     const int64_t room = max_blocks < 0 ? 0 : max_blocks;
     p.use = groups <= kSharedGroups && B <= 8192 && room <= 1 << 22 && tiles * Hkv <= 65535 &&
-            (room + kSharedUnit) * tiles <= (1 << 27) / B && (most_cols > 1 ? rows <= 32 : tiles <= 4);
+            (room + kSharedUnit) * tiles <= (1 << 27) / B;
     if (p.use && max_blocks >= 0) {
         // What sharing saves, in tenths of a microsecond of a wave, were all of the
         // table's room (or the window) the prefix, against the 8 us that finding
@@ -164,7 +164,13 @@ SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, 
         int64_t seen = room;
         if (window > 0 && seen > (window + max_q) / kKvBlock + 2) seen = (window + max_q) / kKvBlock + 2;
         const double wide = D == 64 ? 0.6 : D == 128 ? 1.0 : 2.2;  // of a block's time
-        const double saved = wide * (double)(B * tiles * (3 + 5 * nb) - groups * group_time) * Hkv * (double)seen;
+        const int64_t plain_cols = (rows + 15) / 16 < most_cols ? (rows + 15) / 16 : most_cols;
+        const int64_t plain_time = (rows + 16 * plain_cols - 1) / (16 * plain_cols) * (3 + 5 * plain_cols);
+        // a tile is a workgroup's: more of them than fit at once take whole rounds
+        const int64_t all_tiles = groups * ((mean + 16 * na - 1) / (16 * na)) * Hkv, rounds = (all_tiles + 511) / 512;
+        const double full = rounds > 1 ? 512.0 * (double)rounds / (double)all_tiles : 1.0;
+        const double saved =
+            wide * ((double)(B * plain_time) - (double)(groups * group_time) * full) * Hkv * (double)seen;
         p.use = saved >= (room <= 64 ? 3e5 : 9e4);
     }
     if (!p.use) return p;
@@ -255,10 +261,10 @@ fk_status fk_rope(const fk_rope_args* p, int32_t n, const fk_rope_rows* rows, vo
 size_t fk_verify_workspace_bytes(int64_t B, int64_t T, int64_t V) {
     if (check_verify_sizes(B, T, V) != FK_OK) return 0;
     int32_t by_request, by_row, len;
-    verify_pieces(B, V, by_request, len);
-    verify_pieces(T, V, by_row, len);
+    cut_rows(B, V, false, by_request, len);
+    cut_rows(T, V, true, by_row, len);
     const size_t sampling = (size_t)B * by_request * 2, greedy = (size_t)T * by_row;
-    return (sampling > greedy ? sampling : greedy) * sizeof(uint64_t);
+    return (sampling > greedy ? sampling : greedy) * sizeof(uint64_t) + (size_t)B * sizeof(int32_t);
 }
 
 fk_status fk_verify(const fk_verify_args* p, void* ws, size_t ws_bytes, void* stream) {
@@ -301,8 +307,9 @@ fk_status fk_verify(const fk_verify_args* p, void* ws, size_t ws_bytes, void* st
     a.accepted = p->accepted;
     a.emitted = p->emitted;
     a.keep = p->keep;
-    verify_pieces(p->accept ? p->B : p->T, p->V, a.chunks, a.len);
+    cut_rows(p->accept ? p->B : p->T, p->V, !p->accept, a.pieces, a.len);
     a.sums = static_cast<uint64_t*>(ws);
+    a.kept = reinterpret_cast<int32_t*>(a.sums + p->B * a.pieces * 2);  // sampling only
     const hipError_t e = launch_verify(a, p->dtype, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? FK_OK : hip_fail(e, "fk_verify");
 }

@@ -33,11 +33,12 @@ struct VerifyArgs {
     int64_t p_row, q_row;
     const float *u, *pick;
     int32_t *accepted, *emitted, *keep;
-    int32_t chunks, len;  // pieces of a row, elements of one
-    uint64_t* sums;       // sampling: [B][chunks][2]; greedy: [T][chunks]
+    int32_t pieces, len;  // of a row; elements of one
+    uint64_t* sums;       // sampling: [B][pieces][2]; greedy: [T][pieces]
+    int32_t* kept;        // sampling: [B] drafts kept
 };
 // Pieces a row of V is cut into where `rows` of them are read.
-int verify_chunks(int64_t rows, int64_t V);
+int verify_pieces(int64_t rows, int64_t V, bool greedy);
 hipError_t launch_verify(const VerifyArgs& a, int dtype, hipStream_t s);
 
 // ---- pages ------------------------------------------------------------------------

@@ -60,9 +60,9 @@ def test_verify_arguments(kw, status):
 def test_verify_workspace():
     size = fk.lib.fk_verify_workspace_bytes
     assert size(0, 1, 1) == size(1, 1, (1 << 20) + 1) == 0
-    assert size(1, 1, 1) == 16
+    assert size(1, 1, 1) == 16 + 4
     # a sum for what is left and one for the row, of each piece; a row's largest of each piece
-    assert size(64, 384, 128000) >= 64 * 16 * 16 and size(1, 1, 1 << 20) <= 1024 * 16
+    assert size(64, 384, 128000) >= 64 * 64 * 16 + 64 * 4 and size(1, 1, 1 << 20) <= 4096 * 16 + 4
 
 
 def pool(R=4, M=8, N=50, P=64, reserved=0, table=FAKE, lens=FAKE, shares=FAKE, free=FAKE, count=FAKE):
