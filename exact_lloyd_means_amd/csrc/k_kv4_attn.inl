@@ -243,15 +243,17 @@ struct Block {
     uintx4 k[D / 64], v[D / 64], ks, vs;
     bool there;
 
+    // Both scales come with k's codes: the weights need them, and waiting for the
+    // last load of a block would be waiting for v's codes, a softmax too early.
     __device__ inline void load_k(const Source& s) {
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) k[i] = *reinterpret_cast<const uintx4*>(s.k + 1024 * i);
         ks = *reinterpret_cast<const uintx4*>(s.ks);
+        vs = *reinterpret_cast<const uintx4*>(s.vs);
     }
     __device__ inline void load_v(const Source& s) {
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) v[i] = *reinterpret_cast<const uintx4*>(s.v + 1024 * i);
-        vs = *reinterpret_cast<const uintx4*>(s.vs);
         there = s.there;
     }
 };
@@ -435,9 +437,9 @@ struct Wave {
             x = max3(x, s[1][t][1], s[1][t][2]);
             top[t] = max2(x, s[1][t][3]);
         }
-        blk.load_k(next);
         // a weight might pass 2^kTop: by bounds, largest score and largest scale
         const uint32_t bits = max_u16(max_u16(vw[0], vw[1]), max_u16(vw[2], vw[3]));
+        blk.load_k(next);
         bool raise = max_u16(bits, limit) != limit;
 #pragma unroll
         for (int t = 0; t < NT; ++t) raise |= fmaf(top[t], qs[t], -m[t]) > slack;

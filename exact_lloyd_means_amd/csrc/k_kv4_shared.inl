@@ -285,47 +285,76 @@ __device__ inline Shares shared_plan(const AttnArgs& a, const SharedArgs& s, uin
 
 // Walk with DEPTH blocks on their way.  Two waves a SIMD, as many as the tiles'
 // registers leave, do not cover the way to memory with one block each; a wave of
-// few rows has the registers for more.
+// few rows has the registers for more.  The pages of 64 blocks are looked up at
+// once, one a lane: a lookup a block, which the compiler moves down to where its
+// page is used, made every block wait for all loads before it.
 template <int D, int DEPTH>
 struct DeepWalk {
-    Walk<D> at;
-    Block<D> more[DEPTH];
+    const int32_t* table;
+    int h, first, end, stride;
+    int pages, later;  // of blocks 64 n + lane from the first, and the 64 behind them
+    Block<D> blk[DEPTH];
 
+    __device__ inline int lookup_pages(const AttnArgs& a, int n, int lane) const {
+        // (a walk has fewer than 2^26 blocks)
+        int b = first + (n + lane) * stride;
+        b = b < end ? b : end - 1;
+        return table[a.bpp == 1 ? b : (int)(((uint64_t)(uint32_t)b * a.bpp_magic) >> 32)];
+    }
+    __device__ inline Source source(const AttnArgs& a, int page, int b, int lane) const {
+        const int in = a.bpp == 1 ? 0 : b - (int)(((uint64_t)(uint32_t)b * a.bpp_magic) >> 32) * (int)a.bpp;
+        Source s;
+        s.there = (uint32_t)page < (uint32_t)a.pages;
+        const int64_t at = ((int64_t)(s.there ? page : 0) * a.Hkv + h) * 2;
+        const int64_t code = (at * a.bpp + in) * (16 * D), row = at * a.page_size + in * kKvBlock;
+        s.k = a.codes + code + lane * 16;
+        s.v = a.codes + (code + (int64_t)a.bpp * (16 * D)) + lane * 16;
+        s.ks = a.scales + row + 8 * (lane >> 4);
+        s.vs = a.scales + (row + a.page_size) + 8 * (lane >> 4);
+        return s;
+    }
+    // Block n of the walk (n - DEPTH is the one at hand).
+    __device__ inline Source nth(const AttnArgs& a, int n, int lane) {
+        int b = first + n * stride;
+        b = b < end ? b : end - 1;
+        return source(a, __builtin_amdgcn_readlane(pages, n & 63), b, lane);
+    }
     __device__ inline void begin(const AttnArgs& a, const int32_t* row, int head, int lo, int hi, int by,
                                  int lane) {
-        at.table = row;
-        at.h = head;
-        at.first = lo;
-        at.end = hi;
-        at.stride = by;
-        int page[DEPTH], in[DEPTH];
+        table = row;
+        h = head;
+        first = lo;
+        end = hi;
+        stride = by;
+        pages = lookup_pages(a, 0, lane);
+        later = (hi - lo) / 64 >= by ? lookup_pages(a, 64, lane) : pages;
 #pragma unroll
         for (int i = 0; i < DEPTH; ++i) {
-            at.ahead(a, lo + i * by);
-            page[i] = at.page;
-            in[i] = at.in;
+            const Source src = nth(a, i, lane);
+            blk[i].load_k(src);
+            blk[i].load_v(src);
+            // in this order: a first block loaded last would have the loop wait for all
+            __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int i = 0; i < DEPTH; ++i) {
-            at.page = page[i];
-            at.in = in[i];
-            const Source src = at.source(a, lane);
-            more[i].load_k(src);
-            more[i].load_v(src);
-        }
-        at.ahead(a, lo + DEPTH * by);
     }
     template <int DT, int NT>
     __device__ inline void run(const AttnArgs& a, Wave<D, DT, NT>& wv, int lane) {
         const uint32_t lane4 = 4 * (lane & 31);
         const int g = lane >> 4;
-        for (int b = at.first;;) {
+        int n = 0;
+        for (int b = first; b < end;) {
 #pragma unroll
-            for (int i = 0; i < DEPTH; ++i, b += at.stride) {
-                if (b >= at.end) return;
-                const Source next = at.source(a, lane);
-                at.ahead(a, b + (DEPTH + 1) * at.stride);
-                wv.step(more[i], next, b * kKvBlock, lane4, g, a.qk);
+            for (int i = 0; i < DEPTH; ++i) {
+                if (b < end) {
+                    if (((n + DEPTH) & 63) == 0) {  // the next 64 pages
+                        pages = later;
+                        later = lookup_pages(a, n + DEPTH + 64, lane);
+                    }
+                    const Source next = nth(a, n + DEPTH, lane);
+                    wv.step(blk[i], next, b * kKvBlock, lane4, g, a.qk);
+                }
+                b += stride;
+                ++n;
             }
         }
     }
