@@ -9,6 +9,7 @@ import torch
 import exact_lloyd_means_amd as fk
 import kv4_ref as ref
 import serve_ref
+from test_gpu_streams import Bystanders, stall
 
 pytestmark = pytest.mark.gpu
 H, Hq, D, P = 2, 4, 64, 32
@@ -253,3 +254,84 @@ def test_a_step_captured():
         for a, b in zip((*first, *second), (*want[0], *want[1])):
             assert torch.equal(a, b)
         assert torch.equal(caches[0].lens, caches[1].lens) and torch.equal(caches[0].block_table, caches[1].block_table)
+
+
+def test_more_rows_than_a_call_takes():
+    # 70000 names of the same rows: each is shortened to the least of its lengths, once
+    s = Serving(20, 4)
+    s.step([100, 64, 33, 0])
+    rows = torch.arange(70000, device="cuda") % 4
+    keep = torch.full((70000,), 90, device="cuda")
+    keep[69990:] = 40                                                # in the second call
+    s.cache.release(rows, keep=keep)
+    for b, n in enumerate([40, 40, 33, 0]):
+        s.k[b], s.v[b] = s.k[b][:n], s.v[b][:n]
+    s.check()
+
+
+def test_all_of_it_on_another_stream():
+    # what the calls take for themselves belongs to the stream they run on
+    side = torch.cuda.Stream()
+    V, out = 3000, []
+    for stream in (None, side):
+        g = torch.Generator("cuda").manual_seed(5)
+        cache = fk.KV4Cache(60, P, H, D, ref.codebook(H, 0).cuda(), 4, 400)
+        q, k, v = (torch.randn(43, h, D, device="cuda", generator=g).bfloat16() for h in (Hq, H, H))
+        p = torch.rand(43, V, device="cuda", generator=g).softmax(-1)
+        u, pick = torch.rand(43, device="cuda", generator=g), torch.rand(4, device="cuda", generator=g)
+        n, rows, src, turns = i32([40, 1, 2, 0]), i32([1, 2, 3]), i32([0, 0, 0]), fk.rope_turns(D)
+        cug, prefix, tokens = i32([0, 4]), i32([32]), p.argmax(-1).roll(1).int()
+        ones, zero = i32([1, 1, 1, 1]), i32([0])                     # inputs live until the stream has run
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        if stream is not None:
+            stall(stream)
+        cache.plan(n, 43, stream=stream)
+        cache.rotate(q, k, turns, stream=stream)
+        cache.append(k, v, stream=stream)
+        a = cache.attend(q, 40, stream=stream)
+        b = cache.verify(tokens, p, None, u, pick, stream=stream)
+        c = cache.fork(rows, src, stream=stream)
+        cache.plan(ones, 4, stream=stream)
+        cache.append(k[:4], v[:4], stream=stream)
+        e = cache.attend(q[:4], 1, shared=(cug, prefix), stream=stream)
+        cache.release(zero, stream=stream)
+        f = cache.compact(stream=stream)
+        assert stream is None or Bystanders([1 << 12, 1 << 16, 1 << 20]).untouched()
+        torch.cuda.synchronize()
+        out.append([a, *b, c, e, f, cache.lens, cache.block_table, cache.shares, cache.codes, cache.scales])
+    for x, y in zip(*out):
+        assert torch.equal(x, y)
+
+
+def test_two_graphs_on_one_workspace():
+    # forks and verification captured twice with the same workspaces, replayed in turn
+    R, V = 6, 900
+    s = Serving(50, R)
+    s.step([70, 33, 1, 64, 0, 5])
+    c = s.cache
+    ws = fk.kv_fork_workspace(R, c.block_table, c.shares)
+    pool = (P, c.block_table, c.lens, c.shares, c.free_pages, c.free_count)
+    copies = i32([[0] * 3] * R)
+    plans = [([4, 2], [0, 3], [70, 64]), ([1, 0, 5], [1, 4, 0], [20, 50, 60])]
+    p = torch.rand(5, V, device="cuda").softmax(-1)
+    cu, tokens, u, pick = i32([0, 2, 5]), i32([0, 3, 0, 5, 7]), torch.rand(5, device="cuda"), torch.rand(2, device="cuda")
+    vws, accepted, emitted = fk.verify_workspace(cu, p), [i32([0, 0]) for _ in plans], [i32([0] * 5) for _ in plans]
+    args = [(i32(a), i32(b), i32(k)) for a, b, k in plans]
+    graphs = []
+    for i, (a, b, k) in enumerate(args):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            fk.fk_kv_fork(a, b, k, *pool, copies[:len(a)], seq=c._seq, ws=ws)
+            fk.fk_kv4_copy(copies[:len(a)], c.codes, c.scales)
+            fk.fk_verify(cu, tokens, p, accepted[i], emitted[i], accept=u if i else None, pick=pick if i else None, ws=vws)
+    want = [serve_ref.verify([0, 2, 5], tokens.tolist(), p, None, u.tolist() if i else None, pick.tolist() if i else None, [0, 0]) for i in (0, 1)]
+    for turn in range(4):
+        i = turn % 2
+        graphs[i].replay()
+        rows, src, keep = plans[i]
+        k, v = list(s.k), list(s.v)
+        for r, x, n in zip(rows, src, keep):
+            s.k[r], s.v[r] = k[x][:n], v[x][:n]
+        s.check()
+        assert accepted[i].tolist() == want[i][0] and emitted[i].tolist() == [want[i][1][r] for r in range(5)]
