@@ -5,16 +5,26 @@
 // make a tile that walks the prefix once, whatever requests they belong to: for
 // single tokens a tile serves 16 NA / G requests instead of one, and a block's
 // codes are read and looked up that many times less.  What lies behind the
-// prefix is walked for each request as in the split form.  Three launches:
+// prefix is walked for each request as in the split form.  Two launches:
 //
-//   k_kv4_shared_plan  one workgroup: what every query token sees of the prefix,
-//                      the segments of the tiles' keys (one a workgroup), the
-//                      shares of the requests' own keys (one a wave)
-//   k_kv4_shared_walk  segments and shares; sums of rows go to the workspace
+//   k_kv4_shared_walk  segments of the tiles' keys (one a workgroup) and shares of
+//                      the requests' own keys (one a wave), as many workgroups for
+//                      each as let them end together; sums of rows go to the
+//                      workspace
 //   k_kv4_shared_join  adds up the segments and shares of each request, in order
 //
-// Both kinds of work run in one launch; the plan gives each as many workgroups as
-// let them end together.
+// 64 requests of 16-600 tokens behind 8192 shared ones, 32 / 8 heads of 128: 36.7 us
+// a call (plain 85): 5 us until a workgroup knows its work, 4 until its codes are
+// there, 19 of blocks (1.8 us each at two waves a SIMD; 13 us of it vector
+// instructions, which overlap little with the matrix instructions), 3 to add up
+// its waves, 5 in the join.  Eight groups of sixteen behind 1000-6000, 64 / 8 heads,
+// 122 MB of codes: 68 us (plain 86); memory would take 26, the vector instructions
+// 23: with two waves a SIMD neither hides the other.
+//
+// Tried: the plan as a launch of its own (8 us; 3 to 7 here), pieces of the line of
+// all tiles instead of segments of each (a workgroup in two tiles pays both ends: 8
+// x 16 63 -> 75 us), more workgroups than run at once (37 -> 50), 32 rows a wave of
+// 256 dimensions at one wave a SIMD (82 -> 98 us of 180 requests).
 #pragma once
 
 #include "k_kv4_attn.inl"

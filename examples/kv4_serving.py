@@ -4,6 +4,10 @@ the unquantised rows.
 
     python examples/kv4_serving.py [--steps 8]
 
+Then one prompt is continued in four ways: its pages are shared and read once
+for all, each step brings drafts, and those that the target refuses are taken
+back.
+
 There is no model here: queries, keys and values are drawn at random, keys
 with channels that stand out as they do after rotary embeddings.  The error
 is that of 4 bits, shown for the learned codebooks and for 16 equal steps.
@@ -73,6 +77,40 @@ def serve(codebook, steps, seed=1):
     return errors
 
 
+def continued(codebook, steps, samples=4, drafts=3, vocabulary=5000, seed=2):
+    """A prompt continued in `samples` ways by `steps` steps of drafts; pages in
+    use, pages that rows of their own would take, tokens a step and sample."""
+    source, turns = Source(seed), fk.rope_turns(D)
+    cache = fk.KV4Cache(200, P, H, D, codebook, max_requests=samples, max_len=2048)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    prompt, kept = 900, 0
+
+    def step(new, total, max_q, shared=None):
+        cache.plan(new, total)
+        q, k, v = source(total)
+        cache.rotate(q, k, turns)
+        cache.append(k, v)
+        return cache.attend(q, max_q, shared=shared)
+    step(torch.tensor([prompt] + [0] * (samples - 1), **i32), prompt, prompt)
+    cache.fork(torch.arange(1, samples, **i32), torch.zeros(samples - 1, **i32))
+    shared = torch.tensor([0, samples], **i32), torch.tensor([prompt // P * P], **i32)
+    new, total = torch.full((samples,), 1 + drafts, **i32), samples * (1 + drafts)
+    for _ in range(steps):
+        step(new, total, 1 + drafts, shared)
+        # distributions such as a model and a small model that drafts for it give
+        logits = torch.randn(total, vocabulary, device="cuda", generator=source.g)
+        near = logits + 0.5 * torch.randn(total, vocabulary, device="cuda", generator=source.g)
+        target, draft = logits.softmax(-1), near.softmax(-1)
+        tokens = torch.multinomial(draft, 1, generator=source.g)[:, 0].int().roll(1)
+        accepted, _ = cache.verify(tokens, target, draft, torch.rand(total, device="cuda", generator=source.g),
+                                   torch.rand(samples, device="cuda", generator=source.g))
+        kept += int(accepted.sum()) + samples
+    lens = cache.lens.tolist()
+    assert sum(lens) == samples * prompt + kept and cache.status.tolist()[2:] == [0, 0]
+    alone = sum(-(-n // P) for n in lens)
+    return 200 - int(cache.free_count), alone, kept / (steps * samples)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--steps", type=int, default=8)
@@ -84,6 +122,8 @@ def main():
         e = serve(codebook, steps)
         print(f"{name:15s} error of the prompts {e[0]:.4f}, of single tokens "
               f"{sum(e[1:]) / max(1, len(e) - 1):.4f}")
+    used, alone, tokens = continued(learned, max(1, steps))
+    print(f"one prompt in four ways: {used} pages instead of {alone}, {tokens:.2f} tokens a step")
 
 
 if __name__ == "__main__":
