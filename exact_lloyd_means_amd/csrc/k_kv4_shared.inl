@@ -41,7 +41,7 @@ template <int NT>
 constexpr int kBlockTime = 3 + 5 * NT;
 template <int NT>
 constexpr int kOwnTime = NT < 2 ? 13 : kBlockTime<NT>;
-constexpr int kSegmentTime = 110, kShareTime = 80;
+constexpr int kSegmentTime = 110, kShareTime = 80, kAgainTime = 60;  // a share behind a segment
 constexpr int kUnitBlocks = kSharedUnit;
 
 // Row tiles of requests.
@@ -108,7 +108,16 @@ struct Shares {
     int segments;  // of all groups; workgroups from the first on take one each
     int seg_len;   // most blocks of one
     int total;     // the line of units: kUnitBlocks and the own blocks of each
-    int share;     // what a wave takes of it; the last workgroup's waves first
+    // What a wave takes of it, the last workgroup's waves first: `share` each of
+    // `border` waves, `extra` each of those that had a segment before.
+    int share, extra, border;
+    __device__ inline int64_t begin(int w) const {
+        return w <= border ? (int64_t)w * share : (int64_t)border * share + (int64_t)(w - border) * extra;
+    }
+    __device__ inline int wave_of(int64_t at) const {
+        const int64_t rest = at - (int64_t)border * share;
+        return rest < 0 ? (int)at / share : border + (int)rest / extra;
+    }
 };
 
 // Who does what.  Every workgroup finds out by itself: a launch before would
@@ -208,13 +217,18 @@ __device__ inline Shares shared_plan(const AttnArgs& a, const SharedArgs& s, uin
     }
     __syncthreads();
     // The least number k of blocks that every wave of a segment takes, with shares
-    // that last as long, for which the workgroups are enough.
+    // that last as long, for which the workgroups are enough.  Where segments are
+    // over before that because their groups are, their waves take shares as well.
     auto share_of = [&](int k) {
         const int y = (k * kBlockTime<NA> + kSegmentTime - kShareTime) / kOwnTime<NB>;
         return y > a.least ? y : a.least;
     };
-    const int tiles = *tiles_all;
-    int lo = 1, hi = (*longest + W - 1) / W;
+    const int tiles = *tiles_all, whole = (*longest + W - 1) / W;
+    auto extra_of = [&](int k) {
+        const int y = k > whole ? ((k - whole) * kBlockTime<NA> - kAgainTime) / kOwnTime<NB> : 0;
+        return y < a.least ? 0 : y;
+    };
+    int lo = 1, hi = whole;
     {
         const int room = W * (s.wgs - tiles), need = total / room + 2;
         const int k = need / kBlockTime<NA> * kOwnTime<NB> + kOwnTime<NB> + 1;
@@ -224,15 +238,15 @@ __device__ inline Shares shared_plan(const AttnArgs& a, const SharedArgs& s, uin
         const int step = (hi - lo + kAttnThreads - 1) / kAttnThreads, k = lo + tid * step;
         bool enough = false;
         if (k < hi) {
-            // each at least its ceiling: lengths are below 2^22, total below 2^27
-            const float each = 1.f / (float)(k * W);
-            int n = (int)((float)total / (float)(W * share_of(k))) + 2;
+            // segments, at least their ceilings: lengths are below 2^22
+            const float each = 1.000001f / (float)(k * W);
+            int n = 0;
             for (int g = 0; g < s.groups && n <= s.wgs; ++g) {
                 const int len = grp[g].len;
-                const int64_t t = (int64_t)((grp[g].rows + rowsA - 1) / rowsA) * ((int)((float)len * each) + 1);
+                const int64_t t = (int64_t)((grp[g].rows + rowsA - 1) / rowsA) * ((int)((float)(len - 1) * each) + 1);
                 if (len > 0) n = t < s.wgs ? n + (int)t : s.wgs + 1;
             }
-            enough = n <= s.wgs;
+            enough = n <= s.wgs && (int64_t)(s.wgs - n) * W * share_of(k) + (int64_t)n * W * extra_of(k) >= total;
         }
         const uint64_t m = __ballot(enough);
         if ((tid & 63) == 0) scratch[tid >> 6] = m ? lo + (tid + __builtin_ctzll(m)) * step : hi;
@@ -248,6 +262,7 @@ __device__ inline Shares shared_plan(const AttnArgs& a, const SharedArgs& s, uin
     r.total = total;
     r.seg_len = hi * W;
     r.share = share_of(hi);
+    r.extra = extra_of(hi);
     const int per_g = (s.groups + kAttnThreads - 1) / kAttnThreads, g0 = tid * per_g;
     int segs = 0;
     for (int g = g0; g < g0 + per_g && g < s.groups; ++g)
@@ -259,9 +274,15 @@ __device__ inline Shares shared_plan(const AttnArgs& a, const SharedArgs& s, uin
     }
     __syncthreads();
     const bool tell = x == 0 && h == 0;
-    const int64_t begin = (int64_t)(s.wgs - 1 - x) * W * r.share, stop = begin + (int64_t)W * r.share;
-    if (tell && tid == 0) s.head[0] = r.share;
-    if (tell || (x >= r.segments && at < stop && at + mine > begin)) {
+    r.border = (s.wgs - r.segments) * W;
+    const int w0 = (s.wgs - 1 - x) * W;
+    const int64_t begin = r.begin(w0), stop = r.begin(w0 + W);
+    if (tell && tid == 0) {
+        s.head[0] = r.share;
+        s.head[1] = r.extra;
+        s.head[2] = r.border;
+    }
+    if (tell || (at < stop && at + mine > begin)) {
         for (int b = b0; b < b0 + per && b < a.B; ++b) {
             Rows rw = rows_of(b);
             const int g = b == b0 ? my_group : group_of(grp, s.groups, b);
@@ -282,7 +303,7 @@ __device__ inline Shares shared_plan(const AttnArgs& a, const SharedArgs& s, uin
                 if (n <= 0) continue;
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
-                    const int64_t from = begin + w * r.share;
+                    const int64_t from = r.begin(w0 + w);
                     if (from >= at && from < (int64_t)at + n + kUnitBlocks) start[w] = {unit, at};
                 }
                 at += n + kUnitBlocks;
@@ -513,12 +534,16 @@ __global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_shared_walk(AttnArgs a,
         if (some) wk.run(a, wv, lane);
         const int64_t row = ((int64_t)h * s.wgs + x) * (16 * NA);
         store_segment<D, DT, NA>(a, wv, rw.n, a.part_o + row * D, a.part_ml + row * 2, tab, ml, wave, lane);
-        return;
+        if (plan.begin((s.wgs - 1 - x) * W) >= plan.total) return;
+        Codebook book;
+        book.load(a, h, tid);
+        __syncthreads();  // sums of the segment lay in the table's place
+        book.build(tab, tid);
+        __syncthreads();
     }
     const int w = (s.wgs - 1 - x) * W + wave;
-    const int64_t begin = (int64_t)w * plan.share;
-    const int64_t stop = begin + plan.share < plan.total ? begin + plan.share : plan.total;
-    if (begin >= plan.total) return;
+    const int64_t begin = plan.begin(w), to = plan.begin(w + 1), stop = to < plan.total ? to : plan.total;
+    if (begin >= stop) return;
     const int units = a.B * a.row_tiles;
     const int64_t slots = (int64_t)h * (units + 2 * s.wgs * W);
     int unit = __builtin_amdgcn_readfirstlane(start[wave].unit);
@@ -557,10 +582,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void k_kv4_shared_walk(AttnArgs a,
             // share begins within has its place 0, one that goes on in the next
             // share its place 1
             const int64_t slot = take == all ? now : units + 2 * w + (first > begin);
-            AttnArgs to = a;
-            to.part_o = s.own_o;
-            to.part_ml = s.own_ml;
-            store_part<D, DT, NB>(to, wv, rw, slots + slot, lane);
+            AttnArgs own = a;
+            own.part_o = s.own_o;
+            own.part_ml = s.own_ml;
+            store_part<D, DT, NB>(own, wv, rw, slots + slot, lane);
         }
     }
 }
@@ -577,9 +602,12 @@ __global__ __launch_bounds__(kAttnThreads) void k_kv4_shared_join(AttnArgs a, Sh
     const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y - h * a.row_tiles;
     const int unit = b * a.row_tiles + rt, units = a.B * a.row_tiles;
     const int4 u0 = s.unit[3 * (int64_t)unit], u1 = s.unit[3 * (int64_t)unit + 1], u2 = s.unit[3 * (int64_t)unit + 2];
-    const int share = s.head[0];
+    Shares plan{};
+    plan.share = s.head[0];
+    plan.extra = s.head[1];
+    plan.border = s.head[2];
     const int64_t lo = u1.x, hi = lo + u1.y;
-    const int w0 = (int)(lo / share), w1 = hi > lo ? (int)((hi - 1) / share) : w0;
+    const int w0 = hi > lo ? plan.wave_of(lo) : 0, w1 = hi > lo ? plan.wave_of(hi - 1) : 0;
     const bool whole = hi > lo && w0 == w1;
     if (whole && u0.w < 0) return;
     Rows rw;
@@ -614,7 +642,7 @@ __global__ __launch_bounds__(kAttnThreads) void k_kv4_shared_join(AttnArgs a, Sh
                         const int v = w0 + x - segs;
                         po = s.own_o;
                         pm = s.own_ml;
-                        at = (slots + (whole ? unit : units + 2 * v + (v == w0 && lo > (int64_t)v * share ? 1 : 0))) *
+                        at = (slots + (whole ? unit : units + 2 * v + (v == w0 && lo > plan.begin(v) ? 1 : 0))) *
                                  a.part_rows + row;
                     }
                     ml[i] = *reinterpret_cast<const float2*>(pm + at * 2);

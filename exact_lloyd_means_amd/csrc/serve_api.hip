@@ -171,15 +171,17 @@ SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, 
         const double full = rounds > 1 ? 512.0 * (double)rounds / (double)all_tiles : 1.0;
         const double saved =
             wide * ((double)(B * plain_time) - (double)(groups * group_time) * full) * Hkv * (double)seen;
-        p.use = saved >= (room <= 64 ? 3e5 : 9e4);
+        // the requests' own keys as units of shares, where the plain form has no units
+        const double units = wide * (double)(B * tiles * kSharedUnit * (nb == 1 ? 13 : 3 + 5 * nb)) * Hkv;
+        p.use = room <= 64 ? saved - units >= 3e5 : saved >= 9e4;
     }
     if (!p.use) return p;
     p.rows = (int)(rows < 16 * nb ? rows : 16 * nb);
     p.least = p.rows / 2 < 6 ? 6 : p.rows / 2;  // blocks of a share: see the split form; a unit and two blocks
-    // two workgroups a CU; every tile of a group needs one, and the requests
+    // two workgroups a CU; every tile of a group needs one, and one is left
     const int64_t most = T * G / (16 * na) + groups;
     int64_t wgs = 512 / Hkv;
-    if (wgs < most + most / 8 + 1) wgs = most + most / 8 + 1;
+    if (wgs < most + 1) wgs = most + 1;
     p.wgs = (int)wgs;
     const int64_t tiles_all = B * Hkv * tiles;
     int64_t z = 1024 / tiles_all;

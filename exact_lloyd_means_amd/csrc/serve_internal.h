@@ -83,7 +83,7 @@ struct SharedArgs {       // beside AttnArgs, whose part_o and part_ml are the s
                           // [heads][wgs][16 NA rows]
     const int32_t *cu_groups, *prefix;
     int32_t groups, wgs;  // wgs: workgroups of a head
-    int32_t* head;        // [1] length of a share
+    int32_t* head;        // [3] lengths of shares, and how many have the first
     int4* unit;           // [units][3] for the join: first token, tokens, length, group or -1; place
                           // in the line, own blocks; first row in the group's tiles, first
                           // segment, segments of a tile
