@@ -152,23 +152,37 @@ SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, 
     }
     const int na = p.group_cols;
     const int64_t room = max_blocks < 0 ? 0 : max_blocks;
+    // Two workgroups a CU run at once; every tile of a group needs one, and one is
+    // left.  A tile's segments are a workgroup's each, so tiles that leave much of
+    // the card empty are better cut for two rounds, unless they are so short that
+    // starting again (15 us) costs more.
+    const int64_t most = T * G / (16 * na) + groups, round = 512 / Hkv < 1 ? 1 : 512 / Hkv;
+    int64_t seen = max_blocks < 0 ? 1 << 22 : max_blocks;
+    if (max_blocks >= 0 && window > 0 && seen > (window + max_q) / kKvBlock + 2)
+        seen = (window + max_q) / kKvBlock + 2;
+    const double wide = D == 64 ? 0.6 : D == 128 ? 1.0 : 2.2;  // of a block's time
+    int64_t rounds = most / round + 1;
+    auto time = [&](int64_t r) {
+        const int64_t segs = r * round / (most + 1);
+        return (double)r * (150 + wide * (3 + 5 * na) * (double)((seen + 4 * segs - 1) / (4 * segs)));
+    };
+    if (rounds == 1 && most > round / 4 && time(2) < time(1)) rounds = 2;
+    const int64_t wgs = rounds * round;
     p.use = groups <= kSharedGroups && B <= 8192 && room <= 1 << 22 && tiles * Hkv <= 65535 &&
             (room + kSharedUnit) * tiles <= (1 << 27) / B;
+    // enough rows for the plain form's waves over rows, which beat both
+    const int64_t row_wg = 64 * row_cols(D);
+    p.use = p.use && (rows <= 16 * most_cols || (T * G + row_wg - 1) / row_wg * Hkv < 512);
     if (p.use && max_blocks >= 0) {
         // What sharing saves, in tenths of a microsecond of a wave, were all of the
         // table's room (or the window) the prefix, against the 8 us that finding
         // out who does what costs the walk, or 15 where the plain form is one launch.
-        // Measured over 110 mixes of groups: from 9e4 on 30 of 38 gain (up to 37 us, others
-        // lose up to 17 where the room holds no prefix), below 5 of 30 would, by 3 to 6;
-        // of tables with room for 64 blocks or less, from 3e5 on 1 of 1, below 0 of 41.
-        int64_t seen = room;
-        if (window > 0 && seen > (window + max_q) / kKvBlock + 2) seen = (window + max_q) / kKvBlock + 2;
-        const double wide = D == 64 ? 0.6 : D == 128 ? 1.0 : 2.2;  // of a block's time
+        // Of 400 mixes of groups of one to eight query tokens 59 are shared: 47 of
+        // them gain (at most 81 us, 120 -> 40) and 11 lose, 1 to 11 us but for one
+        // whose prefixes have three blocks of the room's 72 (109 -> 143).
         const int64_t plain_cols = (rows + 15) / 16 < most_cols ? (rows + 15) / 16 : most_cols;
         const int64_t plain_time = (rows + 16 * plain_cols - 1) / (16 * plain_cols) * (3 + 5 * plain_cols);
-        // a tile is a workgroup's: more of them than fit at once take whole rounds
-        const int64_t all_tiles = groups * ((mean + 16 * na - 1) / (16 * na)) * Hkv, rounds = (all_tiles + 511) / 512;
-        const double full = rounds > 1 ? 512.0 * (double)rounds / (double)all_tiles : 1.0;
+        const double full = (double)wgs / (double)(wgs / (most + 1) * (most + 1));
         const double saved =
             wide * ((double)(B * plain_time) - (double)(groups * group_time) * full) * Hkv * (double)seen;
         // the requests' own keys as units of shares, where the plain form has no units
@@ -178,10 +192,6 @@ SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, 
     if (!p.use) return p;
     p.rows = (int)(rows < 16 * nb ? rows : 16 * nb);
     p.least = p.rows / 2 < 6 ? 6 : p.rows / 2;  // blocks of a share: see the split form; a unit and two blocks
-    // two workgroups a CU; every tile of a group needs one, and one is left
-    const int64_t most = T * G / (16 * na) + groups;
-    int64_t wgs = 512 / Hkv;
-    if (wgs < most + 1) wgs = most + 1;
     p.wgs = (int)wgs;
     const int64_t tiles_all = B * Hkv * tiles;
     int64_t z = 1024 / tiles_all;
