@@ -135,6 +135,17 @@ def test_one_long_prefix(D):
     check(problem([(20000, [(i + 1, 1) for i in range(30)])], [], 16, 2, D, 64, DT["bf16"], seed=1))
 
 
+@pytest.mark.parametrize("G,D,dtype", [(1, 64, "bf16"), (20, 64, "f16"), (7, 128, "bf16"), (2, 256, "f16")])
+def test_long_own_keys_behind_short_prefixes(G, D, dtype):
+    # segments end long before the requests' own keys do, whose rest their
+    # workgroups take; a second call gives the same bits
+    groups = [(96, [(700 + 37 * i, 1) for i in range(20)]), (64, [(1100, 1)] * 20), (128, [(1500 - 60 * i, 1) for i in range(20)])]
+    p = problem(groups, [(900, 1), (3, 1)], 16 * G, 16, D, 32, DT[dtype], seed=90 + D + G, first=1, room=900)
+    out, lse = check(p)
+    again, lse_again = run(p, 1)
+    assert torch.equal(out, again) and torch.equal(lse, lse_again)
+
+
 def test_many_groups():
     # more requests than a workgroup has threads
     r = random.Random(4)
