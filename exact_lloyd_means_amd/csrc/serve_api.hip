@@ -254,6 +254,8 @@ fk_status fk_rope(const fk_rope_args* p, int32_t n, const fk_rope_rows* rows, vo
             return fail(FK_EINVAL, "strides must be >= 0");
         if (r.x == r.y && (r.x_token != r.y_token || r.x_head != r.y_head))
             return fail(FK_EINVAL, "rows rotated in place must have the same strides");
+        if ((r.heads > 1 && r.y_head < p->head_dim) || (p->T > 1 && r.y_token < p->head_dim))
+            return fail(FK_EINVAL, "rows of y overlap: their strides must be at least head_dim");
         if (r.reserved) return fail(FK_EINVAL, "reserved must be 0");
         a.set[i] = {r.x, r.y, r.x_token, r.x_head, r.y_token, r.y_head};
         a.heads[i] = r.heads;

@@ -19,7 +19,8 @@ extern "C" {
 #endif
 
 /* Rows of heads: element (t, h, i) of x is at x[t * x_token + h * x_head + i],
- * of y likewise; strides in elements, >= 0. */
+ * of y likewise; strides in elements, >= 0.  Rows of x may overlap (a head that
+ * is broadcast), those of y may not: a stride below head_dim is refused. */
 typedef struct fk_rope_rows {
     const void* x;
     void* y;               /* may be x with the same strides; else no overlap */

@@ -34,7 +34,8 @@ def row(x=FAKE, y=FAKE, xt=1024, xh=128, yt=1024, yh=128, heads=8, reserved=0):
     (dict(rows=[dict(y=None)]), EINVAL), (dict(rows=[dict(x=ODD)]), EINVAL), (dict(dtype=fk.FK_F32, rows=[dict(x=FAKE + 2)]), EINVAL),
     (dict(rows=[dict(heads=0)]), EINVAL), (dict(rows=[dict(heads=65537)]), EUNSUPPORTED), (dict(rows=[dict(xt=-1)]), EINVAL),
     (dict(rows=[dict(yh=-1)]), EINVAL), (dict(rows=[dict(yt=2048)]), EINVAL), (dict(rows=[dict(reserved=1)]), EINVAL),
-    (dict(n=2, rows=[{}, dict(heads=-1)]), EINVAL)])
+    (dict(n=2, rows=[{}, dict(heads=-1)]), EINVAL), (dict(rows=[dict(xh=0, yh=0)]), EINVAL), (dict(rows=[dict(yh=127, xh=127)]), EINVAL),
+    (dict(rows=[dict(xt=0, yt=0)]), EINVAL), (dict(n=2, rows=[{}, dict(y=FAKE * 2, yh=0)]), EINVAL)])
 def test_rope_arguments(kw, status):
     assert rope(**kw) == status
     assert fk.lib.fk_last_error()
