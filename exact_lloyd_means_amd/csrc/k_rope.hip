@@ -131,7 +131,8 @@ hipError_t launch_dt(RopeArgs a, bool inter, hipStream_t s) {
     a.turn_units = a.R / 2 / pairs;
     a.units = a.turn_units + (a.D - a.R) / (vec ? N : 1);
     const int heads = a.heads[0] + a.heads[1];
-    const int x = a.units < 256 ? a.units : 256;
+    // a launch has less than 2^32 threads in a dimension, and up to 2^24 tokens
+    const int most = a.T > 1 << 23 ? 128 : 256, x = a.units < most ? a.units : most;
     int y = 256 / x < heads ? 256 / x : heads;
     // Heads walked by a thread share its sines; few tokens have them spread
     // over more workgroups instead, until about eight waves a SIMD are there.

@@ -142,3 +142,16 @@ def test_captured():
         fk.fk_rope(x, None, pos, turns, want)
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+def test_most_tokens_of_wide_rows():
+    # 2^24 tokens of rows that take a workgroup each
+    T, D, R = 1 << 24, 516, 514
+    x = torch.zeros(T, 1, D, dtype=torch.bfloat16, device="cuda")
+    at = [0, 1, (1 << 23) - 1, 1 << 23, T - 2, T - 1]
+    rows = torch.randn(len(at), 1, D, generator=torch.Generator().manual_seed(3)).bfloat16()
+    x[at] = rows.cuda()
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    fk.fk_rope(x, None, pos, fk.rope_turns(R))
+    check(x[at], rows, at, ref.frequencies(R), False, False, 1.0)
+    assert not bool(x[5:100].any()) and not bool(x[-100:-2].any())
