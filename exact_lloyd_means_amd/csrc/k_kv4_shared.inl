@@ -41,7 +41,7 @@ template <int NT>
 constexpr int kBlockTime = 3 + 5 * NT;
 template <int NT>
 constexpr int kOwnTime = NT < 2 ? 13 : kBlockTime<NT>;
-constexpr int kSegmentTime = 110, kShareTime = 80, kAgainTime = 60;  // a share behind a segment
+constexpr int kSegmentTime = 140, kShareTime = 80, kAgainTime = 60;  // a share behind a segment
 constexpr int kUnitBlocks = kSharedUnit;
 
 // Row tiles of requests.
