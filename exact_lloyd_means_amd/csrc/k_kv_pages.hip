@@ -21,7 +21,7 @@ constexpr int kNone = 0x7fffffff;
 // Sums are of integers and the order is that of the pairs, so timing shows
 // nowhere.  Bound by the chain of dependent reads of the five steps; they are
 // one launch where one workgroup will do (4 rows of 16 pages: 8.6 us), else five
-// (240 rows of 62-125 pages: 3.6 to 6.0 us each).
+// (240 rows of 62-125 pages: 3.4 to 5.6 us each).
 //
 // Entries that a row holds and takes again at the same place (those before its
 // new end when it is its own source, pages that it shares with its source) give
@@ -290,7 +290,7 @@ hipError_t fork_steps(const ForkArgs& a, hipStream_t s) {
 //
 // Places are ranks: the k-th page to move goes to the k-th free one, and both are
 // counted in a bitmap of the free pages, so that any thread finds any page's new
-// number by itself.  4096 pages, 64 rows: 4.6 + 4.8 us, launches and dependent
+// number by itself.  4096 pages, 64 rows: 4.6 + 4.4 us, launches and dependent
 // reads.
 
 constexpr int kMarkThreads = 1024;
@@ -406,7 +406,7 @@ __global__ __launch_bounds__(256) void k_compact_apply(CompactArgs a) {
 
 constexpr int kCopyThreads = 256, kCopyUnits = 1024;
 
-// Bound by memory: 1024 pages of 66 KB 31.6 us, 4.3 TB/s read and written (a large
+// Bound by memory: 1024 pages of 66 KB 32 us, 4.3 TB/s read and written (a large
 // copy: 4.7).
 //
 // Grid (entries, 16-byte units of codes in pieces of 1024).

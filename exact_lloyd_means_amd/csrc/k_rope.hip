@@ -10,8 +10,8 @@
 // Bound by memory: read and written once.  A thread keeps the sines of its
 // pairs and walks the heads; threads of a row lie side by side and rows of
 // neighbouring heads behind them, so that a wave reads 2 KB in one piece.  16384
-// tokens x 40 heads of 128 bf16: 70.7 us, 4.75 TB/s, what a copy reaches; 64
-// tokens: 3.8 us, a launch and two dependent reads.
+// tokens x 40 heads of 128 bf16: 71 us, 4.7 TB/s, what a copy reaches; 64
+// tokens: 3.6 us, a launch and two dependent reads.
 #include "serve_internal.h"
 
 namespace fk {

@@ -9,9 +9,9 @@
 // largest values of all rows), k_verify_pick finds the piece that holds the
 // point and searches that piece alone.  Bound by memory for many requests: one
 // row of the target and one of the draft a request are read once (64 requests of
-// 128000 tokens in fp32: 13.9 us, 4.7 TB/s), then by the chain sums, piece, token
-// (5.6 us; 8.9 with pieces of a workgroup, and each request's drafts looked at
-// again); for few by two launches of that chain (4.2 + 4.0 us).
+// 128000 tokens in fp32: 13.8 us, 4.7 TB/s), then by the chain sums, piece, token
+// (5.7 us; 8.9 with pieces of a workgroup, whose search reads four times as
+// much); for few by two launches of that chain (4.1 + 4.0 us).
 #include "serve_internal.h"
 
 namespace fk {
