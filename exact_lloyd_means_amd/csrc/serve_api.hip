@@ -158,8 +158,8 @@ SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, 
     // starting again (15 us) costs more.
     const int64_t most = T * G / (16 * na) + groups, round = 512 / Hkv < 1 ? 1 : 512 / Hkv;
     int64_t seen = max_blocks < 0 ? 1 << 22 : max_blocks;
-    if (max_blocks >= 0 && window > 0 && seen > (window + max_q) / kKvBlock + 2)
-        seen = (window + max_q) / kKvBlock + 2;
+    const int64_t behind = ((int64_t)window + max_q) / kKvBlock + 2;
+    if (max_blocks >= 0 && window > 0 && seen > behind) seen = behind;
     const double wide = D == 64 ? 0.6 : D == 128 ? 1.0 : 2.2;  // of a block's time
     int64_t rounds = most / round + 1;
     auto time = [&](int64_t r) {

@@ -109,6 +109,14 @@ def test_windows(window, causal):
     check(problem(groups, [(50, 1)], 8, 2, 128, 64, DT["bf16"], seed=window), causal=causal, window=window)
 
 
+def test_a_window_of_everything():
+    # the largest that there is leaves nothing out, and is shared like none
+    p = problem([(1024, [(1 + 17 * i, 1 + i % 3) for i in range(14)])], [(50, 1)], 16, 4, 128, 64, DT["f16"], seed=77)
+    out, lse = check(p, window=2 ** 31 - 1)
+    again, lse_again = run(p, 3)
+    assert torch.equal(out, again) and torch.equal(lse, lse_again)
+
+
 @pytest.mark.parametrize("window", [700, 1000, 1900])
 @pytest.mark.parametrize("causal", [True, False])
 def test_windows_of_many_heads(window, causal):
