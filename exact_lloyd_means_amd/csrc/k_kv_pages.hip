@@ -21,7 +21,7 @@ constexpr int kNone = 0x7fffffff;
 // Sums are of integers and the order is that of the pairs, so timing shows
 // nowhere.  Bound by the chain of dependent reads of the five steps; they are
 // one launch where one workgroup will do (4 rows of 16 pages: 8.6 us), else five
-// (240 rows of 62-125 pages: 3.4 to 5.6 us each).
+// (240 rows of 64-121 pages: 3.4 to 5.6 us each).
 //
 // Entries that a row holds and takes again at the same place (those before its
 // new end when it is its own source, pages that it shares with its source) give

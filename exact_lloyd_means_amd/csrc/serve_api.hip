@@ -177,7 +177,7 @@ SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, 
         // What sharing saves, in tenths of a microsecond of a wave, were all of the
         // table's room (or the window) the prefix, against the 8 us that finding
         // out who does what costs the walk, or 15 where the plain form is one launch.
-        // Of 400 mixes of groups of one to eight query tokens 59 are shared: 46 of
+        // Of 400 mixes of groups of one to seven query tokens 59 are shared: 46 of
         // them gain (at most 80 us, 120 -> 40) and 11 lose, 1 to 13 us but for one
         // whose prefixes have three blocks of the room's 72 (109 -> 147).
         const int64_t plain_cols = (rows + 15) / 16 < most_cols ? (rows + 15) / 16 : most_cols;
