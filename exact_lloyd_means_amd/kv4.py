@@ -384,9 +384,7 @@ class KV4Cache:
         within a page that another holds too."""
         with _on(stream, self.codes.device):
             rows = self._rows(rows)
-            if not isinstance(keep, torch.Tensor):                   # filled there: a copy would wait
-                keep = self.lens.new_full((rows.numel(),), max(0, keep or 0))
-            keep = keep.int().clamp(min=0).expand(rows.numel()).contiguous()
+            keep = self._keep(0 if keep is None else keep, rows.numel())
             # as many at a time as one call takes: a row's least length is what it comes to
             most = min(65536, (2 ** 31 - 1) // self.block_table.shape[1])
             parts = [self._fork(rows[i:i + most], None, keep[i:i + most]) for i in range(0, max(1, rows.numel()), most)]
@@ -407,9 +405,7 @@ class KV4Cache:
             sources = self._rows(sources)
             if sources.shape != rows.shape:
                 raise ValueError(f"rows and sources must have one length, got {rows.numel()} and {sources.numel()}")
-            if keep is None or not isinstance(keep, torch.Tensor):
-                keep = self.lens.new_full((rows.numel(),), 2 ** 31 - 1 if keep is None else min(max(0, keep), 2 ** 31 - 1))
-            return self._fork(rows, sources, keep.int().clamp(min=0).expand(rows.numel()).contiguous())
+            return self._fork(rows, sources, self._keep(2 ** 31 - 1 if keep is None else keep, rows.numel()))
 
     def _rows(self, rows) -> torch.Tensor:
         """Rows of the table as int32; R: none of them."""
@@ -420,6 +416,16 @@ class KV4Cache:
             return torch.where(rows, torch.arange(R, dtype=torch.int32, device=table.device), R)
         rows = torch.where(rows < 0, rows + R, rows)
         return torch.where((rows >= 0) & (rows < R), rows, R).int().flatten()
+
+    def _keep(self, keep, n: int) -> torch.Tensor:
+        """What is kept of each of n rows as int32: lengths beyond its range
+        are its ends, not what narrowing would make of them."""
+        most = 2 ** 31 - 1
+        if not isinstance(keep, torch.Tensor):                       # filled there: a copy would wait
+            return self.lens.new_full((n,), min(max(0, keep), most))
+        if keep.dtype is not torch.int32:
+            keep = keep.double()                                     # holds every int32, and the order of the others
+        return keep.clamp(0, most).int().expand(n).contiguous()
 
     def _fork(self, rows, sources, keep) -> torch.Tensor:
         from .serve import fk_kv4_copy, fk_kv_fork
