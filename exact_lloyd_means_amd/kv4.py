@@ -414,6 +414,8 @@ class KV4Cache:
         rows = torch.as_tensor(rows, device=table.device)
         if rows.dtype is torch.bool:
             return torch.where(rows, torch.arange(R, dtype=torch.int32, device=table.device), R)
+        if rows.dtype not in (torch.int32, torch.int64):             # fewer bits may not hold R
+            rows = rows.long()
         rows = torch.where(rows < 0, rows + R, rows)
         return torch.where((rows >= 0) & (rows < R), rows, R).int().flatten()
 
