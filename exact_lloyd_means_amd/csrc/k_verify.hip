@@ -89,8 +89,12 @@ __device__ inline Source<DT> source(const VerifyArgs& a, const Rows& r, int j) {
     const int64_t row = r.first + j;
     Source<DT> s{static_cast<const E*>(a.p) + row * a.p_row, nullptr, -1};
     if (j < r.n - 1) {
-        if (a.q) s.q = static_cast<const E*>(a.q) + row * a.q_row;
-        else s.without = a.tokens[row + 1];
+        // a draft that is no token was drawn from nothing: there is nothing to take away
+        const int d = a.tokens[row + 1];
+        if (d >= 0 && d < a.V) {
+            if (a.q) s.q = static_cast<const E*>(a.q) + row * a.q_row;
+            else s.without = d;
+        }
     }
     return s;
 }

@@ -152,7 +152,9 @@ def fk_verify(cu, tokens, target, accepted, emitted, draft=None, accept=None, pi
     request after its first being drafts; target (T, V) the probabilities of
     the token after each row, draft (T, V) those that the drafts were drawn
     from or None where they are certain; accept (T) and pick (B) fp32 uniform
-    numbers, or both None for greedy decoding (target may then be logits).
+    numbers, or both None for greedy decoding (target may then be logits).  A
+    draft that is no token (-1, say) stands for none: it is refused, and the
+    token is drawn from the target alone.
     Writes accepted (B), emitted (T: the drafts kept, a token more, then -1)
     and, unless None, keep (B): seq_lens without the drafts refused, as
     KV4Cache.release takes it."""

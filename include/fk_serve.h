@@ -98,7 +98,8 @@ size_t fk_verify_workspace_bytes(int64_t B, int64_t T, int64_t V);
  * 2^31), or -1 where the row has no positive value.
  * Greedy: a draft is kept where it is the first largest value of its row (NaN
  * counts as the least; logits will do), and that of the next row follows.
- * A request without rows gets accepted 0; drafts outside [0, V) are refused.
+ * A request without rows gets accepted 0.  A draft outside [0, V) is none: it is
+ * refused, and the token after it is drawn from p, with nothing taken away.
  * Entries of emitted that belong to no request are not written.
  */
 fk_status fk_verify(const fk_verify_args* a, void* ws, size_t ws_bytes, void* stream);
