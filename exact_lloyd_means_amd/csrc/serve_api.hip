@@ -39,6 +39,27 @@ fk_status check_dtype(int32_t dtype) {
     return FK_OK;
 }
 
+// ---- rotary positions --------------------------------------------------------------------
+
+// Whether two of T x H rows of D elements share one: rows (dt, dh) apart start
+// dt token - dh head elements apart.
+bool rows_overlap(int64_t T, int64_t token, int64_t H, int64_t head, int64_t D) {
+    if (H == 1) return T > 1 && token < D;
+    if (T == 1) return head < D;
+    if (token < D || head < D) return true;
+    typedef __int128 wide;
+    // rows of a token, or of a head, lie together: those of fused projections, of
+    // either order of the dimensions
+    if (token >= (wide)head * (H - 1) + D || head >= (wide)token * (T - 1) + D) return false;
+    // else every distance of heads against the nearest two of tokens
+    for (int64_t h = 1; h < H; ++h) {
+        const wide at = (wide)head * h, t = at / token;
+        if (t < T && at - t * token < D) return true;
+        if (t + 1 < T && (t + 1) * token - at < D) return true;
+    }
+    return false;
+}
+
 // ---- verification -----------------------------------------------------------------------
 
 fk_status check_verify_sizes(int64_t B, int64_t T, int64_t V) {
@@ -254,8 +275,11 @@ fk_status fk_rope(const fk_rope_args* p, int32_t n, const fk_rope_rows* rows, vo
             return fail(FK_EINVAL, "strides must be >= 0");
         if (r.x == r.y && (r.x_token != r.y_token || r.x_head != r.y_head))
             return fail(FK_EINVAL, "rows rotated in place must have the same strides");
-        if ((r.heads > 1 && r.y_head < p->head_dim) || (p->T > 1 && r.y_token < p->head_dim))
-            return fail(FK_EINVAL, "rows of y overlap: their strides must be at least head_dim");
+        if (rows_overlap(p->T, r.y_token, r.heads, r.y_head, p->head_dim))
+            return fail(FK_EINVAL, "rows of y overlap (strides %lld, %lld of %lld tokens, %d heads of %d)",
+                        (long long)r.y_token, (long long)r.y_head, (long long)p->T, (int)r.heads,
+                        (int)p->head_dim);
+        if (i && r.y == rows[0].y) return fail(FK_EINVAL, "both sets have the same rows of y");
         if (r.reserved) return fail(FK_EINVAL, "reserved must be 0");
         a.set[i] = {r.x, r.y, r.x_token, r.x_head, r.y_token, r.y_head};
         a.heads[i] = r.heads;

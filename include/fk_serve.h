@@ -20,7 +20,8 @@ extern "C" {
 
 /* Rows of heads: element (t, h, i) of x is at x[t * x_token + h * x_head + i],
  * of y likewise; strides in elements, >= 0.  Rows of x may overlap (a head that
- * is broadcast), those of y may not: a stride below head_dim is refused. */
+ * is broadcast), those of y may not: strides that make rows of a set share an
+ * element are refused, and so are two sets with one y. */
 typedef struct fk_rope_rows {
     const void* x;
     void* y;               /* may be x with the same strides; else no overlap */
