@@ -49,7 +49,7 @@ def test_strides_of_all_kinds():
     (1 << 24, 40 * D, 40, D, False), (1 << 24, D, 40, D << 24, False), (1 << 24, D, 40, (D << 24) - 1, True),
     (1 << 24, 65536 * D - 1, 65536, D, True),
     (1 << 24, 2 ** 62, 65536, 2 ** 63 - 1, True),      # four tokens are 2^64, two heads 2^64 - 2
-    (3, 2 ** 62, 65536, 2 ** 63 - 1, False), (3, 2 ** 63 - 1, 65536, 2 ** 63 - 1, True)])
+    (2, 2 ** 62, 65536, 2 ** 63 - 1, False), (3, 2 ** 63 - 1, 65536, 2 ** 63 - 1, True)])
 def test_the_largest(T, yt, H, yh, overlap):
     assert ("overlap" in refused((T, 2 * FAKE, yt, yh, H))) == overlap
 
