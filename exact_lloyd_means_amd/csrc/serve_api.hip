@@ -329,6 +329,8 @@ fk_status fk_verify(const fk_verify_args* p, void* ws, size_t ws_bytes, void* st
         FK_CHECK(need(p->seq_lens, "seq_lens", 4));
     }
     FK_CHECK(need_ws(ws, ws_bytes, fk_verify_workspace_bytes(p->B, p->T, p->V)));
+    // a request's drafts are read while tokens before them are written
+    if (p->emitted == p->tokens) return fail(FK_EINVAL, "emitted must not be tokens");
     VerifyArgs a{};
     a.B = p->B;
     a.T = p->T;

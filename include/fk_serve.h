@@ -78,7 +78,7 @@ typedef struct fk_verify_args {
                               them; or NULL */
     int32_t* accepted;     /* [B] drafts kept */
     int32_t* emitted;      /* [T] from cu[b] on: the drafts kept, one token
-                              more, then -1 */
+                              more, then -1; not tokens itself */
     int32_t* keep;         /* [B] seq - drafts not kept; or NULL */
 } fk_verify_args;
 
