@@ -390,6 +390,17 @@ int verify_pieces(int64_t rows, int64_t V, bool greedy) {
     return (int)(greedy ? c : c * kWaves);
 }
 
+int64_t verify_most_pieces(int64_t rows, int64_t V, bool greedy) {
+    // r rows have r ceil(1024 / r) <= r + 1023 pieces between the two limits, and a
+    // piece has eight elements or is the row
+    const int64_t most = (V + 1023) / 1024, least = (V + 8191) / 8192;
+    int64_t n = rows + 1023 < rows * most ? rows + 1023 : rows * most;
+    n = n < rows * least ? rows * least : n;
+    n = greedy ? n : n * kWaves;
+    const int64_t finest = rows * ((V + 7) / 8);
+    return n < finest ? n : finest;
+}
+
 hipError_t launch_verify(const VerifyArgs& a, int dtype, hipStream_t s) {
     return dtype == FK_F32   ? run<FK_F32>(a, s)
            : dtype == FK_F16 ? run<FK_F16>(a, s)

@@ -298,10 +298,8 @@ fk_status fk_rope(const fk_rope_args* p, int32_t n, const fk_rope_rows* rows, vo
 
 size_t fk_verify_workspace_bytes(int64_t B, int64_t T, int64_t V) {
     if (check_verify_sizes(B, T, V) != FK_OK) return 0;
-    int32_t by_request, by_row, len;
-    cut_rows(B, V, false, by_request, len);
-    cut_rows(T, V, true, by_row, len);
-    const size_t sampling = (size_t)B * by_request * 2, greedy = (size_t)T * by_row;
+    const size_t sampling = (size_t)verify_most_pieces(B, V, false) * 2;
+    const size_t greedy = (size_t)verify_most_pieces(T, V, true);
     return (sampling > greedy ? sampling : greedy) * sizeof(uint64_t) + (size_t)B * sizeof(int32_t);
 }
 

@@ -39,6 +39,8 @@ struct VerifyArgs {
 };
 // Pieces a row of V is cut into where `rows` of them are read.
 int verify_pieces(int64_t rows, int64_t V, bool greedy);
+// Pieces of all rows together, at most, of up to so many rows of up to V.
+int64_t verify_most_pieces(int64_t rows, int64_t V, bool greedy);
 hipError_t launch_verify(const VerifyArgs& a, int dtype, hipStream_t s);
 
 // ---- pages ------------------------------------------------------------------------

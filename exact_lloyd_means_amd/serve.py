@@ -139,7 +139,7 @@ def _distribution(t, name, dtype, shape, index):
 
 
 def verify_workspace(cu, target) -> torch.Tensor:
-    """A caller-owned workspace for fk_verify of these sizes."""
+    """A caller-owned workspace for fk_verify of these sizes and smaller ones."""
     T, V = _tensor(target, "target", 2)
     return torch.empty(_sized(lib.fk_verify_workspace_bytes(_tensor(cu, "cu", 1)[0] - 1, T, V)), dtype=torch.uint8,
                        device=target.device)

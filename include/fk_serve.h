@@ -82,7 +82,8 @@ typedef struct fk_verify_args {
     int32_t* keep;         /* [B] seq - drafts not kept; or NULL */
 } fk_verify_args;
 
-/* Bytes of workspace for fk_verify (0 when the sizes are invalid). */
+/* Bytes of workspace for fk_verify of up to so many requests, rows and tokens of
+ * the vocabulary (0 when the sizes are invalid). */
 size_t fk_verify_workspace_bytes(int64_t B, int64_t T, int64_t V);
 
 /*
