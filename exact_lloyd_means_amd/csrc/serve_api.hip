@@ -150,9 +150,30 @@ size_t compact_layout(int64_t pages, char* base, CompactArgs& a) {
 
 // ---- attention of shared prefixes ------------------------------------------------------
 
-// max_blocks < 0: the workspace of any block table and window.
+// Workgroups of a head that run at once, two a CU.
+int64_t shared_round(int Hkv) { return 512 / Hkv < 1 ? 1 : 512 / Hkv; }
+
+// Places of a plan's sums in the workspace.
+void shared_places(SharedPlan& p, int64_t B, int Hkv, int D) {
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t x = at;
+        at = align256(at + bytes);
+        return x;
+    };
+    const size_t units = (size_t)B * p.row_tiles, own = (size_t)Hkv * (units + 8 * (size_t)p.wgs) * p.rows;
+    const size_t parts = (size_t)Hkv * (size_t)p.wgs * 16 * p.group_cols;
+    p.head = take(16);
+    p.unit = take(units * 48);
+    p.part_o = take(parts * D * 4);
+    p.part_ml = take(parts * 8);
+    p.own_o = take(own * D * 4);
+    p.own_ml = take(own * 8);
+    p.total = at;
+}
+
 SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, int64_t groups,
-                       int64_t max_blocks, int window) {
+                       int64_t room, int window) {
     SharedPlan p{};
     const int64_t G = Hq / Hkv, rows = G * max_q;
     const int most_cols = tile_cols(D), nb = rows <= 16 || most_cols == 1 ? 1 : 2;
@@ -172,15 +193,14 @@ SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, 
         }
     }
     const int na = p.group_cols;
-    const int64_t room = max_blocks < 0 ? 0 : max_blocks;
     // Two workgroups a CU run at once; every tile of a group needs one, and one is
     // left.  A tile's segments are a workgroup's each, so tiles that leave much of
     // the card empty are better cut for two rounds, unless they are so short that
     // starting again (15 us) costs more.
-    const int64_t most = T * G / (16 * na) + groups, round = 512 / Hkv < 1 ? 1 : 512 / Hkv;
-    int64_t seen = max_blocks < 0 ? 1 << 22 : max_blocks;
+    const int64_t most = T * G / (16 * na) + groups, round = shared_round(Hkv);
+    int64_t seen = room;
     const int64_t behind = ((int64_t)window + max_q) / kKvBlock + 2;
-    if (max_blocks >= 0 && window > 0 && seen > behind) seen = behind;
+    if (window > 0 && seen > behind) seen = behind;
     const double wide = D == 64 ? 0.6 : D == 128 ? 1.0 : 2.2;  // of a block's time
     int64_t rounds = most / round + 1;
     auto time = [&](int64_t r) {
@@ -194,7 +214,7 @@ SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, 
     // enough rows for the plain form's waves over rows, which beat both
     const int64_t row_wg = 64 * row_cols(D);
     p.use = p.use && (rows <= 16 * most_cols || (T * G + row_wg - 1) / row_wg * Hkv < 512);
-    if (p.use && max_blocks >= 0) {
+    if (p.use) {
         // What sharing saves, in tenths of a microsecond of a wave, were all of the
         // table's room (or the window) the prefix, against the 8 us that finding
         // out who does what costs the walk, or 15 where the plain form is one launch.
@@ -221,22 +241,51 @@ SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, 
     const int each = (int)((p.rows + z - 1) / z), fit = 1024 / D;
     p.join_rows = 1;
     while (p.join_rows < each && p.join_rows < fit) p.join_rows *= 2;
-    size_t at = 0;
-    auto take = [&](size_t bytes) {
-        const size_t x = at;
-        at = align256(at + bytes);
-        return x;
-    };
-    const size_t units = (size_t)B * tiles, own = (size_t)Hkv * (units + 8 * (size_t)wgs) * p.rows;
-    const size_t parts = (size_t)Hkv * (size_t)wgs * 16 * na;
-    p.head = take(16);
-    p.unit = take(units * 48);
-    p.part_o = take(parts * D * 4);
-    p.part_ml = take(parts * 8);
-    p.own_o = take(own * D * 4);
-    p.own_ml = take(own * 8);
-    p.total = at;
+    shared_places(p, B, Hkv, D);
     return p;
+}
+
+// Most bytes that plan_shared takes on any table and window for up to B requests
+// and so many groups; and for up to T tokens and max_q where a request's rows fit
+// a tile, else for those.
+size_t shared_most(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, int64_t groups) {
+    const int64_t G = Hq / Hkv, rows = G * max_q;
+    const int most_cols = tile_cols(D);
+    groups = groups < kSharedGroups ? groups : kSharedGroups;
+    B = B < 8192 ? B : 8192;
+    size_t most = 0;
+    auto form = [&](int64_t tokens, int64_t rows, int nb, int na) {
+        const int64_t tiles = (rows + 16 * nb - 1) / (16 * nb), held = (1 << 27) / kSharedUnit / tiles;
+        if (tiles * Hkv > 65535 || held < 1) return;
+        SharedPlan p{};
+        p.row_tiles = (int)tiles;
+        p.rows = (int)(rows < 16 * nb ? rows : 16 * nb);
+        p.group_cols = na;
+        const int64_t n = tokens * G / (16 * na) + groups, round = shared_round(Hkv);
+        // fewer tiles never take more rounds, but those above a quarter may take two
+        const int64_t rounds = n < round && n > round / 4 ? 2 : n / round + 1;
+        p.wgs = (int)(rounds * round);
+        shared_places(p, B < held ? B : held, Hkv, D);
+        most = most > p.total ? most : p.total;
+    };
+    // Rows of a tile of one block: groups of a mean of up to 16 rows have tiles of
+    // one block (8 against 13 and 18 for two and three), and above 576 none has two
+    // (13 ceil(m / 32) >= 18 ceil(m / 48)).
+    auto blocks = [&](int64_t tokens, int64_t rows) {
+        for (int na = 1; na <= most_cols; ++na) {
+            const int64_t mean = na == most_cols ? T * G : na == 1 ? 16 : 576, fit = mean * groups / G;
+            form(na < most_cols && fit < tokens ? fit : tokens, rows, 1, na);
+        }
+    };
+    if (rows <= 16) {
+        blocks(T, rows);
+        return most;
+    }
+    const int64_t row_wg = 64 * row_cols(D);
+    if (rows <= 16 * most_cols || (T * G + row_wg - 1) / row_wg * Hkv < 512)
+        form(T, rows, most_cols == 1 ? 1 : 2, most_cols);
+    if (rows <= 16 * most_cols && G <= 16) blocks(T, 16 / G * G);
+    return most;
 }
 
 fk_status check_groups(int64_t groups, int64_t B) {
@@ -450,12 +499,16 @@ fk_status fk_kv4_copy(const fk_kv4_cache* c, int64_t n, const int32_t* copies, v
 
 size_t fk_kv4_attn_shared_workspace_bytes(const fk_kv4_cache* c, int64_t B, int64_t T,
                                           int32_t q_heads, int32_t max_q, int64_t groups) {
-    const size_t plain = fk_kv4_attn_workspace_bytes(c, B, T, q_heads, max_q);
+    size_t plain = fk_kv4_attn_workspace_bytes(c, B, T, q_heads, max_q);
     if (!plain || check_groups(groups, B) != FK_OK) return 0;
-    // as much as a call with any block table needs
-    const SharedPlan p = plan_shared(B, T, q_heads, c->kv_heads, c->head_dim,
-                                     (int)(T < max_q ? T : max_q), groups, -1, 0);
-    return p.total > plain ? p.total : plain;
+    const int G = q_heads / c->kv_heads, q = (int)(T < max_q ? T : max_q);
+    if (G <= 16 && G * q > 16 && G * q <= 16 * tile_cols(c->head_dim)) {
+        // rows that fit a block: twice the waves
+        const size_t few = fk_kv4_attn_workspace_bytes(c, B, T, q_heads, 16 / G);
+        plain = plain > few ? plain : few;
+    }
+    const size_t most = shared_most(B, T, q_heads, c->kv_heads, c->head_dim, q, groups);
+    return most > plain ? most : plain;
 }
 
 fk_status fk_kv4_attention_shared(const fk_kv4_cache* c, const fk_kv4_attn* p, int64_t groups,

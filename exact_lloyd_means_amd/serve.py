@@ -275,7 +275,9 @@ def fk_kv4_copy(copies, codes, scales, stream=None) -> None:
 # ---- attention of requests that share a prefix ------------------------------------------
 
 def kv4_attention_shared_workspace(q, seq_lens, prefix_lens, codes, max_q: int) -> torch.Tensor:
-    """A caller-owned workspace for fk_kv4_attention_shared of these sizes."""
+    """A caller-owned workspace for fk_kv4_attention_shared of these sizes, and of
+    fewer requests and groups; of fewer tokens too where max_q q_heads /
+    kv_heads is at most 48 (16 for 256 dimensions)."""
     T, Hq, D = _tensor(q, "q", 3)
     pages, H, _, blocks, _ = _tensor(codes, "codes", 5)
     c = _CACHE.pack(0, 0, 0, pages, 32 * blocks, H, D, DTYPES.get(q.dtype, -1))

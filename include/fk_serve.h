@@ -176,7 +176,10 @@ fk_status fk_kv_compact(const fk_kv_pool* p, int32_t* new_table, int32_t* new_sh
  */
 fk_status fk_kv4_copy(const fk_kv4_cache* c, int64_t n, const int32_t* copies, void* stream);
 
-/* Bytes of workspace for fk_kv4_attention_shared; 0 when invalid. */
+/* Bytes of workspace for fk_kv4_attention_shared on any block table and window, of
+ * up to B requests and so many groups; and of up to T tokens and max_q where
+ * max_q q_heads / kv_heads is at most 48 (16 for 256 dimensions), else of T tokens
+ * and this max_q.  0 when invalid. */
 size_t fk_kv4_attn_shared_workspace_bytes(const fk_kv4_cache* c, int64_t B, int64_t T,
                                           int32_t q_heads, int32_t max_q, int64_t groups);
 
