@@ -23,6 +23,12 @@ constexpr int kNone = 0x7fffffff;
 // one launch where one workgroup will do (4 rows of 16 pages: 8.6 us), else five
 // (240 rows of 64-121 pages: 3.4 to 5.6 us each).
 //
+// A wave finds the other pairs of its row, and what the pairs before it give up
+// and copy, by reading all pairs.  That is n^2 in all, so many pairs have three
+// launches more: names and least lengths by row (two), sums of the pairs before
+// (one workgroup).  Rows that return their last pages, us with them / without: 1024
+// 26 / 26, 2048 27 / 36, 16384 72 / 560, 65536 226 / 8440.
+//
 // Entries that a row holds and takes again at the same place (those before its
 // new end when it is its own source, pages that it shares with its source) give
 // and take the same page and are left out.
@@ -69,7 +75,11 @@ __device__ inline void fork_read(const ForkArgs& a, int i, int lane) {
     const int r = a.rows[i];
     int first = kNone, least = kNone;
     bool act = r >= 0 && r < a.R;
-    if (act) {
+    if (act && a.named) {
+        first = a.named[2 * (int64_t)r];
+        least = a.named[2 * (int64_t)r + 1];
+        act = first == i;
+    } else if (act) {
         for (int j = lane; j < a.n; j += 64)
             if (a.rows[j] == r) {
                 first = j < first ? j : first;
@@ -179,24 +189,28 @@ __device__ inline int list_len(const ForkArgs& a) {
     return n < 0 ? 0 : n > a.N ? (int)a.N : n;
 }
 
+// The list with the pages given up, and how many of it the copies take.
+__device__ inline void count_list(const ForkArgs& a, int gone, int copies) {
+    const int64_t have = (int64_t)list_len(a) + gone;
+    a.have[0] = (int)(have < a.N ? have : a.N);
+    a.have[1] = copies < a.have[0] ? copies : a.have[0];
+}
+
 __device__ inline void fork_give(const ForkArgs& a, int i, int lane) {
     const int* info = a.info + 8 * i;
     int upto, all;
-    if (i == 0) {
+    if (i == 0 && !a.upto) {
         int copies;
         before(a, kGone, 0, lane, upto, all);
         before(a, kCopy, 0, lane, upto, copies);
-        if (lane == 0) {
-            const int64_t have = (int64_t)list_len(a) + all;
-            a.have[0] = (int)(have < a.N ? have : a.N);
-            a.have[1] = copies < a.have[0] ? copies : a.have[0];
-        }
+        if (lane == 0) count_list(a, all, copies);
     }
     if (!info[kAct]) return;
     const int* row = a.table + info[kRow] * a.M;
     const int* fresh = a.fresh + i * a.M;
     if (info[kGone]) {
-        before(a, kGone, i, lane, upto, all);
+        if (a.upto) upto = a.upto[2 * i];
+        else before(a, kGone, i, lane, upto, all);
         int64_t at = (int64_t)list_len(a) + upto;
         for (int e0 = info[kFrom]; e0 < info[kHeld]; e0 += 64) {
             const int e = e0 + lane, p = e < info[kHeld] ? row[e] : -1;
@@ -226,7 +240,8 @@ __device__ inline void fork_take(const ForkArgs& a, int i, int lane) {
         int end = info[kEnd];
         if (info[kCopy]) {
             int upto, all;
-            before(a, kCopy, i, lane, upto, all);
+            if (a.upto) upto = a.upto[2 * i + 1];
+            else before(a, kCopy, i, lane, upto, all);
             if (upto < a.have[1]) {
                 end = to = a.free_pages[a.have[0] - a.have[1] + upto];
                 from = fresh[whole];
@@ -277,9 +292,57 @@ __global__ __launch_bounds__(kStepThreads) void k_fork_step(ForkArgs a) {
     if constexpr (STEP == 4) fork_take(a, i, lane);
 }
 
+// Threads: pairs.  The rows' names, cleared and then taken.
+template <bool CLEAR>
+__global__ __launch_bounds__(kStepThreads) void k_fork_name(ForkArgs a) {
+    const int i = blockIdx.x * kStepThreads + threadIdx.x, r = i < a.n ? a.rows[i] : -1;
+    if (r < 0 || r >= a.R) return;
+    int* named = a.named + 2 * (int64_t)r;
+    if constexpr (CLEAR) {
+        named[0] = named[1] = kNone;
+    } else {
+        atomicMin(&named[0], i);
+        atomicMin(&named[1], a.keep[i]);
+    }
+}
+
+// One workgroup, neighbouring pairs a thread.  Copies in the upper half of a sum,
+// pages in the lower: no page is given up twice, so neither passes 2^31.
+__global__ __launch_bounds__(kForkThreads) void k_fork_upto(ForkArgs a) {
+    constexpr int W = kForkThreads / 64;
+    __shared__ uint64_t part[W];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int per = (a.n + kForkThreads - 1) / kForkThreads, i0 = tid * per;
+    auto of = [&](int i) { return (uint64_t)(uint32_t)a.info[8 * i + kCopy] << 32 | (uint32_t)a.info[8 * i + kGone]; };
+    uint64_t mine = 0;
+    for (int i = i0; i < i0 + per && i < a.n; ++i) mine += of(i);
+    uint64_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const uint64_t y = __shfl_up((unsigned long long)x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 63) part[wave] = x;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) x += part[w];
+    if (tid == kForkThreads - 1) count_list(a, (int)(uint32_t)x, (int)(x >> 32));
+    x -= mine;
+    for (int i = i0; i < i0 + per && i < a.n; ++i) {
+        a.upto[2 * i] = (int)(uint32_t)x;
+        a.upto[2 * i + 1] = (int)(x >> 32);
+        x += of(i);
+    }
+}
+
 template <int STEP>
 hipError_t fork_steps(const ForkArgs& a, hipStream_t s) {
     constexpr int W = kStepThreads / 64;
+    const dim3 pairs((a.n + kStepThreads - 1) / kStepThreads);
+    if (STEP == 0 && a.named) {
+        k_fork_name<true><<<pairs, dim3(kStepThreads), 0, s>>>(a);
+        k_fork_name<false><<<pairs, dim3(kStepThreads), 0, s>>>(a);
+    }
+    if (STEP == 3 && a.upto) k_fork_upto<<<dim3(1), dim3(kForkThreads), 0, s>>>(a);
     k_fork_step<STEP><<<dim3((a.n + W - 1) / W), dim3(kStepThreads), 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if constexpr (STEP < 4) return e == hipSuccess ? fork_steps<STEP + 1>(a, s) : e;

@@ -131,6 +131,11 @@ size_t fork_layout(int64_t n, const fk_kv_pool* p, char* base, ForkArgs& a) {
     a.tail = reinterpret_cast<int32_t*>(take((size_t)p->pages * sizeof(int32_t)));
     a.next = reinterpret_cast<int32_t*>(take((size_t)p->pages * sizeof(int32_t)));
     a.first = reinterpret_cast<uint64_t*>(take((size_t)p->pages * sizeof(uint64_t)));
+    a.named = a.upto = nullptr;
+    if (n >= kForkMany) {
+        a.named = reinterpret_cast<int32_t*>(take((size_t)p->R * 2 * sizeof(int32_t)));
+        a.upto = reinterpret_cast<int32_t*>(take((size_t)n * 2 * sizeof(int32_t)));
+    }
     return at;
 }
 

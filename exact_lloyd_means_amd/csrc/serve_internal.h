@@ -55,7 +55,11 @@ struct ForkArgs {
     int32_t *count, *tail, *next;  // [N] change of the holders, first row that
                                    // goes on in the page, new shares
     uint64_t* first;               // [N] first entry that gives the page up
+    // of many pairs, else null:
+    int32_t* named;  // [R][2] first pair that names a row, least of its lengths
+    int32_t* upto;   // [n][2] pages given up and copies of the pairs before
 };
+constexpr int kForkMany = 1024;  // pairs from which on these are made
 hipError_t launch_kv_fork(const ForkArgs& a, hipStream_t s);
 
 struct CompactArgs {
