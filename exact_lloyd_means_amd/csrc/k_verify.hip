@@ -54,24 +54,26 @@ __device__ inline Rows rows_of(const VerifyArgs& a, int b) {
     return {c0, c1 - c0};
 }
 
-// Drafts kept of a request: its first row whose draft is refused, or the last.
-// `least` in LDS; all threads call it.
+// Drafts kept of a request, up to its first row whose draft is refused, or the
+// last; times two, and one more unless that draft is no token.  `least` in LDS;
+// all threads call it.
 template <int DT>
 __device__ inline int kept(const VerifyArgs& a, const Rows& r, int* least, int threads) {
     typedef typename Elem<DT>::type E;
-    if (threadIdx.x == 0) *least = r.n - 1;
+    if (threadIdx.x == 0) *least = 2 * (r.n - 1) + 1;
     __syncthreads();
     for (int i = threadIdx.x; i < r.n - 1; i += threads) {
-        if (i >= *(volatile int*)least) break;
+        if (i >= *(volatile int*)least / 2) break;
         const int64_t row = r.first + i;
         const int d = a.tokens[row + 1];
-        bool good = d >= 0 && d < a.V;
+        const bool token = d >= 0 && d < a.V;
+        bool good = token;
         if (good) {
             const float p = Elem<DT>::get(static_cast<const E*>(a.p)[row * a.p_row + d]);
             const float q = a.q ? Elem<DT>::get(static_cast<const E*>(a.q)[row * a.q_row + d]) : 1.f;
             good = (double)a.u[row] * (double)q < (double)p;  // 48 bits: exact
         }
-        if (!good) atomicMin(least, i);
+        if (!good) atomicMin(least, 2 * i + token);
     }
     __syncthreads();
     return *least;
@@ -84,17 +86,14 @@ struct Source {
     int without;                           // or this token is, alone; -1: none
 };
 template <int DT>
-__device__ inline Source<DT> source(const VerifyArgs& a, const Rows& r, int j) {
+__device__ inline Source<DT> source(const VerifyArgs& a, const Rows& r, int kept) {
     typedef typename Elem<DT>::type E;
-    const int64_t row = r.first + j;
+    const int64_t row = r.first + kept / 2;
     Source<DT> s{static_cast<const E*>(a.p) + row * a.p_row, nullptr, -1};
-    if (j < r.n - 1) {
-        // a draft that is no token was drawn from nothing: there is nothing to take away
-        const int d = a.tokens[row + 1];
-        if (d >= 0 && d < a.V) {
-            if (a.q) s.q = static_cast<const E*>(a.q) + row * a.q_row;
-            else s.without = d;
-        }
+    // a draft that is no token was drawn from nothing: there is nothing to take away
+    if (kept / 2 < r.n - 1 && kept % 2) {
+        if (a.q) s.q = static_cast<const E*>(a.q) + row * a.q_row;
+        else s.without = a.tokens[row + 1];
     }
     return s;
 }
@@ -271,7 +270,7 @@ __global__ __launch_bounds__(kThreads) void k_verify_pick(VerifyArgs a) {
         __syncthreads();
         token = found;
     }
-    tell(a, b, r, j, token, kThreads);
+    tell(a, b, r, j / 2, token, kThreads);
 }
 
 // ---- greedy ------------------------------------------------------------------------

@@ -35,7 +35,7 @@ struct VerifyArgs {
     int32_t *accepted, *emitted, *keep;
     int32_t pieces, len;  // of a row; elements of one
     uint64_t* sums;       // sampling: [B][pieces][2]; greedy: [T][pieces]
-    int32_t* kept;        // sampling: [B] drafts kept
+    int32_t* kept;        // sampling: [B] 2 drafts kept, + 1 unless the next is no token
 };
 // Pieces a row of V is cut into where `rows` of them are read.
 int verify_pieces(int64_t rows, int64_t V, bool greedy);
