@@ -14,17 +14,19 @@
 //   k_kv4_shared_join  adds up the segments and shares of each request, in order
 //
 // 64 requests of 16-600 tokens behind 8192 shared ones, 32 / 8 heads of 128: 36.8 us
-// a call (as plain attention 82).  Of a workgroup's 30 us in the walk 6 pass until
-// it knows its work, 3.5 until its codes are there, 14 to 20 with the 10 or 11 blocks
-// of a wave, 3 with adding up its waves; the join takes 5.  Eight groups of sixteen
-// behind 1000-6000, 64 / 8 heads, 122 MB of codes: 66 us (85).  Memory alone would
-// take 26 of them and the vector instructions 24 (13 of the 36.8): two waves a SIMD,
-// as many as the registers leave, hide neither behind the other.
+// a call (as plain attention 82; the two launches take 40 when traced).  Of a
+// workgroup's 30 us in the walk 6 pass until it knows its work, 3.5 until its codes
+// are there, 14 to 20 with the 10 or 11 blocks of a wave, 3 with adding up its
+// waves; the join takes 5.  Eight groups of sixteen behind 1000-6000, 64 / 8 heads,
+// 122 MB of codes: 66 us (85).  Memory alone would take 26 of them and the vector
+// instructions 24 (13 of the 36.8): two waves a SIMD, as many as the registers
+// leave, hide neither behind the other.
 //
-// Tried: the plan as a launch of its own (44 us, now 41), pieces of the line of all
-// tiles instead of segments of each (a workgroup in two tiles pays both ends: 8 x 16
-// 63 -> 75), more workgroups than run at once (37 -> 50), 32 rows a wave of 256
-// dimensions at one wave a SIMD (82 -> 98 for 180 requests).
+// Tried: the plan as a launch of its own (44 us against 41, before later steps),
+// pieces of the line of all tiles instead of segments of each (a workgroup in two
+// tiles pays both ends: 8 x 16 63 -> 75), more workgroups than run at once (37 ->
+// 50), 32 rows a wave of 256 dimensions at one wave a SIMD (82 -> 98 for 180
+// requests).
 #pragma once
 
 #include "k_kv4_attn.inl"

@@ -11,7 +11,9 @@
 // pairs and walks the heads; threads of a row lie side by side and rows of
 // neighbouring heads behind them, so that a wave reads 2 KB in one piece.  16384
 // tokens x 40 heads of 128 bf16: 71 us, 4.7 TB/s, what a copy reaches; 64
-// tokens: 3.6 us, a launch and two dependent reads.
+// tokens: 3.6 us, a launch and two dependent reads.  5001 tokens x 9 heads of 64
+// fp32, half rotated: 8.0 us (memory alone 4.9), since eight heads are walked at
+// once and the ninth takes a round of its own.
 #include "serve_internal.h"
 
 namespace fk {

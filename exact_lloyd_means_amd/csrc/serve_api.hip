@@ -223,9 +223,12 @@ SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, 
         // What sharing saves, in tenths of a microsecond of a wave, were all of the
         // table's room (or the window) the prefix, against the 8 us that finding
         // out who does what costs the walk, or 15 where the plain form is one launch.
-        // Of 400 mixes of groups of one to seven query tokens 59 are shared: 46 of
-        // them gain (at most 80 us, 120 -> 40) and 11 lose, 1 to 13 us but for one
-        // whose prefixes have three blocks of the room's 72 (109 -> 147).
+        // That is right where prefixes fill much of the room: of 400 mixes of groups
+        // of one to seven query tokens, in tables cut to the longest request, 59 are
+        // shared, 47 of them gain (at most 82 us, 124 -> 41; 571 in all) and 11 lose
+        // (at most 36, 111 -> 147; 71 in all).  With room for 131072 tokens 261 of the
+        // same are shared, 81 gain (671 in all) and 165 lose (4 at the median, at most
+        // 72, 94 -> 166; 1009 in all): how long prefixes are is not known here.
         const int64_t plain_cols = (rows + 15) / 16 < most_cols ? (rows + 15) / 16 : most_cols;
         const int64_t plain_time = (rows + 16 * plain_cols - 1) / (16 * plain_cols) * (3 + 5 * plain_cols);
         const double full = (double)wgs / (double)(wgs / (most + 1) * (most + 1));
@@ -237,7 +240,9 @@ SharedPlan plan_shared(int64_t B, int64_t T, int Hq, int Hkv, int D, int max_q, 
     }
     if (!p.use) return p;
     p.rows = (int)(rows < 16 * nb ? rows : 16 * nb);
-    p.least = p.rows / 2 < 6 ? 6 : p.rows / 2;  // blocks of a share: see the split form; a unit and two blocks
+    // Least of a share: see the split form; and what a unit costs beside its blocks
+    // (two blocks more: 64 groups of 4 96 -> 93 us, 16 of 16 54 -> 55, others alike).
+    p.least = p.rows / 2 < kSharedUnit ? kSharedUnit : p.rows / 2;
     p.wgs = (int)wgs;
     const int64_t tiles_all = B * Hkv * tiles;
     int64_t z = 1024 / tiles_all;

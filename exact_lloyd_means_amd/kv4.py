@@ -358,7 +358,8 @@ class KV4Cache:
         head_dim) over their requests, the planned tokens among them.  shared:
         (cu_groups, prefix_lens), int32 on the GPU, where neighbouring rows have
         their first tokens in common (fk_kv4_attention_shared); they are read
-        once for all rows of a group."""
+        once for all rows of a group.  For prefixes that are long beside max_len
+        and the rows' own tokens: short ones are faster without."""
         with _on(stream, q.device):
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if not len(q):
@@ -463,7 +464,11 @@ class KV4Cache:
     def verify(self, tokens: torch.Tensor, target: torch.Tensor, draft: torch.Tensor | None = None,
                accept: torch.Tensor | None = None, pick: torch.Tensor | None = None, stream=None):
         """Keeps the planned tokens' drafts that the target keeps (fk_verify)
-        and takes the others back.  Returns (accepted, emitted)."""
+        and takes the others back.  Every planned token of a row behind its first
+        is a draft: a step that brings prompts is not verified with this, but with
+        fk_verify on the rows that drafted.  Where pages ran out (status), drafts
+        may be kept whose tokens are not in the cache: lens says how many are.
+        Returns (accepted, emitted)."""
         from .serve import fk_verify
         R, device = self.block_table.shape[0], self.codes.device
         with _on(stream, device):

@@ -67,8 +67,10 @@ def rope_turns(rot_dim: int, base: float = 10000.0, stretch: float = 1.0, traine
     long as the `trained` length, pairs that turn `slow` times or less over it
     advance stretch times slower, those that turn `fast` times or more as
     before, and those between by a mean of both, weighted by the turns; trained
-    0: all stretch times slower.  The usual factor beside it is 1 + 0.1
-    ln(stretch)."""
+    0: all stretch times slower.  That is interpolation "by parts" as published by
+    Peng et al. (YaRN, 2023), whose factor beside it is 1 + 0.1 ln(stretch);
+    positions that are all interpolated are trained = 0.  Other frequencies w
+    (radians a position) are round(w / 2 pi 2^64) modulo 2^64, as int64."""
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError("rot_dim must be even and at least 2")
     if not base > 0 or not stretch > 0 or not math.isfinite(base) or not math.isfinite(stretch):
@@ -291,7 +293,8 @@ def fk_kv4_attention_shared(q, cu_q, seq_lens, block_table, cu_groups, prefix_le
     """fk_kv4_attention where the requests cu_groups[g] .. cu_groups[g + 1] - 1
     (int32, ascending; others share nothing) have their first prefix_lens[g]
     tokens in common: those are read once for all of them, through the table's
-    row of the first."""
+    row of the first.  For prefixes that are long beside the requests' own tokens
+    and the table's room; short ones in a wide table are faster without."""
     c, H, D, dtype, index = _cache(codebook, codes, scales)
     T, Hq, _ = _tensor(q, "q", 3)
     rows = torch.Size((T, Hq, D))

@@ -191,7 +191,10 @@ size_t fk_kv4_attn_shared_workspace_bytes(const fk_kv4_cache* c, int64_t B, int6
  * table of the group's first request, once for the query rows of all of them.
  * Tokens behind the prefix's last whole block of 32 are read for each request.
  * out and lse are those of fk_kv4_attention up to the order of fp32 sums, and
- * its limits apply; groups <= B.
+ * its limits apply; groups <= B.  It pays for prefixes that are long beside the
+ * requests' own tokens and the table's room: who shares is decided before
+ * prefix_lens can be read, as if they filled max_pages, and short prefixes in a
+ * wide table may take two to three times as long as fk_kv4_attention.
  */
 fk_status fk_kv4_attention_shared(const fk_kv4_cache* c, const fk_kv4_attn* a, int64_t groups,
                                   const int32_t* cu_groups, const int32_t* prefix_lens, void* ws,
