@@ -545,8 +545,8 @@ def run(st):
                    factor=st["factor"])
         return {"q": st["qo"], "k": st["ko"]}
     if kind == "verify":
-        fk.fk_verify(st["cu"], st["tokens"], st["p"], st["accepted"], st["emitted"], draft=st["q"], accept=st["u"], pick=st["pick"],
-                     seq_lens=st["seq"], keep=st["keep"], ws=st["ws"])
+        fk.fk_verify(st["cu"], st["tokens"], st["p"], st["accepted"], st["emitted"], draft=None if c["greedy"] else st["q"], accept=st["u"],
+                     pick=st["pick"], seq_lens=st["seq"], keep=st["keep"], ws=st["ws"])
         return {k: st[k] for k in ("accepted", "emitted", "keep")}
     if kind == "fork":
         pool = (st["P"], st["table"], st["lens"], st["shares"], st["free"], st["count"])
